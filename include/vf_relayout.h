@@ -350,6 +350,133 @@ int vf_head_merge_fp8(const void *codes, const float *scales, const int64_t dst_
  * 0), or a negative vf_status.  Pure host function. */
 int64_t vf_scale_count(int op, int64_t T, int64_t H, int64_t D, int64_t P, int64_t C);
 
+/*
+ * Expert relayouts: the token rows of a mixture-of-experts layer, moved to
+ * expert-major rows and back.  The same move as the relayouts above (token-
+ * major rows to destination-major storage, written once, and back), with a
+ * destination that depends on the data: each of T tokens names K experts.
+ *
+ *   Slot i = t*K + k (0 <= k < K) is token t's k-th choice.  A slot whose
+ *   expert index lies outside [0, E) is dropped (padding tokens, capacity
+ *   limits, experts of another rank).
+ *   counts[e] = number of slots of expert e;
+ *   offsets[0] = 0, offsets[e+1] = offsets[e] + counts[e] rounded up to a
+ *   multiple of `align`: expert e's rows start at offsets[e], a multiple of
+ *   `align` (for products tiled over rows);
+ *   row_of[t][k] = the slot's row, offsets[e] + its rank among e's slots in
+ *   slot order (a stable sort), or -1 when it is dropped;
+ *   slot_of[row] = the slot of a row, or -1 where none goes.
+ * The packed side holds `rows` = vf_expert_rows() rows of M contiguous
+ * elements, enough for any routing (the counts are known on the device only).
+ * Gap rows (behind an expert's last row, before the next expert's first) are
+ * written as zeros; rows at and behind offsets[E] are left as they were.
+ * With experts numbered by destination rank, the rows of destination p of P
+ * are offsets[p*E/P] .. offsets[(p+1)*E/P]: a destination-major send buffer.
+ *
+ * Tokens are [T][M] views with any non-negative element strides (row, column);
+ * a view that is written must not overlap itself.  Element types: vf_type.
+ * Arithmetic is in float32, each output rounded once, to nearest even; sums
+ * run over k in order, so results do not depend on the launch.
+ * Rows named by row_of outside [0, rows) are treated as dropped, so no
+ * content of a plan makes a kernel read or write out of bounds; a plan that
+ * names a row twice gives unspecified rows.
+ *
+ * 8-bit checkpoints (vf_format, VF_TYPE_BF16 only): a row of M elements is cut
+ * into groups of `group` (32, 64, 128 or 256; the last group may be shorter)
+ * and each group is a head row of the lossy transport's format above, the
+ * non-finite cases included.  codes: one byte per element [n][M]; scales: one
+ * float per group [n][ceil(M / group)]; n = T (of tokens) or `rows` (of packed
+ * rows, where only rows that hold a slot are written).
+ *
+ * Ownership, streams, pointers and errors as above.  Every argument is
+ * checked on the host before anything is enqueued; a written range that
+ * overlaps another range of the call is VF_ERR_ALIAS.  Limits (VF_ERR_ARG):
+ * K >= 1, T*K at most 2^30, rows below 2^31, 1 <= E <= 4096, align >= 1.
+ */
+typedef enum vf_type {
+    VF_TYPE_BF16 = 0,
+    VF_TYPE_F16 = 1,
+    VF_TYPE_F32 = 2
+} vf_type;
+
+/* Rows of the packed side: T*K + min(E, T*K) * (align - 1), the most that any
+ * routing takes; or a negative vf_status.  Pure host function. */
+int64_t vf_expert_rows(int64_t T, int64_t K, int64_t E, int64_t align);
+
+/* Bytes of workspace of vf_expert_plan (0: none needed); or a negative
+ * vf_status.  The workspace holds nothing between calls.  Pure host function. */
+int64_t vf_expert_workspace(int64_t T, int64_t K, int64_t E);
+
+/*
+ * The plan of a routing.  experts: [T][K] view of expert indices, int32 or
+ * int64 (index_bytes 4 or 8), element strides expert_strides[2].
+ * Writes row_of [T][K], slot_of [vf_expert_rows()], counts [E] and offsets
+ * [E + 1], all int32 and contiguous.  With T = 0, counts and offsets are
+ * written as zeros and slot_of and row_of hold nothing.
+ * workspace: vf_expert_workspace() bytes, 4-byte aligned (may be NULL when 0);
+ * calls that may run at the same time need one each.
+ */
+int vf_expert_plan(const void *experts, int index_bytes, const int64_t expert_strides[2],
+                   int64_t T, int64_t K, int64_t E, int64_t align,
+                   int32_t *row_of, int32_t *slot_of, int32_t *counts, int32_t *offsets,
+                   void *workspace, vf_stream_t stream);
+
+/* Arguments of the calls below; each names the fields it uses, besides type,
+ * T, K, M, E, rows, align and row_of, which all use.  counts and offsets are
+ * read by the calls that write packed rows, when align > 1. */
+typedef struct vf_expert_desc {
+    int32_t type;               /* vf_type of tokens, packed and grad_packed */
+    int32_t format;             /* 0: no checkpoint; else the vf_format of codes */
+    int64_t T, K, M, E;
+    int64_t rows;               /* rows of packed, grad_packed (and of slot_of) */
+    int64_t align;
+    int64_t group;              /* with a format: elements per scale */
+    const int32_t *row_of;      /* [T][K] */
+    const int32_t *counts;      /* [E] */
+    const int32_t *offsets;     /* [E + 1] */
+    void *tokens;               /* [T][M] view */
+    int64_t token_strides[2];
+    void *packed;               /* [rows][M] */
+    const float *weights;       /* [T][K] view */
+    int64_t weight_strides[2];
+    void *codes;                /* with a format */
+    float *scales;
+    void *grad_packed;          /* [rows][M] */
+    float *grad_weights;        /* [T][K] contiguous */
+} vf_expert_desc;
+
+/*
+ * packed[row_of[t][k]] = tokens[t], bit for bit.  With a format, codes and
+ * scales also receive the checkpoint of tokens, in the same pass.
+ * Its gradient to the tokens is vf_expert_merge of the packed gradient with
+ * weights NULL.
+ */
+int vf_expert_pack(const vf_expert_desc *desc, vf_stream_t stream);
+
+/*
+ * The pack of a checkpoint of tokens: packed[row_of[t][k]] = bfloat16 values
+ * of codes and scales (a format is required); tokens is not used.
+ */
+int vf_expert_restore(const vf_expert_desc *desc, vf_stream_t stream);
+
+/*
+ * tokens[t] = sum over k of weights[t][k] * packed[row_of[t][k]], dropped
+ * slots left out (whatever their weight); all of tokens is written.  weights
+ * NULL: the plain sum.  With a format, codes and scales also receive the
+ * checkpoint of the packed rows, in the same pass.
+ */
+int vf_expert_merge(const vf_expert_desc *desc, vf_stream_t stream);
+
+/*
+ * The gradients of vf_expert_merge with weights: tokens holds the gradient of
+ * its output (read), and
+ *   grad_packed[row_of[t][k]] = weights[t][k] * tokens[t],
+ *   grad_weights[t][k] = sum over m of tokens[t][m] * packed[row_of[t][k]][m]
+ * (0 for a dropped slot).  With a format, the packed rows are the values of
+ * codes and scales, code times scale in float32, and packed is not used.
+ */
+int vf_expert_merge_backward(const vf_expert_desc *desc, vf_stream_t stream);
+
 /* Static, NUL-terminated description of a vf_status value. */
 const char *vf_status_string(int status);
 

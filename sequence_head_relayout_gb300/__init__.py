@@ -31,16 +31,26 @@ Opt-in lossy transport (same page, table "Upstream gap and disposition", row
 codes) plus one float32 scale per head row, in the exact ops' layout, and
 dequantise to bfloat16 on the receive side.  The format is stated in
 ``include/vf_relayout.h``.
+
+Expert relayouts (mixture-of-experts layers): :func:`expert_plan` sorts the
+routing slots by expert, :func:`expert_pack` moves token rows to expert-major
+rows, :func:`expert_merge` takes them back with the routing weights and
+:func:`expert_merge_backward` gives its gradients.  With 8-bit checkpoints for
+the backward pass: :func:`expert_pack_q`, :func:`expert_restore_q`,
+:func:`expert_merge_q` and :func:`expert_merge_backward_q`.
 """
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
 __all__ = ["qkv_pack", "qkv_pack3", "attn_split", "head_merge", "qkv_unpack", "packed_elems",
            "piece_table", "VFError", "lib", "OP_QKV_PACK", "OP_ATTN_SPLIT", "OP_HEAD_MERGE",
            "OP_QKV_UNPACK", "qkv_pack_q", "attn_split_q", "head_merge_q", "qkv_unpack_q",
-           "scale_count", "FORMATS"]
+           "scale_count", "FORMATS", "ExpertPlan", "expert_rows", "expert_plan", "expert_pack",
+           "expert_merge", "expert_merge_backward", "expert_pack_q", "expert_restore_q",
+           "expert_merge_q", "expert_merge_backward_q"]
 
 OP_QKV_PACK, OP_ATTN_SPLIT, OP_HEAD_MERGE, OP_QKV_UNPACK = 0, 1, 2, 3
 ORDERS = {"chunk_major": 0, "slot_major": 1}
@@ -61,6 +71,17 @@ class _Desc(ctypes.Structure):
                 ("T", _I64), ("H", _I64), ("D", _I64), ("P", _I64), ("C", _I64),
                 ("c_begin", _I64), ("c_count", _I64), ("packed", _P),
                 ("strided", _P * 3), ("strides", _I64 * 3)]
+
+
+class _ExpertDesc(ctypes.Structure):
+    """vf_expert_desc of the C ABI."""
+    _fields_ = [("type", ctypes.c_int32), ("format", ctypes.c_int32),
+                ("T", _I64), ("K", _I64), ("M", _I64), ("E", _I64), ("rows", _I64),
+                ("align", _I64), ("group", _I64),
+                ("row_of", _P), ("counts", _P), ("offsets", _P),
+                ("tokens", _P), ("token_strides", _I64 * 2), ("packed", _P),
+                ("weights", _P), ("weight_strides", _I64 * 2), ("codes", _P), ("scales", _P),
+                ("grad_packed", _P), ("grad_weights", _P)]
 
 
 class VFError(RuntimeError):
@@ -118,6 +139,17 @@ def lib():
             f.restype = ctypes.c_int
         l.vf_scale_count.argtypes = [ctypes.c_int, _I64, _I64, _I64, _I64, _I64]
         l.vf_scale_count.restype = _I64
+        l.vf_expert_rows.argtypes = [_I64] * 4
+        l.vf_expert_rows.restype = _I64
+        l.vf_expert_workspace.argtypes = [_I64] * 3
+        l.vf_expert_workspace.restype = _I64
+        l.vf_expert_plan.argtypes = [_P, ctypes.c_int, _I64P] + [_I64] * 4 + [_P] * 6
+        l.vf_expert_plan.restype = ctypes.c_int
+        for name in ("vf_expert_pack", "vf_expert_restore", "vf_expert_merge",
+                     "vf_expert_merge_backward"):
+            f = getattr(l, name)
+            f.argtypes = [ctypes.POINTER(_ExpertDesc), _P]
+            f.restype = ctypes.c_int
         l.vf_status_string.argtypes = [ctypes.c_int]
         l.vf_status_string.restype = ctypes.c_char_p
         _lib = l
@@ -500,3 +532,342 @@ def qkv_unpack_q(codes: torch.Tensor, scales: torch.Tensor, T: int, H: int, D: i
               [q.data_ptr(), k.data_ptr(), v.data_ptr()], q.stride(),
               _stream(stream, codes.device), f, scales.data_ptr())
     return outs
+
+
+# ---- expert relayouts ----------------------------------------------------------
+
+_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+class ExpertPlan(NamedTuple):
+    """A routing's rows, as :func:`expert_plan` writes them (all int32).
+
+    row_of  [T, K]   row of each slot (slot t*K + k), -1 when it is dropped;
+    slot_of [rows]   slot of each row, -1 where none goes;
+    counts  [E]      slots of each expert;
+    offsets [E + 1]  first row of each expert, a multiple of ``align``.
+    """
+    row_of: torch.Tensor
+    slot_of: torch.Tensor
+    counts: torch.Tensor
+    offsets: torch.Tensor
+    align: int = 1
+
+
+def _rows_type(t: torch.Tensor, what: str) -> int:
+    _gpu_addressable(t, what)
+    f = _TYPES.get(t.dtype)
+    if f is None:
+        raise ValueError("%s must hold bfloat16, float16 or float32 values" % what)
+    return f
+
+
+def _check_plan(plan, T=None):
+    """(T, K, rows, E) of a plan whose tensors have the types and shapes that
+    the kernels take; what they hold is checked by the kernels."""
+    row_of, slot_of, counts, offsets, align = plan
+    for t, name in ((row_of, "row_of"), (slot_of, "slot_of"), (counts, "counts"),
+                    (offsets, "offsets")):
+        _gpu_addressable(t, "plan." + name)
+        if t.dtype != torch.int32 or not t.is_contiguous():
+            raise ValueError("plan.%s must be a contiguous int32 tensor" % name)
+    if row_of.dim() != 2 or slot_of.dim() != 1 or counts.dim() != 1 or \
+            tuple(offsets.shape) != (counts.shape[0] + 1,):
+        raise ValueError("plan must hold row_of [T,K], slot_of [rows], counts [E] and "
+                         "offsets [E+1]")
+    if T is not None and row_of.shape[0] != T:
+        raise ValueError("plan is for %d tokens, not %d" % (row_of.shape[0], T))
+    return row_of.shape[0], row_of.shape[1], slot_of.shape[0], counts.shape[0]
+
+
+def _new(stream, like, shape, dtype):
+    """An output tensor beside ``like``, allocated on the stream that fills it
+    (so that its memory is not handed out while that stream still uses it)."""
+    if like.device.type != "cuda":
+        return torch.empty(shape, dtype=dtype, pin_memory=True)
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _rows_out(t, stream, like, shape, dtype, what):
+    """Check (or allocate) a contiguous [rows, M] tensor."""
+    if t is None:
+        return _new(stream, like, shape, dtype)
+    _gpu_addressable(t, what)
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s tensor of shape %s" % (what, dtype, shape))
+    return t
+
+
+def _tokens_out(t, stream, like, shape, dtype, what):
+    """Check (or allocate) a [T, M] view."""
+    if t is None:
+        return _new(stream, like, shape, dtype)
+    _gpu_addressable(t, what)
+    if t.dtype != dtype or tuple(t.shape) != shape:
+        raise ValueError("%s must be a %s view of shape %s" % (what, dtype, shape))
+    return t
+
+
+def _kept(codes, scales, stream, like, n, M, f, group):
+    """Check (or allocate) a checkpoint: codes [n, M], scales [n, groups]."""
+    if group not in (32, 64, 128, 256):
+        raise ValueError("group must be 32, 64, 128 or 256")
+    codes = _rows_out(codes, stream, like, (n, M), _code_dtype(f), "codes")
+    scales = _rows_out(scales, stream, like, (n, -(-M // group)), torch.float32, "scales")
+    return codes, scales
+
+
+def _expert_desc(typ, plan, dims, M):
+    T, K, rows, E = dims
+    d = _ExpertDesc(type=typ, T=T, K=K, M=M, E=E, rows=rows, align=plan.align)
+    d.row_of = plan.row_of.data_ptr()
+    d.counts = plan.counts.data_ptr()
+    d.offsets = plan.offsets.data_ptr()
+    return d
+
+
+def _set_tokens(d, t):
+    d.tokens = t.data_ptr()
+    d.token_strides[0], d.token_strides[1] = t.stride()
+
+
+def _set_weights(d, weights, T, K):
+    if weights is None:
+        return
+    _gpu_addressable(weights, "weights")
+    if weights.dtype != torch.float32 or tuple(weights.shape) != (T, K):
+        raise ValueError("weights must be a float32 view of shape [T,K]")
+    d.weights = weights.data_ptr()
+    d.weight_strides[0], d.weight_strides[1] = weights.stride()
+
+
+def _set_kept(d, codes, scales, f, group):
+    d.format, d.group = f, group
+    d.codes, d.scales = codes.data_ptr(), scales.data_ptr()
+
+
+def _expert_call(fn, d, stream, like):
+    rc = getattr(_lib or lib(), fn)(ctypes.byref(d), _stream(stream, like.device))
+    if rc != 0:
+        raise VFError(fn, rc)
+
+
+def _matrix(t, what):
+    if t.dim() != 2:
+        raise ValueError("%s must have two dimensions" % what)
+    return t.shape
+
+
+def expert_rows(T: int, K: int, E: int, align: int = 1) -> int:
+    """Rows of the expert-major side: T*K + min(E, T*K) * (align - 1), the most
+    that any routing of T tokens to K of E experts takes."""
+    n = lib().vf_expert_rows(T, K, E, align)
+    if n < 0:
+        raise VFError("vf_expert_rows", n)
+    return n
+
+
+def expert_plan(experts: torch.Tensor, E: int, align: int = 1, out: ExpertPlan = None,
+                stream: torch.cuda.Stream = None) -> ExpertPlan:
+    """Sort the slots of a [T,K] view of expert indices (int32 or int64) by
+    expert, stably; indices outside [0, E) are dropped.
+
+    Each expert's rows start at a multiple of ``align``.  ``out`` gives the
+    tensors of an earlier plan of the same sizes to be written again.
+    """
+    _gpu_addressable(experts, "experts")
+    if experts.dtype not in (torch.int32, torch.int64) or experts.dim() != 2:
+        raise ValueError("experts must be an int32 or int64 view of shape [T,K]")
+    T, K = experts.shape
+    rows = expert_rows(T, K, E, align)
+    if out is None:
+        out = ExpertPlan(*(_new(stream, experts, shape, torch.int32)
+                           for shape in ((T, K), (rows,), (E,), (E + 1,))), align)
+    elif _check_plan(out) != (T, K, rows, E) or out.align != align:
+        raise ValueError("out is a plan of other sizes")
+    n = lib().vf_expert_workspace(T, K, E)
+    if n < 0:
+        raise VFError("vf_expert_workspace", n)
+    work = _new(stream, experts, (n,), torch.uint8) if n else None
+    _call("vf_expert_plan", experts.data_ptr(), experts.element_size(), _strides(experts), T, K,
+          E, align, out.row_of.data_ptr(), out.slot_of.data_ptr(), out.counts.data_ptr(),
+          out.offsets.data_ptr(), None if work is None else work.data_ptr(),
+          _stream(stream, experts.device))
+    return out
+
+
+def expert_pack(x: torch.Tensor, plan: ExpertPlan, out: torch.Tensor = None,
+                stream: torch.cuda.Stream = None) -> torch.Tensor:
+    """Token rows of a [T,M] view to expert-major rows [rows,M], bit for bit:
+    ``out[plan.row_of[t,k]] = x[t]``.
+
+    Gap rows (``plan.align``) are written as zeros, rows behind the last expert
+    are left as they were.  The gradient of ``x`` is :func:`expert_merge` of the
+    gradient of the result.
+    """
+    typ = _rows_type(x, "x")
+    T, M = _matrix(x, "x")
+    dims = _check_plan(plan, T)
+    out = _rows_out(out, stream, x, (dims[2], M), x.dtype, "out")
+    d = _expert_desc(typ, plan, dims, M)
+    _set_tokens(d, x)
+    d.packed = out.data_ptr()
+    _expert_call("vf_expert_pack", d, stream, x)
+    return out
+
+
+def expert_merge(packed: torch.Tensor, plan: ExpertPlan, weights: torch.Tensor = None,
+                 out: torch.Tensor = None, stream: torch.cuda.Stream = None) -> torch.Tensor:
+    """Expert-major rows [rows,M] back to tokens [T,M]: the sum over k of
+    ``weights[t,k] * packed[plan.row_of[t,k]]`` (float32 weights; None: the
+    plain sum), dropped slots left out, summed in float32 and rounded once.
+
+    ``out`` may be any non-overlapping [T,M] view.  The gradient of ``packed``
+    without weights is :func:`expert_pack` of the gradient of the result; with
+    weights see :func:`expert_merge_backward`.
+    """
+    typ = _rows_type(packed, "packed")
+    rows, M = _matrix(packed, "packed")
+    dims = _check_plan(plan)
+    T, K = dims[:2]
+    _rows_out(packed, stream, packed, (dims[2], M), packed.dtype, "packed")
+    out = _tokens_out(out, stream, packed, (T, M), packed.dtype, "out")
+    d = _expert_desc(typ, plan, dims, M)
+    _set_tokens(d, out)
+    _set_weights(d, weights, T, K)
+    d.packed = packed.data_ptr()
+    _expert_call("vf_expert_merge", d, stream, packed)
+    return out
+
+
+def _backward(grad, plan, weights, grad_packed, grad_weights, stream):
+    """What the two backward passes share: (descriptor, gradients, dims)."""
+    typ = _rows_type(grad, "grad")
+    T, M = _matrix(grad, "grad")
+    dims = _check_plan(plan, T)
+    if weights is None:
+        raise ValueError("weights are required (without, the gradient is expert_pack)")
+    grad_packed = _rows_out(grad_packed, stream, grad, (dims[2], M), grad.dtype, "grad_packed")
+    grad_weights = _rows_out(grad_weights, stream, grad, (T, dims[1]), torch.float32,
+                             "grad_weights")
+    d = _expert_desc(typ, plan, dims, M)
+    _set_tokens(d, grad)
+    _set_weights(d, weights, T, dims[1])
+    d.grad_packed, d.grad_weights = grad_packed.data_ptr(), grad_weights.data_ptr()
+    return d, grad_packed, grad_weights, dims
+
+
+def expert_merge_backward(grad: torch.Tensor, packed: torch.Tensor, plan: ExpertPlan,
+                          weights: torch.Tensor, grad_packed: torch.Tensor = None,
+                          grad_weights: torch.Tensor = None,
+                          stream: torch.cuda.Stream = None):
+    """Gradients of :func:`expert_merge` with weights, given the gradient
+    ``grad`` [T,M] of its result: (grad_packed [rows,M], grad_weights [T,K]).
+
+    ``grad_packed[row_of[t,k]] = weights[t,k] * grad[t]`` (gap rows zero, rows
+    behind the last expert left as they were); ``grad_weights[t,k]`` is the dot
+    product of ``grad[t]`` and the slot's row, 0 for a dropped slot.
+    """
+    d, grad_packed, grad_weights, dims = _backward(grad, plan, weights, grad_packed,
+                                                   grad_weights, stream)
+    _rows_out(packed, stream, grad, (dims[2], grad.shape[1]), grad.dtype, "packed")
+    d.packed = packed.data_ptr()
+    _expert_call("vf_expert_merge_backward", d, stream, grad)
+    return grad_packed, grad_weights
+
+
+def _bf16_matrix(t, what):
+    if isinstance(t, torch.Tensor) and t.dtype != torch.bfloat16:
+        raise ValueError("%s must hold bfloat16 values" % what)
+    _gpu_addressable(t, what)
+    return _matrix(t, what)
+
+
+def expert_pack_q(x: torch.Tensor, plan: ExpertPlan, fmt="e4m3", group: int = 128,
+                  out: torch.Tensor = None, codes: torch.Tensor = None,
+                  scales: torch.Tensor = None, stream: torch.cuda.Stream = None):
+    """:func:`expert_pack` of bfloat16 tokens that also keeps them in 8 bits for
+    the backward pass -> (packed, codes [T,M], scales [T, ceil(M/group)]).
+
+    The packed rows are exact; the checkpoint takes 1/(2K) of their memory, and
+    :func:`expert_restore_q` packs it again when the backward pass needs the
+    rows.  Each ``group`` consecutive elements share a scale, in the format of
+    the lossy transport.
+    """
+    T, M = _bf16_matrix(x, "x")
+    f = _fmt(fmt)
+    dims = _check_plan(plan, T)
+    codes, scales = _kept(codes, scales, stream, x, T, M, f, group)
+    out = _rows_out(out, stream, x, (dims[2], M), x.dtype, "out")
+    d = _expert_desc(0, plan, dims, M)
+    _set_tokens(d, x)
+    _set_kept(d, codes, scales, f, group)
+    d.packed = out.data_ptr()
+    _expert_call("vf_expert_pack", d, stream, x)
+    return out, codes, scales
+
+
+def expert_restore_q(codes: torch.Tensor, scales: torch.Tensor, plan: ExpertPlan, fmt="e4m3",
+                     group: int = 128, out: torch.Tensor = None,
+                     stream: torch.cuda.Stream = None) -> torch.Tensor:
+    """Expert-major bfloat16 rows [rows,M] of a checkpoint that
+    :func:`expert_pack_q` kept (gap rows and the rows behind as there)."""
+    f = _fmt(fmt)
+    _gpu_addressable(codes, "codes")
+    T, M = _matrix(codes, "codes")
+    dims = _check_plan(plan, T)
+    if scales is None:
+        raise ValueError("scales are required")
+    _kept(codes, scales, stream, codes, T, M, f, group)
+    out = _rows_out(out, stream, codes, (dims[2], M), torch.bfloat16, "out")
+    d = _expert_desc(0, plan, dims, M)
+    _set_kept(d, codes, scales, f, group)
+    d.packed = out.data_ptr()
+    _expert_call("vf_expert_restore", d, stream, codes)
+    return out
+
+
+def expert_merge_q(packed: torch.Tensor, plan: ExpertPlan, weights: torch.Tensor = None,
+                   fmt="e4m3", group: int = 128, out: torch.Tensor = None,
+                   codes: torch.Tensor = None, scales: torch.Tensor = None,
+                   stream: torch.cuda.Stream = None):
+    """:func:`expert_merge` of bfloat16 rows that also keeps the rows in 8 bits
+    for :func:`expert_merge_backward_q` -> (merged [T,M], codes [rows,M],
+    scales [rows, ceil(M/group)]).  Rows that no slot owns are not written."""
+    rows, M = _bf16_matrix(packed, "packed")
+    f = _fmt(fmt)
+    dims = _check_plan(plan)
+    T, K = dims[:2]
+    _rows_out(packed, stream, packed, (dims[2], M), packed.dtype, "packed")
+    codes, scales = _kept(codes, scales, stream, packed, rows, M, f, group)
+    out = _tokens_out(out, stream, packed, (T, M), packed.dtype, "out")
+    d = _expert_desc(0, plan, dims, M)
+    _set_tokens(d, out)
+    _set_weights(d, weights, T, K)
+    _set_kept(d, codes, scales, f, group)
+    d.packed = packed.data_ptr()
+    _expert_call("vf_expert_merge", d, stream, packed)
+    return out, codes, scales
+
+
+def expert_merge_backward_q(grad: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
+                            plan: ExpertPlan, weights: torch.Tensor, fmt="e4m3",
+                            group: int = 128, grad_packed: torch.Tensor = None,
+                            grad_weights: torch.Tensor = None,
+                            stream: torch.cuda.Stream = None):
+    """:func:`expert_merge_backward` with the expert rows read from the
+    checkpoint that :func:`expert_merge_q` kept; only ``grad_weights`` depends
+    on it."""
+    _bf16_matrix(grad, "grad")
+    f = _fmt(fmt)
+    d, grad_packed, grad_weights, dims = _backward(grad, plan, weights, grad_packed,
+                                                   grad_weights, stream)
+    if codes is None or scales is None:
+        raise ValueError("codes and scales are required")
+    _kept(codes, scales, stream, grad, dims[2], grad.shape[1], f, group)
+    _set_kept(d, codes, scales, f, group)
+    _expert_call("vf_expert_merge_backward", d, stream, grad)
+    return grad_packed, grad_weights

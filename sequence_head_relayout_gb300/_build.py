@@ -1,9 +1,9 @@
 """Build ``libvf_relayout.so`` in-tree with nvcc for sm_103a (GB300).
 
-Two translation units (the exact relayouts with the host checks, and the
-lossy-transport kernels) compiled in parallel, one ``-gencode``, then linked;
-the CUDA runtime is linked statically so the library needs nothing but the
-driver at load time.
+Three translation units (the exact relayouts, the lossy-transport kernels and
+the expert relayouts) compiled in parallel, one ``-gencode``, then linked; the
+CUDA runtime is linked statically so the library needs nothing but the driver
+at load time.
 """
 import os
 import subprocess
@@ -13,10 +13,11 @@ from concurrent.futures import ThreadPoolExecutor
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
-SOURCES = [os.path.join(CSRC, "vf_relayout.cu"), os.path.join(CSRC, "vf_quant.cu")]
+SOURCES = [os.path.join(CSRC, n) for n in ("vf_relayout.cu", "vf_quant.cu", "vf_expert.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, n) for n in ("relayout_kernel.cuh", "launch.cuh",
                                                   "tiled_kernel.cuh", "quant_kernel.cuh",
-                                                  "quant.h")] \
+                                                  "quant.h", "checks.h",
+                                                  "expert_kernel.cuh")] \
     + [os.path.join(ROOT, "include", "vf_relayout.h")]
 LIB = os.path.join(PKG, "libvf_relayout.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
