@@ -36,27 +36,46 @@ constexpr int kPlanThreads = 1024;
 constexpr int kGapBlocks = 4;            // blocks that zero one expert's gap rows
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 
-// Element types: storage S, exact widening to float32, one rounding back.
+// Element types: storage S; exact widening to float32 and one rounding back,
+// for the two elements of a 32-bit word (one for F32).
 struct Bf16 {
     using S = uint16_t;
-    static __device__ __forceinline__ float widen(S v) { return bf16_bits_to_float(v); }
-    static __device__ __forceinline__ S round(float f) {
-        return __bfloat16_as_ushort(__float2bfloat16_rn(f));
+    static __device__ __forceinline__ void widen(uint32_t w, float *f) {
+        f[0] = __uint_as_float(w << 16);
+        f[1] = __uint_as_float(w & 0xFFFF0000u);
+    }
+    static __device__ __forceinline__ uint32_t round(const float *f) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(f[0], f[1]);
+        return *reinterpret_cast<const uint32_t *>(&b);
     }
 };
 struct F16 {
     using S = uint16_t;
-    static __device__ __forceinline__ float widen(S v) {
-        return __half2float(__ushort_as_half(v));
+    static __device__ __forceinline__ void widen(uint32_t w, float *f) {
+        const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+        f[0] = v.x;
+        f[1] = v.y;
     }
-    static __device__ __forceinline__ S round(float f) {
-        return __half_as_ushort(__float2half_rn(f));
+    static __device__ __forceinline__ uint32_t round(const float *f) {
+        const __half2 h = __floats2half2_rn(f[0], f[1]);
+        return *reinterpret_cast<const uint32_t *>(&h);
     }
 };
 struct F32 {
     using S = uint32_t;
-    static __device__ __forceinline__ float widen(S v) { return __uint_as_float(v); }
-    static __device__ __forceinline__ S round(float f) { return __float_as_uint(f); }
+    static __device__ __forceinline__ void widen(uint32_t w, float *f) {
+        f[0] = __uint_as_float(w);
+    }
+    static __device__ __forceinline__ uint32_t round(const float *f) {
+        return __float_as_uint(f[0]);
+    }
+};
+
+// A lane's 8 columns of a span, as 32-bit words: unit u's elements at
+// [u * VW, u * VW + VW).
+template <class S> constexpr int kWords = 8 * int(sizeof(S)) / 4;
+template <class S> struct Lane8 {
+    uint32_t w[kWords<S>];
 };
 
 template <int BYTES> struct UnitBits;
@@ -94,44 +113,103 @@ struct ExpertArgs {
     float *scales;
     void *grad_packed;
     float *grad_weights;
-    int64_t T, M;
-    int32_t K, rows, E, group;
+    int64_t T;
+    int32_t M, K, rows, E;
+    int32_t group_log2;           // elements of a checkpoint's group
     int32_t spans;                // ceil(M / kSpan)
     int32_t groups;               // ceil(M / group)
+    int32_t step_tokens, step_spans;     // row_blocks * kExpertWarps items, as Walk counts
+    int32_t token_warps;          // merge backward: warps that share a token
     uint32_t row_blocks;          // blocks of the row part; the rest zero the gap rows
+};
+
+// The (token, span) items of the row blocks, one per warp at a time, spans
+// fastest: the block's warps share a token's routing and cover consecutive
+// columns.  The division is done once; a step adds to both numbers.
+struct Walk {
+    int64_t t;
+    int s;
+
+    __device__ __forceinline__ explicit Walk(const ExpertArgs &a) {
+        // row_blocks * kExpertWarps fits 32 bits
+        const uint32_t it = blockIdx.x * kExpertWarps + (threadIdx.x >> 5);
+        t = it / uint32_t(a.spans);
+        s = int(it - uint32_t(t) * uint32_t(a.spans));
+    }
+    __device__ __forceinline__ void step(const ExpertArgs &a) {
+        t += a.step_tokens;
+        s += a.step_spans;
+        if (s >= a.spans) {
+            s -= a.spans;
+            ++t;
+        }
+    }
 };
 
 // First column of unit u in a span.
 template <int VW>
 __device__ __forceinline__ int unit_col(int u, int lane) { return u * 32 * VW + lane * VW; }
 
-// The span's units of a row; units past the row's end are zeros.
+// The lane's units of a row's span; units past the row's end, and all of them
+// where `there` is false, are zeros.
 template <class S, int VW>
-__device__ __forceinline__ void load_span(const S *row, int64_t stride, int64_t col0, int64_t M,
-                                          int lane, S (&v)[8]) {
+__device__ __forceinline__ Lane8<S> load_span(const void *base, int64_t offset, int64_t stride,
+                                              int col0, int M, int lane,
+                                              bool there = true) {
+    const S *row = static_cast<const S *>(base) + offset;
+    Lane8<S> v = {};
 #pragma unroll
     for (int u = 0; u < 8 / VW; ++u) {
-        const int64_t c = col0 + unit_col<VW>(u, lane);
-#pragma unroll
-        for (int i = 0; i < VW; ++i) v[u * VW + i] = S(0);
-        if (c < M) load_unit<S, VW>(row + c * stride, v + u * VW);
+        const int c = col0 + unit_col<VW>(u, lane);
+        if (there && c < M)
+            load_unit<S, VW>(row + int64_t(c) * stride, reinterpret_cast<S *>(v.w) + u * VW);
     }
+    return v;
 }
 
 template <class S, int VW>
-__device__ __forceinline__ void store_span(S *row, int64_t stride, int64_t col0, int64_t M,
-                                           int lane, const S (&v)[8]) {
+__device__ __forceinline__ void store_span(void *base, int64_t offset, int64_t stride,
+                                           int col0, int M, int lane,
+                                           const Lane8<S> &v) {
+    S *row = static_cast<S *>(base) + offset;
 #pragma unroll
     for (int u = 0; u < 8 / VW; ++u) {
-        const int64_t c = col0 + unit_col<VW>(u, lane);
-        if (c < M) store_unit<S, VW>(row + c * stride, v + u * VW);
+        const int c = col0 + unit_col<VW>(u, lane);
+        if (c < M)
+            store_unit<S, VW>(row + int64_t(c) * stride, reinterpret_cast<const S *>(v.w) + u * VW);
     }
 }
 
-// Slot k's row of token t, or -1 (dropped, or a row that does not exist).
-__device__ __forceinline__ int slot_row(const ExpertArgs &a, int64_t t, int k) {
-    const int r = a.row_of[t * a.K + k];
+template <class E>
+__device__ __forceinline__ void widen_span(const Lane8<typename E::S> &v, float (&f)[8]) {
+    constexpr int N = 4 / int(sizeof(typename E::S));
+#pragma unroll
+    for (int i = 0; i < kWords<typename E::S>; ++i) E::widen(v.w[i], f + N * i);
+}
+
+template <class E>
+__device__ __forceinline__ Lane8<typename E::S> round_span(const float (&f)[8]) {
+    constexpr int N = 4 / int(sizeof(typename E::S));
+    Lane8<typename E::S> v;
+#pragma unroll
+    for (int i = 0; i < kWords<typename E::S>; ++i) v.w[i] = E::round(f + N * i);
+    return v;
+}
+
+// Rows of up to 32 slots of token t, k0 onward: lane j holds slot k0 + j's
+// row, -1 when it is dropped, past K, or names a row that does not exist.
+__device__ __forceinline__ int slot_rows(const ExpertArgs &a, int64_t t, int k0, int lane) {
+    const int r = k0 + lane < a.K ? a.row_of[t * a.K + k0 + lane] : -1;
     return r >= 0 && r < a.rows ? r : -1;
+}
+
+// Their weights; 0 where the row is -1, whatever the weight is.
+__device__ __forceinline__ float slot_weights(const ExpertArgs &a, int64_t t, int k0, int lane,
+                                              int row) {
+    if (row < 0) return 0.0f;
+    return a.weights == nullptr
+               ? 1.0f
+               : a.weights[t * a.weight_stride + (k0 + lane) * a.weight_col_stride];
 }
 
 // Zeros for the gap rows of every expert: block `b` of kGapBlocks * E.
@@ -140,9 +218,7 @@ __device__ __forceinline__ void zero_gaps(const ExpertArgs &a, void *packed, uin
     const int e = int(b / kGapBlocks);
     const int64_t first = int64_t(a.offsets[e]) + a.counts[e] + b % kGapBlocks;
     const int64_t end = min(int64_t(a.offsets[e + 1]), int64_t(a.rows));
-    S zero[VW];
-#pragma unroll
-    for (int i = 0; i < VW; ++i) zero[i] = S(0);
+    const S zero[VW] = {};
     for (int64_t r = max(first, int64_t(0)); r < end; r += kGapBlocks) {
         S *row = static_cast<S *>(packed) + r * a.M;
         for (int64_t c = int64_t(threadIdx.x) * VW; c < a.M; c += kExpertThreads * VW)
@@ -152,67 +228,142 @@ __device__ __forceinline__ void zero_gaps(const ExpertArgs &a, void *packed, uin
 
 // ---- 8-bit checkpoints of a span ----------------------------------------------
 
-// Quantises one span of a row (bfloat16 patterns v; zeros past the row's end)
-// group by group and stores its codes and scales.  All 32 lanes are here.  A
-// group lies within one span (group divides kSpan): within one unit of
-// consecutive lanes, or over consecutive units of all lanes.
+// fl(top / M) and fl(M / top) of the 128 bfloat16 mantissas M, in shared
+// memory (quant_kernel.cuh derives the format's inverse and scale from them
+// without a division per group).
+struct ScaleTable {
+    float inv[kMantissas], scale[kMantissas];
+};
+
+template <int FMT>
+__device__ __forceinline__ void fill_table(ScaleTable &tab) {
+    const float top = top_code<FMT>();
+    for (int i = int(threadIdx.x); i < kMantissas; i += kExpertThreads) {
+        const float M = 1.0f + float(i) * (1.0f / 128.0f);      // exact
+        tab.inv[i] = __fdiv_rn(top, M);
+        tab.scale[i] = __fdiv_rn(M, top);
+    }
+    __syncthreads();
+}
+
+// inv and scale of a group whose largest magnitude is the bfloat16 pattern m.
+__device__ __forceinline__ void group_scale(const ScaleTable &tab, uint32_t m, float *inv,
+                                            float *scale) {
+    const bool lost = non_finite_magnitude(m);
+    const bool live = !lost && m >= 0x0F80u;                    // amax >= 2^-96
+    const uint32_t k23 = uint32_t((int32_t(m >> 7) - 127) * (1 << 23));
+    const uint32_t i = m & 0x7Fu;
+    *inv = live ? __uint_as_float(__float_as_uint(tab.inv[i]) - k23) : 0.0f;
+    *scale = lost ? __uint_as_float(kLostScaleBits)
+             : live ? __uint_as_float(__float_as_uint(tab.scale[i]) + k23) : 0.0f;
+}
+
+// Quantises one span of a row (zeros past the row's end) group by group and
+// stores its codes and scales.  All 32 lanes are here.  A group lies within one
+// span (its size divides kSpan): within one unit, over consecutive lanes, or
+// over consecutive units of all lanes.
 template <int VW, int FMT>
-__device__ __forceinline__ void checkpoint_span(const ExpertArgs &a, int64_t row, int64_t col0,
-                                                int lane, const uint16_t (&v)[8]) {
+__device__ __forceinline__ void checkpoint_span(const ExpertArgs &a, const ScaleTable &tab,
+                                                int64_t row, int col0, int lane,
+                                                const Lane8<uint16_t> &v) {
     constexpr int U = 8 / VW;
-    const int lanes = min(32, a.group / VW);               // of a unit that share a group
-    const int units = max(1, a.group / (32 * VW));         // that share a group
+    const int lanes = min(32, (1 << a.group_log2) / VW);               // of a unit that share a group
+    const int units = max(1, (1 << a.group_log2) / (32 * VW));         // that share a group
+    const uint16_t *h = reinterpret_cast<const uint16_t *>(v.w);
     uint32_t m[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        m[u] = 0;
+        if constexpr (VW == 8) {
+            m[u] = max_u16x2(max_u16x2(mag2(v.w[0]), mag2(v.w[1])),
+                             max_u16x2(mag2(v.w[2]), mag2(v.w[3])));
+        } else {
+            m[u] = 0;
 #pragma unroll
-        for (int i = 0; i < VW; ++i) m[u] = max(m[u], uint32_t(v[u * VW + i]) & 0x7FFFu);
-        for (int o = lanes >> 1; o > 0; o >>= 1) m[u] = max(m[u], __shfl_xor_sync(kAll, m[u], o));
+            for (int i = 0; i < VW; ++i) m[u] = max(m[u], uint32_t(h[u * VW + i]) & 0x7FFFu);
+        }
+        for (int o = lanes >> 1; o > 0; o >>= 1)
+            m[u] = max_u16x2(m[u], __shfl_xor_sync(kAll, m[u], o));
+        m[u] = max(m[u] & 0xFFFFu, m[u] >> 16);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const int64_t c = col0 + unit_col<VW>(u, lane);
-        uint32_t top_mag = 0;
+        const int c = col0 + unit_col<VW>(u, lane);
+        uint32_t top_mag = m[u];
 #pragma unroll
         for (int w = 0; w < U; ++w)
             if (w / units == u / units) top_mag = max(top_mag, m[w]);
-        const float amax = bf16_bits_to_float(top_mag), top = top_code<FMT>();
-        const bool lost = non_finite_magnitude(top_mag);
-        const bool live = !lost && amax >= 0x1p-96f;
-        const float inv = live ? __fdiv_rn(top, amax) : 0.0f;
+        float inv, scale;
+        group_scale(tab, top_mag, &inv, &scale);
         if (c >= a.M) continue;
         if (lane % lanes == 0 && u % units == 0)
-            a.scales[row * a.groups + c / a.group] =
-                lost ? __uint_as_float(kLostScaleBits) : live ? __fdiv_rn(amax, top) : 0.0f;
-        uint16_t h[VW];
-        uint8_t code[VW];
+            a.scales[row * a.groups + (c >> a.group_log2)] = scale;
+        if constexpr (VW == 8) {
+            uint2 code = encode8<FMT>(make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]), inv);
+            // (a lost group's codes are 0 whatever its elements: inv is 0 and
+            // a NaN or an infinity times 0 would not be)
+            if (inv == 0.0f) code = make_uint2(0, 0);
+            *reinterpret_cast<uint2 *>(a.codes + row * a.M + c) = code;
+        } else {
+            uint16_t x[VW];
+            uint8_t code[VW];
 #pragma unroll
-        for (int i = 0; i < VW; ++i) h[i] = v[u * VW + i];
-        encode<VW, FMT>(h, inv, live, code);
-        store_unit<uint8_t, VW>(a.codes + row * a.M + c, code);
+            for (int i = 0; i < VW; ++i) x[i] = h[u * VW + i];
+            encode<VW, FMT>(x, inv, inv != 0.0f, code);
+            store_unit<uint8_t, VW>(a.codes + row * a.M + c, code);
+        }
     }
 }
 
-// The float32 values that a span of a checkpointed row stands for: code times
-// scale, NaN where the scale is not finite.
-template <int VW, int FMT>
-__device__ __forceinline__ void restore_span(const ExpertArgs &a, int64_t row, int64_t col0,
-                                             int lane, float (&f)[8]) {
+// The lane's codes of a span of a checkpointed row and the scales of its units
+// (NaN where a stored scale is not finite); zeros where there are none.
+template <int VW> struct KeptLane {
+    uint8_t code[8];
+    float scale[8 / VW];
+};
+
+template <int VW>
+__device__ __forceinline__ KeptLane<VW> load_kept(const ExpertArgs &a, int64_t row, int col0,
+                                                  int lane, bool there = true) {
+    KeptLane<VW> q = {};
 #pragma unroll
     for (int u = 0; u < 8 / VW; ++u) {
-        const int64_t c = col0 + unit_col<VW>(u, lane);
-#pragma unroll
-        for (int i = 0; i < VW; ++i) f[u * VW + i] = 0.0f;
-        if (c >= a.M) continue;
-        uint8_t code[VW];
-        load_unit<uint8_t, VW>(a.codes + row * a.M + c, code);
-        const float s = a.scales[row * a.groups + c / a.group];
-#pragma unroll
-        for (int i = 0; i < VW; ++i)
-            f[u * VW + i] = lost_scale(s) ? __uint_as_float(kLostScaleBits)
-                                          : __fmul_rn(code_value<FMT>(code[i]), s);
+        const int c = col0 + unit_col<VW>(u, lane);
+        if (there && c < a.M) {
+            load_unit<uint8_t, VW>(a.codes + row * a.M + c, q.code + u * VW);
+            q.scale[u] = a.scales[row * a.groups + (c >> a.group_log2)];
+        }
     }
+    return q;
+}
+
+// Code values of the lane's columns, as float32 (exact).
+template <int FMT>
+__device__ __forceinline__ void code_values(const uint8_t (&code)[8], float (&f)[8]) {
+    uint32_t w[2];
+    memcpy(w, code, 8);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if constexpr (FMT == kFmtInt8) {
+            const uint32_t u = w[h] ^ 0x80808080u;               // code + 128, per byte
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                f[4 * h + i] = __fsub_rn(
+                    __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7540u | i)), 8388736.0f);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(
+                    __nv_fp8x2_storage_t((w[h] >> (16 * i)) & 0xFFFFu), __NV_E4M3);
+                const float2 p = __half22float2(__half2(hr));    // exact: E4M3 fits in half
+                f[4 * h + 2 * i] = p.x;
+                f[4 * h + 2 * i + 1] = p.y;
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ float finite_or_nan(float s) {
+    return lost_scale(s) ? __uint_as_float(kLostScaleBits) : s;
 }
 
 // ---- row kernels ---------------------------------------------------------------
@@ -221,26 +372,27 @@ __device__ __forceinline__ void restore_span(const ExpertArgs &a, int64_t row, i
 template <class S, int VW, int FMT>
 __global__ void __launch_bounds__(kExpertThreads)
 expert_pack_rows(const __grid_constant__ ExpertArgs a) {
+    __shared__ ScaleTable tab;
+    if constexpr (FMT != 0) fill_table<FMT>(tab);
     wait_for_previous_grid();
     if (blockIdx.x >= a.row_blocks) {
         zero_gaps<S, VW>(a, a.packed, blockIdx.x - a.row_blocks);
         return;
     }
     const int lane = int(threadIdx.x & 31);
-    const int64_t items = a.T * a.spans;
-    for (int64_t it = int64_t(blockIdx.x) * kExpertWarps + (threadIdx.x >> 5); it < items;
-         it += int64_t(a.row_blocks) * kExpertWarps) {
-        const int64_t t = it / a.spans, col0 = (it - t * a.spans) * kSpan;
-        S v[8];
-        load_span<S, VW>(static_cast<const S *>(a.tokens) + t * a.token_stride, a.col_stride,
-                         col0, a.M, lane, v);
-        for (int k = 0; k < a.K; ++k) {
-            const int r = slot_row(a, t, k);
-            if (r >= 0)
-                store_span<S, VW>(static_cast<S *>(a.packed) + int64_t(r) * a.M, 1, col0, a.M,
-                                  lane, v);
+    for (Walk at(a); at.t < a.T; at.step(a)) {
+        const int64_t t = at.t;
+        const int col0 = at.s * kSpan;
+        const Lane8<S> v = load_span<S, VW>(a.tokens, t * a.token_stride, a.col_stride, col0,
+                                            a.M, lane);
+        for (int k0 = 0; k0 < a.K; k0 += 32) {
+            const int rows = slot_rows(a, t, k0, lane);
+            for (int j = 0; j < min(32, a.K - k0); ++j) {
+                const int r = __shfl_sync(kAll, rows, j);
+                if (r >= 0) store_span<S, VW>(a.packed, int64_t(r) * a.M, 1, col0, a.M, lane, v);
+            }
         }
-        if constexpr (FMT != 0) checkpoint_span<VW, FMT>(a, t, col0, lane, v);
+        if constexpr (FMT != 0) checkpoint_span<VW, FMT>(a, tab, t, col0, lane, v);
     }
 }
 
@@ -254,103 +406,178 @@ expert_restore_rows(const __grid_constant__ ExpertArgs a) {
         return;
     }
     const int lane = int(threadIdx.x & 31);
-    const int64_t items = a.T * a.spans;
-    for (int64_t it = int64_t(blockIdx.x) * kExpertWarps + (threadIdx.x >> 5); it < items;
-         it += int64_t(a.row_blocks) * kExpertWarps) {
-        const int64_t t = it / a.spans, col0 = (it - t * a.spans) * kSpan;
+    for (Walk at(a); at.t < a.T; at.step(a)) {
+        const int64_t t = at.t;
+        const int col0 = at.s * kSpan;
+        const KeptLane<VW> q = load_kept<VW>(a, t, col0, lane);
         float f[8];
-        restore_span<VW, FMT>(a, t, col0, lane, f);
-        uint16_t v[8];
+        code_values<FMT>(q.code, f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = __fmul_rn(f[i], q.scale[i / VW]);
+        Lane8<uint16_t> v = round_span<Bf16>(f);
+        // a lost group arrives as one NaN pattern
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            v[i] = isnan(f[i]) ? uint16_t(kLostValue2 & 0xFFFFu) : Bf16::round(f[i]);
-        for (int k = 0; k < a.K; ++k) {
-            const int r = slot_row(a, t, k);
-            if (r >= 0)
-                store_span<uint16_t, VW>(static_cast<uint16_t *>(a.packed) + int64_t(r) * a.M, 1,
-                                         col0, a.M, lane, v);
+            if (lost_scale(q.scale[i / VW]))
+                reinterpret_cast<uint16_t *>(v.w)[i] = uint16_t(kLostValue2 & 0xFFFFu);
+        for (int k0 = 0; k0 < a.K; k0 += 32) {
+            const int rows = slot_rows(a, t, k0, lane);
+            for (int j = 0; j < min(32, a.K - k0); ++j) {
+                const int r = __shfl_sync(kAll, rows, j);
+                if (r >= 0)
+                    store_span<uint16_t, VW>(a.packed, int64_t(r) * a.M, 1, col0, a.M, lane, v);
+            }
         }
     }
 }
 
 // Merge; FMT != 0 also keeps the packed rows' checkpoint (a row belongs to one
-// slot, so it is read once).  Walks (token, span).
-template <class E, int VW, int FMT>
+// slot, so it is read once).  Walks (token, span); KU rows' loads are in
+// flight at a time.
+template <class E, int VW, int FMT, int KU>
 __global__ void __launch_bounds__(kExpertThreads)
 expert_merge_rows(const __grid_constant__ ExpertArgs a) {
     using S = typename E::S;
+    __shared__ ScaleTable tab;
+    if constexpr (FMT != 0) fill_table<FMT>(tab);
     wait_for_previous_grid();
     const int lane = int(threadIdx.x & 31);
-    const int64_t items = a.T * a.spans;
-    for (int64_t it = int64_t(blockIdx.x) * kExpertWarps + (threadIdx.x >> 5); it < items;
-         it += int64_t(a.row_blocks) * kExpertWarps) {
-        const int64_t t = it / a.spans, col0 = (it - t * a.spans) * kSpan;
+    for (Walk at(a); at.t < a.T; at.step(a)) {
+        const int64_t t = at.t;
+        const int col0 = at.s * kSpan;
         float acc[8] = {};
-        for (int k = 0; k < a.K; ++k) {
-            const int r = slot_row(a, t, k);
-            if (r < 0) continue;
-            S v[8];
-            load_span<S, VW>(static_cast<const S *>(a.packed) + int64_t(r) * a.M, 1, col0, a.M,
-                             lane, v);
-            const float w = a.weights == nullptr
-                                ? 1.0f
-                                : a.weights[t * a.weight_stride + k * a.weight_col_stride];
+        for (int k0 = 0; k0 < a.K; k0 += KU) {
+            const int rows = slot_rows(a, t, k0, lane);
+            const float weights = slot_weights(a, t, k0, lane, rows);
+            Lane8<S> v[KU];
+            int r[KU];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) acc[i] = __fmaf_rn(w, E::widen(v[i]), acc[i]);
-            if constexpr (FMT != 0) checkpoint_span<VW, FMT>(a, r, col0, lane, v);
+            for (int j = 0; j < KU; ++j) {
+                r[j] = __shfl_sync(kAll, rows, j);
+                v[j] = load_span<S, VW>(a.packed, int64_t(r[j]) * a.M, 1, col0, a.M, lane,
+                                        r[j] >= 0);
+            }
+#pragma unroll
+            for (int j = 0; j < KU; ++j) {
+                const float w = __shfl_sync(kAll, weights, j);
+                float f[8];
+                widen_span<E>(v[j], f);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) acc[i] = __fmaf_rn(w, f[i], acc[i]);
+            }
+            if constexpr (FMT != 0) {
+#pragma unroll
+                for (int j = 0; j < KU; ++j)
+                    if (r[j] >= 0) checkpoint_span<VW, FMT>(a, tab, r[j], col0, lane, v[j]);
+            }
         }
-        S out[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) out[i] = E::round(acc[i]);
-        store_span<S, VW>(static_cast<S *>(a.tokens) + t * a.token_stride, a.col_stride, col0,
-                          a.M, lane, out);
+        store_span<S, VW>(a.tokens, t * a.token_stride, a.col_stride, col0, a.M, lane,
+                          round_span<E>(acc));
     }
 }
 
-// Gradients of the merge; FMT != 0: the packed rows come from a checkpoint.  A
-// warp walks the spans of a token, so each weight's gradient is one sum.
-template <class E, int VW, int FMT>
+// The sums of N values over the warp's lanes (N a power of two, at most 32):
+// lane l gets the sum of value l % N.  Each step halves the values a lane
+// holds, so it takes N - 1 + log2(32 / N) shuffles, not 5 N.
+template <int N>
+__device__ __forceinline__ float warp_sums(float (&v)[N], int lane) {
+    int n = N;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        if (o < N) {
+            n >>= 1;
+            const bool up = lane & o;
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i)
+                if (i < n) {
+                    const float give = up ? v[2 * i] : v[2 * i + 1];
+                    const float keep = up ? v[2 * i + 1] : v[2 * i];
+                    v[i] = keep + __shfl_xor_sync(kAll, give, o);
+                }
+        } else {
+            v[0] += __shfl_xor_sync(kAll, v[0], o);
+        }
+    }
+    return v[0];
+}
+
+// Gradients of the merge; FMT != 0: the packed rows come from a checkpoint.
+// a.token_warps warps share a token's spans and add their parts of each
+// weight's gradient up in shared memory, in warp order.  KU rows' loads are in
+// flight at a time.
+template <class E, int VW, int FMT, int KU>
 __global__ void __launch_bounds__(kExpertThreads)
 expert_merge_backward_rows(const __grid_constant__ ExpertArgs a) {
     using S = typename E::S;
+    __shared__ float parts[kExpertWarps][KU];
     wait_for_previous_grid();
     if (blockIdx.x >= a.row_blocks) {
         zero_gaps<S, VW>(a, a.grad_packed, blockIdx.x - a.row_blocks);
         return;
     }
-    const int lane = int(threadIdx.x & 31);
-    for (int64_t t = int64_t(blockIdx.x) * kExpertWarps + (threadIdx.x >> 5); t < a.T;
-         t += int64_t(a.row_blocks) * kExpertWarps) {
-        for (int k = 0; k < a.K; ++k) {
-            const int r = slot_row(a, t, k);
-            float dot = 0.0f;
-            if (r >= 0) {
-                const float w = a.weights[t * a.weight_stride + k * a.weight_col_stride];
-                for (int64_t col0 = 0; col0 < a.M; col0 += kSpan) {
-                    S g[8], d[8];
-                    float y[8];
-                    load_span<S, VW>(static_cast<const S *>(a.tokens) + t * a.token_stride,
-                                     a.col_stride, col0, a.M, lane, g);
+    const int lane = int(threadIdx.x & 31), warp = int(threadIdx.x >> 5);
+    const int tokens = kExpertWarps / a.token_warps;             // of a block at a time
+    const int part = warp % a.token_warps;
+    for (int64_t t0 = int64_t(blockIdx.x) * tokens; t0 < a.T;    // block-uniform
+         t0 += int64_t(a.row_blocks) * tokens) {
+        const int64_t t = t0 + warp / a.token_warps;
+        for (int k0 = 0; k0 < a.K; k0 += KU) {
+            const int rows = t < a.T ? slot_rows(a, t, k0, lane) : -1;
+            const float weights = slot_weights(a, t, k0, lane, rows);
+            float dot[KU] = {};
+            for (int s = t < a.T ? part : a.spans; s < a.spans; s += a.token_warps) {
+                const int col0 = s * kSpan;
+                const Lane8<S> gv = load_span<S, VW>(a.tokens, t * a.token_stride, a.col_stride,
+                                                     col0, a.M, lane);
+                Lane8<S> v[KU];
+                KeptLane<VW> q[KU];
+                int r[KU];
+#pragma unroll
+                for (int j = 0; j < KU; ++j) {
+                    r[j] = __shfl_sync(kAll, rows, j);
+                    if constexpr (FMT != 0)
+                        q[j] = load_kept<VW>(a, r[j], col0, lane, r[j] >= 0);
+                    else
+                        v[j] = load_span<S, VW>(a.packed, int64_t(r[j]) * a.M, 1, col0, a.M,
+                                                lane, r[j] >= 0);
+                }
+                float g[8];
+                widen_span<E>(gv, g);
+#pragma unroll
+                for (int j = 0; j < KU; ++j) {
+                    const float w = __shfl_sync(kAll, weights, j);
+                    float y[8], d[8];
                     if constexpr (FMT != 0) {
-                        restore_span<VW, FMT>(a, r, col0, lane, y);
+                        code_values<FMT>(q[j].code, y);
+#pragma unroll
+                        for (int u = 0; u < 8 / VW; ++u) {
+                            float sum = 0.0f;                    // of codes; the scale once
+#pragma unroll
+                            for (int i = 0; i < VW; ++i)
+                                sum = __fmaf_rn(g[u * VW + i], y[u * VW + i], sum);
+                            dot[j] = __fmaf_rn(finite_or_nan(q[j].scale[u]), sum, dot[j]);
+                        }
                     } else {
-                        S v[8];
-                        load_span<S, VW>(static_cast<const S *>(a.packed) + int64_t(r) * a.M, 1,
-                                         col0, a.M, lane, v);
+                        widen_span<E>(v[j], y);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) y[i] = E::widen(v[i]);
+                        for (int i = 0; i < 8; ++i) dot[j] = __fmaf_rn(g[i], y[i], dot[j]);
                     }
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        dot = __fmaf_rn(E::widen(g[i]), y[i], dot);
-                        d[i] = E::round(w * E::widen(g[i]));
-                    }
-                    store_span<S, VW>(static_cast<S *>(a.grad_packed) + int64_t(r) * a.M, 1,
-                                      col0, a.M, lane, d);
+                    for (int i = 0; i < 8; ++i) d[i] = w * g[i];
+                    if (r[j] >= 0)
+                        store_span<S, VW>(a.grad_packed, int64_t(r[j]) * a.M, 1, col0, a.M, lane,
+                                          round_span<E>(d));
                 }
             }
-            for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(kAll, dot, o);
-            if (lane == 0) a.grad_weights[t * a.K + k] = dot;
+            const float sum = warp_sums<KU>(dot, lane);
+            __syncthreads();                                     // parts is free again
+            if (lane < KU) parts[warp][lane] = sum;
+            __syncthreads();
+            if (part == 0 && t < a.T && lane < KU && k0 + lane < a.K) {
+                float all = 0.0f;
+                for (int p = 0; p < a.token_warps; ++p) all += parts[warp + p][lane];
+                a.grad_weights[t * a.K + k0 + lane] = all;
+            }
         }
     }
 }

@@ -7,6 +7,7 @@
 #include <climits>
 #include <cstdint>
 #include <cstring>
+#include <type_traits>
 
 #include "checks.h"
 #include "expert_kernel.cuh"
@@ -19,7 +20,8 @@ using namespace vfc;
 constexpr int64_t kMaxSlots = int64_t(1) << 30;     // T * K
 constexpr int64_t kMaxExperts = 4096;
 constexpr int64_t kMaxRows = INT32_MAX;
-constexpr int64_t kMaxGrid = int64_t(1) << 30;
+constexpr int64_t kMaxGrid = int64_t(1) << 28;
+constexpr int64_t kTableBlocks = 152 * 8;
 
 cudaStream_t as_stream(vf_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
 
@@ -67,7 +69,9 @@ constexpr int64_t kPlanOneBlock = 8192;                // slots that one block s
 
 PlanShape plan_shape(int64_t slots, int64_t E) {
     PlanShape p;
-    p.warps = std::max<int64_t>(1, std::min<int64_t>(32, kPlanCounters / E));
+    // a warp for every 32 slots, at most what the counters have room for
+    p.warps = std::min<int64_t>(32, std::max<int64_t>(1, ceil_div(slots, 32)));
+    p.warps = std::max<int64_t>(1, std::min(p.warps, kPlanCounters / E));
     const int64_t step = 32 * p.warps;
     p.blocks = slots <= kPlanOneBlock ? 1 : std::min(kPlanBlocks, ceil_div(slots, 2048));
     p.tile = std::max<int64_t>(1, ceil_div(ceil_div(slots, p.blocks), step)) * step;
@@ -213,22 +217,22 @@ vf::ExpertArgs make_args(const vf_expert_desc *d) {
     a.grad_packed = d->grad_packed;
     a.grad_weights = d->grad_weights;
     a.T = d->T;
-    a.M = d->M;
+    a.M = int32_t(d->M);
     a.K = int32_t(d->K);
     a.rows = int32_t(d->rows);
     a.E = int32_t(d->E);
-    a.group = d->format ? int32_t(d->group) : 1;
+    while (d->format && (int64_t(1) << a.group_log2) < d->group) ++a.group_log2;
     a.spans = int32_t(ceil_div(d->M, vf::kSpan));
     a.groups = d->format ? int32_t(ceil_div(d->M, d->group)) : 0;
     return a;
 }
 
-int launch_rows(void (*kernel)(vf::ExpertArgs), vf::ExpertArgs a, int64_t items, bool gaps,
-                cudaStream_t stream) {
-    const int64_t blocks = std::min(kMaxGrid, ceil_div(items, vf::kExpertWarps));
-    a.row_blocks = uint32_t(blocks);
-    return launch(kernel, blocks + (gaps ? int64_t(a.E) * vf::kGapBlocks : 0),
-                  vf::kExpertThreads, 0, stream, a);
+// Warps that share a token in the merge's backward pass: one per span, at most
+// the block's, a power of two.
+int token_warps(int64_t spans) {
+    int w = 1;
+    while (w < vf::kExpertWarps && w < spans) w *= 2;
+    return w;
 }
 
 using RowKernel = void (*)(vf::ExpertArgs);
@@ -248,45 +252,67 @@ RowKernel restore_kernel(int format) {
                                     : vf::expert_restore_rows<VW, vf::kFmtE4M3>;
 }
 
-template <class E, int VW>
+// Rows whose loads are in flight at a time.
+template <class E, int VW, int KU>
 RowKernel merge_kernel(int format) {
     if constexpr (std::is_same_v<E, vf::Bf16>) {
-        if (format == VF_FORMAT_INT8) return vf::expert_merge_rows<E, VW, vf::kFmtInt8>;
-        if (format == VF_FORMAT_E4M3) return vf::expert_merge_rows<E, VW, vf::kFmtE4M3>;
+        if (format == VF_FORMAT_INT8) return vf::expert_merge_rows<E, VW, vf::kFmtInt8, 4>;
+        if (format == VF_FORMAT_E4M3) return vf::expert_merge_rows<E, VW, vf::kFmtE4M3, 4>;
     }
-    return vf::expert_merge_rows<E, VW, 0>;
+    return vf::expert_merge_rows<E, VW, 0, KU>;
 }
 
-template <class E, int VW>
+template <class E, int VW, int KU>
 RowKernel backward_kernel(int format) {
     if constexpr (std::is_same_v<E, vf::Bf16>) {
-        if (format == VF_FORMAT_INT8) return vf::expert_merge_backward_rows<E, VW, vf::kFmtInt8>;
-        if (format == VF_FORMAT_E4M3) return vf::expert_merge_backward_rows<E, VW, vf::kFmtE4M3>;
+        if (format == VF_FORMAT_INT8)
+            return vf::expert_merge_backward_rows<E, VW, vf::kFmtInt8, 4>;
+        if (format == VF_FORMAT_E4M3)
+            return vf::expert_merge_backward_rows<E, VW, vf::kFmtE4M3, 4>;
     }
-    return vf::expert_merge_backward_rows<E, VW, 0>;
+    return vf::expert_merge_backward_rows<E, VW, 0, KU>;
 }
 
 // The kernel of a call for a type, unit width and format.
 template <class E, int VW>
-RowKernel pick(Call call, int format) {
+RowKernel pick(Call call, int format, int64_t K) {
+    constexpr bool wide = VW * sizeof(typename E::S) == 16;
+    constexpr int most = wide && sizeof(typename E::S) == 2 ? 8 : 4;
     switch (call) {
         case Call::kPack: return pack_kernel<typename E::S, VW>(format);
         case Call::kRestore: return restore_kernel<VW>(format);
-        case Call::kMerge: return merge_kernel<E, VW>(format);
-        default: return backward_kernel<E, VW>(format);
+        case Call::kMerge:
+            if constexpr (wide) {
+                if (K <= 2) return merge_kernel<E, VW, 2>(format);
+                if (K <= 4) return merge_kernel<E, VW, 4>(format);
+            }
+            return merge_kernel<E, VW, most>(format);
+        default:
+            if constexpr (wide) {
+                if (K <= 2) return backward_kernel<E, VW, 2>(format);
+                if (K <= 4) return backward_kernel<E, VW, 4>(format);
+            }
+            return backward_kernel<E, VW, most>(format);
     }
 }
 
 template <class E>
-RowKernel pick_width(Call call, int format, int vw) {
-    return pick<E, 1>(call, format);
+RowKernel pick_width(Call call, int format, int vw, int64_t K) {
+    switch (vw) {
+        case 8:
+            if constexpr (sizeof(typename E::S) == 2) return pick<E, 8>(call, format, K);
+            return pick<E, 4>(call, format, K);
+        case 4: return pick<E, 4>(call, format, K);
+        case 2: return pick<E, 2>(call, format, K);
+        default: return pick<E, 1>(call, format, K);
+    }
 }
 
-RowKernel pick_type(Call call, int type, int format, int vw) {
+RowKernel pick_type(Call call, int type, int format, int vw, int64_t K) {
     switch (type) {
-        case VF_TYPE_BF16: return pick_width<vf::Bf16>(call, format, vw);
-        case VF_TYPE_F16: return pick_width<vf::F16>(call, format, vw);
-        default: return pick_width<vf::F32>(call, format, vw);
+        case VF_TYPE_BF16: return pick_width<vf::Bf16>(call, format, vw, K);
+        case VF_TYPE_F16: return pick_width<vf::F16>(call, format, vw, K);
+        default: return pick_width<vf::F32>(call, format, vw, K);
     }
 }
 
@@ -302,7 +328,7 @@ int run(const vf_expert_desc *d, Call call, vf_stream_t stream) {
     const int64_t groups = fmt ? ceil_div(d->M, d->group) : 0;
     // the checkpoint covers packed rows in the merge, token rows in the pack
     const int64_t kept = call == Call::kMerge || backward ? d->rows : d->T;
-    int64_t n_packed, n_kept, n_scales = 0;
+    int64_t n_packed, n_kept, n_scales;
     if (!mul_ok(d->rows, d->M, &n_packed) || !mul_ok(kept, d->M, &n_kept) ||
         !mul_ok(kept, groups, &n_scales))
         return VF_ERR_OVERFLOW;
@@ -332,11 +358,24 @@ int run(const vf_expert_desc *d, Call call, vf_stream_t stream) {
     }
     if ((rc = rs.check()) != VF_OK) return rc;
 
-    const vf::ExpertArgs a = make_args(d);
+    vf::ExpertArgs a = make_args(d);
     const int vw = unit_width(d, tokens, packed, fmt, backward);
+    const RowKernel kernel = pick_type(call, d->type, d->format, vw, d->K);
+    a.token_warps = token_warps(a.spans);
+    int64_t blocks = backward ? ceil_div(a.T, vf::kExpertWarps / a.token_warps)
+                              : ceil_div(a.T * a.spans, vf::kExpertWarps);
+    // a checkpoint's blocks fill a table of scales first: few blocks, long ones
+    if (fmt && (call == Call::kMerge || call == Call::kPack))
+        blocks = std::min<int64_t>(blocks, kTableBlocks);
+    blocks = std::min(blocks, kMaxGrid);
+    a.row_blocks = uint32_t(blocks);
+    if (a.spans > 0) {
+        a.step_tokens = int32_t(blocks * vf::kExpertWarps / a.spans);
+        a.step_spans = int32_t(blocks * vf::kExpertWarps % a.spans);
+    }
     const bool gaps = writes_rows && d->align > 1 && n_packed > 0;
-    return launch_rows(pick_type(call, d->type, d->format, vw), a,
-                       backward ? d->T : d->T * a.spans, gaps, as_stream(stream));
+    return launch(kernel, blocks + (gaps ? int64_t(a.E) * vf::kGapBlocks : 0),
+                  vf::kExpertThreads, 0, as_stream(stream), a);
 }
 
 }  // namespace
