@@ -176,9 +176,11 @@ def _strides(t: torch.Tensor):
 def _stream(stream, device):
     """The stream to enqueue on: the given one, else the current stream of the
     tensor's device (of the current device for pinned host tensors)."""
-    if stream is None:
-        stream = torch.cuda.current_stream(device if device.type == "cuda" else None)
-    return ctypes.c_void_p(stream.cuda_stream)
+    if stream is not None:
+        return ctypes.c_void_p(stream.cuda_stream)
+    # (the handle itself: building a Stream object costs 2 us a call)
+    index = device.index if device.type == "cuda" else torch.cuda.current_device()
+    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(index))
 
 
 def _call(fn, *args):
@@ -555,7 +557,8 @@ class ExpertPlan(NamedTuple):
 
 
 def _rows_type(t: torch.Tensor, what: str) -> int:
-    _gpu_addressable(t, what)
+    if not (isinstance(t, torch.Tensor) and t.is_cuda):
+        _gpu_addressable(t, what)
     f = _TYPES.get(t.dtype)
     if f is None:
         raise ValueError("%s must hold bfloat16, float16 or float32 values" % what)
@@ -565,19 +568,20 @@ def _rows_type(t: torch.Tensor, what: str) -> int:
 def _check_plan(plan, T=None):
     """(T, K, rows, E) of a plan whose tensors have the types and shapes that
     the kernels take; what they hold is checked by the kernels."""
-    row_of, slot_of, counts, offsets, align = plan
-    for t, name in ((row_of, "row_of"), (slot_of, "slot_of"), (counts, "counts"),
-                    (offsets, "offsets")):
-        _gpu_addressable(t, "plan." + name)
-        if t.dtype != torch.int32 or not t.is_contiguous():
-            raise ValueError("plan.%s must be a contiguous int32 tensor" % name)
-    if row_of.dim() != 2 or slot_of.dim() != 1 or counts.dim() != 1 or \
-            tuple(offsets.shape) != (counts.shape[0] + 1,):
+    row_of, slot_of, counts, offsets, _ = plan
+    i32 = torch.int32
+    for t in (row_of, slot_of, counts, offsets):
+        if not t.is_cuda:
+            _gpu_addressable(t, "plan")
+        if t.dtype != i32 or not t.is_contiguous():
+            raise ValueError("the tensors of a plan must be contiguous and int32")
+    a, rows, E, o = row_of.shape, slot_of.shape, counts.shape, offsets.shape
+    if len(a) != 2 or len(rows) != 1 or len(E) != 1 or len(o) != 1 or o[0] != E[0] + 1:
         raise ValueError("plan must hold row_of [T,K], slot_of [rows], counts [E] and "
                          "offsets [E+1]")
-    if T is not None and row_of.shape[0] != T:
-        raise ValueError("plan is for %d tokens, not %d" % (row_of.shape[0], T))
-    return row_of.shape[0], row_of.shape[1], slot_of.shape[0], counts.shape[0]
+    if T is not None and a[0] != T:
+        raise ValueError("plan is for %d tokens, not %d" % (a[0], T))
+    return a[0], a[1], rows[0], E[0]
 
 
 def _new(stream, like, shape, dtype):
@@ -586,7 +590,7 @@ def _new(stream, like, shape, dtype):
     if like.device.type != "cuda":
         return torch.empty(shape, dtype=dtype, pin_memory=True)
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=like.device)
 
@@ -595,8 +599,9 @@ def _rows_out(t, stream, like, shape, dtype, what):
     """Check (or allocate) a contiguous [rows, M] tensor."""
     if t is None:
         return _new(stream, like, shape, dtype)
-    _gpu_addressable(t, what)
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+    if not (isinstance(t, torch.Tensor) and t.is_cuda):
+        _gpu_addressable(t, what)
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError("%s must be a contiguous %s tensor of shape %s" % (what, dtype, shape))
     return t
 
@@ -605,8 +610,9 @@ def _tokens_out(t, stream, like, shape, dtype, what):
     """Check (or allocate) a [T, M] view."""
     if t is None:
         return _new(stream, like, shape, dtype)
-    _gpu_addressable(t, what)
-    if t.dtype != dtype or tuple(t.shape) != shape:
+    if not (isinstance(t, torch.Tensor) and t.is_cuda):
+        _gpu_addressable(t, what)
+    if t.dtype != dtype or t.shape != shape:
         raise ValueError("%s must be a %s view of shape %s" % (what, dtype, shape))
     return t
 
@@ -621,27 +627,25 @@ def _kept(codes, scales, stream, like, n, M, f, group):
 
 
 def _expert_desc(typ, plan, dims, M):
-    T, K, rows, E = dims
-    d = _ExpertDesc(type=typ, T=T, K=K, M=M, E=E, rows=rows, align=plan.align)
-    d.row_of = plan.row_of.data_ptr()
-    d.counts = plan.counts.data_ptr()
-    d.offsets = plan.offsets.data_ptr()
+    d = _ExpertDesc(typ, 0, dims[0], dims[1], M, dims[3], dims[2], plan[4])
+    d.row_of, d.counts, d.offsets = plan[0].data_ptr(), plan[2].data_ptr(), plan[3].data_ptr()
     return d
 
 
 def _set_tokens(d, t):
     d.tokens = t.data_ptr()
-    d.token_strides[0], d.token_strides[1] = t.stride()
+    d.token_strides = t.stride()
 
 
 def _set_weights(d, weights, T, K):
     if weights is None:
         return
-    _gpu_addressable(weights, "weights")
-    if weights.dtype != torch.float32 or tuple(weights.shape) != (T, K):
+    if not (isinstance(weights, torch.Tensor) and weights.is_cuda):
+        _gpu_addressable(weights, "weights")
+    if weights.dtype != torch.float32 or weights.shape != (T, K):
         raise ValueError("weights must be a float32 view of shape [T,K]")
     d.weights = weights.data_ptr()
-    d.weight_strides[0], d.weight_strides[1] = weights.stride()
+    d.weight_strides = weights.stride()
 
 
 def _set_kept(d, codes, scales, f, group):
@@ -678,24 +682,27 @@ def expert_plan(experts: torch.Tensor, E: int, align: int = 1, out: ExpertPlan =
     Each expert's rows start at a multiple of ``align``.  ``out`` gives the
     tensors of an earlier plan of the same sizes to be written again.
     """
-    _gpu_addressable(experts, "experts")
+    if not (isinstance(experts, torch.Tensor) and experts.is_cuda):
+        _gpu_addressable(experts, "experts")
     if experts.dtype not in (torch.int32, torch.int64) or experts.dim() != 2:
         raise ValueError("experts must be an int32 or int64 view of shape [T,K]")
     T, K = experts.shape
+    slots = T * K
     rows = expert_rows(T, K, E, align)
+    words = lib().vf_expert_workspace(T, K, E) // 4
     if out is None:
-        out = ExpertPlan(*(_new(stream, experts, shape, torch.int32)
-                           for shape in ((T, K), (rows,), (E,), (E + 1,))), align)
-    elif _check_plan(out) != (T, K, rows, E) or out.align != align:
-        raise ValueError("out is a plan of other sizes")
-    n = lib().vf_expert_workspace(T, K, E)
-    if n < 0:
-        raise VFError("vf_expert_workspace", n)
-    work = _new(stream, experts, (n,), torch.uint8) if n else None
+        # one allocation: each costs more than the checks of a whole call
+        both = _new(stream, experts, (slots + rows + 2 * E + 1 + words,), torch.int32)
+        row_of, slot_of, counts, offsets, work = both.split_with_sizes(
+            (slots, rows, E, E + 1, words))
+        out = ExpertPlan(row_of.view(T, K), slot_of, counts, offsets, align)
+    else:
+        if _check_plan(out) != (T, K, rows, E) or out.align != align:
+            raise ValueError("out is a plan of other sizes")
+        work = _new(stream, experts, (words,), torch.int32)
     _call("vf_expert_plan", experts.data_ptr(), experts.element_size(), _strides(experts), T, K,
           E, align, out.row_of.data_ptr(), out.slot_of.data_ptr(), out.counts.data_ptr(),
-          out.offsets.data_ptr(), None if work is None else work.data_ptr(),
-          _stream(stream, experts.device))
+          out.offsets.data_ptr(), work.data_ptr(), _stream(stream, experts.device))
     return out
 
 

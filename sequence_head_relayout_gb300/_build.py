@@ -17,7 +17,7 @@ SOURCES = [os.path.join(CSRC, n) for n in ("vf_relayout.cu", "vf_quant.cu", "vf_
 DEPS = SOURCES + [os.path.join(CSRC, n) for n in ("relayout_kernel.cuh", "launch.cuh",
                                                   "tiled_kernel.cuh", "quant_kernel.cuh",
                                                   "quant.h", "checks.h",
-                                                  "expert_kernel.cuh")] \
+                                                  "expert_kernel.cuh", "expert_q_kernel.cuh")] \
     + [os.path.join(ROOT, "include", "vf_relayout.h")]
 LIB = os.path.join(PKG, "libvf_relayout.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

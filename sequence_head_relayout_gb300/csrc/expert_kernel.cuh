@@ -33,6 +33,7 @@ constexpr int kSpan = 256;               // columns of a warp's span
 constexpr int kExpertThreads = 256;      // threads per block of the row kernels
 constexpr int kExpertWarps = kExpertThreads / 32;
 constexpr int kPlanThreads = 1024;
+constexpr int kMergeResident = 4;        // blocks of the merge that fit an SM
 constexpr int kGapBlocks = 4;            // blocks that zero one expert's gap rows
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 
@@ -100,6 +101,10 @@ __device__ __forceinline__ void store_unit(S *p, const S *v) {
     *reinterpret_cast<B *>(p) = b;
 }
 
+// Packed rows whose loads a lane has in flight in the merge and its backward
+// pass: 64 bytes.
+template <class S> constexpr int kRowsInFlight = sizeof(S) == 2 ? 4 : 2;
+
 // Arguments of the row kernels.
 struct ExpertArgs {
     const int32_t *row_of;        // [T][K]
@@ -132,7 +137,7 @@ struct Walk {
 
     __device__ __forceinline__ explicit Walk(const ExpertArgs &a) {
         // row_blocks * kExpertWarps fits 32 bits
-        const uint32_t it = blockIdx.x * kExpertWarps + (threadIdx.x >> 5);
+        const uint32_t it = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
         t = it / uint32_t(a.spans);
         s = int(it - uint32_t(t) * uint32_t(a.spans));
     }
@@ -180,6 +185,18 @@ __device__ __forceinline__ void store_span(void *base, int64_t offset, int64_t s
     }
 }
 
+// Two float32 fused multiply-adds, a * b + c, in one instruction (sm_100 and
+// later), each rounded once.
+__device__ __forceinline__ float2 fma2_rn(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 pa, pb, pc, pd;\n\t"
+        "mov.b64 pa, {%2, %3};\n\tmov.b64 pb, {%4, %5};\n\tmov.b64 pc, {%6, %7};\n\t"
+        "fma.rn.f32x2 pd, pa, pb, pc;\n\tmov.b64 {%0, %1}, pd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+
 template <class E>
 __device__ __forceinline__ void widen_span(const Lane8<typename E::S> &v, float (&f)[8]) {
     constexpr int N = 4 / int(sizeof(typename E::S));
@@ -196,21 +213,27 @@ __device__ __forceinline__ Lane8<typename E::S> round_span(const float (&f)[8]) 
     return v;
 }
 
-// Rows of up to 32 slots of token t, k0 onward: lane j holds slot k0 + j's
-// row, -1 when it is dropped, past K, or names a row that does not exist.
-__device__ __forceinline__ int slot_rows(const ExpertArgs &a, int64_t t, int k0, int lane) {
-    const int r = k0 + lane < a.K ? a.row_of[t * a.K + k0 + lane] : -1;
-    return r >= 0 && r < a.rows ? r : -1;
-}
+// The routing of up to 32 slots of token t, k0 onward: lane j holds slot k0 + j's
+// row, -1 when it is dropped, past K or the token past T, or when it names a row
+// that does not exist, and its weight, 0 where the row is -1 (whatever is
+// stored).  Both loads are issued at once.
+struct Slots {
+    int row;
+    float weight;
 
-// Their weights; 0 where the row is -1, whatever the weight is.
-__device__ __forceinline__ float slot_weights(const ExpertArgs &a, int64_t t, int k0, int lane,
-                                              int row) {
-    if (row < 0) return 0.0f;
-    return a.weights == nullptr
-               ? 1.0f
-               : a.weights[t * a.weight_stride + (k0 + lane) * a.weight_col_stride];
-}
+    __device__ __forceinline__ Slots(const ExpertArgs &a, int64_t t, int k0, int lane,
+                                     bool weighted) {
+        const bool there = t < a.T && k0 + lane < a.K;
+        row = there ? a.row_of[t * a.K + k0 + lane] : -1;
+        weight = 1.0f;
+        if (weighted && there)
+            weight = a.weights[t * a.weight_stride + (k0 + lane) * a.weight_col_stride];
+        if (row < 0 || row >= a.rows) {
+            row = -1;
+            weight = 0.0f;
+        }
+    }
+};
 
 // Zeros for the gap rows of every expert: block `b` of kGapBlocks * E.
 template <class S, int VW>
@@ -221,41 +244,47 @@ __device__ __forceinline__ void zero_gaps(const ExpertArgs &a, void *packed, uin
     const S zero[VW] = {};
     for (int64_t r = max(first, int64_t(0)); r < end; r += kGapBlocks) {
         S *row = static_cast<S *>(packed) + r * a.M;
-        for (int64_t c = int64_t(threadIdx.x) * VW; c < a.M; c += kExpertThreads * VW)
+        for (int64_t c = int64_t(threadIdx.x) * VW; c < a.M; c += int64_t(blockDim.x) * VW)
             store_unit<S, VW>(row + c, zero);
     }
 }
 
 // ---- 8-bit checkpoints of a span ----------------------------------------------
 
-// fl(top / M) and fl(M / top) of the 128 bfloat16 mantissas M, in shared
-// memory (quant_kernel.cuh derives the format's inverse and scale from them
-// without a division per group).
+// fl(top / M) and fl(M / top) of the 128 bfloat16 mantissas M, as bits, in
+// shared memory: quant_kernel.cuh derives a row's inverse and scale from them
+// without a division.  The exponent's bias is folded in, so that adding or
+// subtracting the group's exponent field gives the result.
 struct ScaleTable {
-    float inv[kMantissas], scale[kMantissas];
+    uint32_t inv[kMantissas], scale[kMantissas];
 };
+
+constexpr uint32_t kBias = 127u << 23;
 
 template <int FMT>
 __device__ __forceinline__ void fill_table(ScaleTable &tab) {
     const float top = top_code<FMT>();
-    for (int i = int(threadIdx.x); i < kMantissas; i += kExpertThreads) {
+    for (int i = int(threadIdx.x); i < kMantissas; i += int(blockDim.x)) {
         const float M = 1.0f + float(i) * (1.0f / 128.0f);      // exact
-        tab.inv[i] = __fdiv_rn(top, M);
-        tab.scale[i] = __fdiv_rn(M, top);
+        tab.inv[i] = __float_as_uint(__fdiv_rn(top, M)) + kBias;
+        tab.scale[i] = __float_as_uint(__fdiv_rn(M, top)) - kBias;
     }
     __syncthreads();
 }
 
-// inv and scale of a group whose largest magnitude is the bfloat16 pattern m.
-__device__ __forceinline__ void group_scale(const ScaleTable &tab, uint32_t m, float *inv,
-                                            float *scale) {
-    const bool lost = non_finite_magnitude(m);
-    const bool live = !lost && m >= 0x0F80u;                    // amax >= 2^-96
-    const uint32_t k23 = uint32_t((int32_t(m >> 7) - 127) * (1 << 23));
-    const uint32_t i = m & 0x7Fu;
-    *inv = live ? __uint_as_float(__float_as_uint(tab.inv[i]) - k23) : 0.0f;
-    *scale = lost ? __uint_as_float(kLostScaleBits)
-             : live ? __uint_as_float(__float_as_uint(tab.scale[i]) + k23) : 0.0f;
+// 1 / scale of a group whose largest magnitude is the bfloat16 pattern m; 0
+// where the group is not live (amax < 2^-96, or not finite).
+__device__ __forceinline__ bool live_group(uint32_t m) { return m - 0x0F80u < 0x7F80u - 0x0F80u; }
+
+__device__ __forceinline__ float group_inverse(const ScaleTable &tab, uint32_t m) {
+    const uint32_t bits = tab.inv[m & 0x7Fu] - ((m << 16) & 0x7F800000u);
+    return live_group(m) ? __uint_as_float(bits) : 0.0f;
+}
+
+__device__ __forceinline__ float group_scale(const ScaleTable &tab, uint32_t m) {
+    if (non_finite_magnitude(m)) return __uint_as_float(kLostScaleBits);
+    const uint32_t bits = tab.scale[m & 0x7Fu] + ((m << 16) & 0x7F800000u);
+    return live_group(m) ? __uint_as_float(bits) : 0.0f;
 }
 
 // Quantises one span of a row (zeros past the row's end) group by group and
@@ -266,51 +295,35 @@ template <int VW, int FMT>
 __device__ __forceinline__ void checkpoint_span(const ExpertArgs &a, const ScaleTable &tab,
                                                 int64_t row, int col0, int lane,
                                                 const Lane8<uint16_t> &v) {
+    static_assert(VW < 8, "expert_q_kernel.cuh has the form for 16-byte accesses");
     constexpr int U = 8 / VW;
-    const int lanes = min(32, (1 << a.group_log2) / VW);               // of a unit that share a group
-    const int units = max(1, (1 << a.group_log2) / (32 * VW));         // that share a group
+    const int lanes = min(32, (1 << a.group_log2) / VW);        // of a unit that share a group
     const uint16_t *h = reinterpret_cast<const uint16_t *>(v.w);
     uint32_t m[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        if constexpr (VW == 8) {
-            m[u] = max_u16x2(max_u16x2(mag2(v.w[0]), mag2(v.w[1])),
-                             max_u16x2(mag2(v.w[2]), mag2(v.w[3])));
-        } else {
-            m[u] = 0;
+        m[u] = 0;
 #pragma unroll
-            for (int i = 0; i < VW; ++i) m[u] = max(m[u], uint32_t(h[u * VW + i]) & 0x7FFFu);
-        }
-        for (int o = lanes >> 1; o > 0; o >>= 1)
-            m[u] = max_u16x2(m[u], __shfl_xor_sync(kAll, m[u], o));
-        m[u] = max(m[u] & 0xFFFFu, m[u] >> 16);
+        for (int i = 0; i < VW; ++i) m[u] = max(m[u], uint32_t(h[u * VW + i]) & 0x7FFFu);
+        for (int o = lanes >> 1; o > 0; o >>= 1) m[u] = max(m[u], __shfl_xor_sync(kAll, m[u], o));
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int c = col0 + unit_col<VW>(u, lane);
-        uint32_t top_mag = m[u];
+        uint32_t top_mag = m[u];                                // over the units that share it
 #pragma unroll
         for (int w = 0; w < U; ++w)
-            if (w / units == u / units) top_mag = max(top_mag, m[w]);
-        float inv, scale;
-        group_scale(tab, top_mag, &inv, &scale);
+            if ((w * 32 * VW) >> a.group_log2 == (u * 32 * VW) >> a.group_log2)
+                top_mag = max(top_mag, m[w]);
         if (c >= a.M) continue;
-        if (lane % lanes == 0 && u % units == 0)
-            a.scales[row * a.groups + (c >> a.group_log2)] = scale;
-        if constexpr (VW == 8) {
-            uint2 code = encode8<FMT>(make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]), inv);
-            // (a lost group's codes are 0 whatever its elements: inv is 0 and
-            // a NaN or an infinity times 0 would not be)
-            if (inv == 0.0f) code = make_uint2(0, 0);
-            *reinterpret_cast<uint2 *>(a.codes + row * a.M + c) = code;
-        } else {
-            uint16_t x[VW];
-            uint8_t code[VW];
+        if ((c & ((1 << a.group_log2) - 1)) == 0)
+            a.scales[row * a.groups + (c >> a.group_log2)] = group_scale(tab, top_mag);
+        uint16_t x[VW];
+        uint8_t code[VW];
 #pragma unroll
-            for (int i = 0; i < VW; ++i) x[i] = h[u * VW + i];
-            encode<VW, FMT>(x, inv, inv != 0.0f, code);
-            store_unit<uint8_t, VW>(a.codes + row * a.M + c, code);
-        }
+        for (int i = 0; i < VW; ++i) x[i] = h[u * VW + i];
+        encode<VW, FMT>(x, group_inverse(tab, top_mag), live_group(top_mag), code);
+        store_unit<uint8_t, VW>(a.codes + row * a.M + c, code);
     }
 }
 
@@ -319,6 +332,12 @@ __device__ __forceinline__ void checkpoint_span(const ExpertArgs &a, const Scale
 template <int VW> struct KeptLane {
     uint8_t code[8];
     float scale[8 / VW];
+
+    __device__ __forceinline__ uint2 words() const {
+        uint2 w;
+        memcpy(&w, code, 8);
+        return w;
+    }
 };
 
 template <int VW>
@@ -338,9 +357,8 @@ __device__ __forceinline__ KeptLane<VW> load_kept(const ExpertArgs &a, int64_t r
 
 // Code values of the lane's columns, as float32 (exact).
 template <int FMT>
-__device__ __forceinline__ void code_values(const uint8_t (&code)[8], float (&f)[8]) {
-    uint32_t w[2];
-    memcpy(w, code, 8);
+__device__ __forceinline__ void code_values(uint2 code, float (&f)[8]) {
+    const uint32_t w[2] = {code.x, code.y};
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         if constexpr (FMT == kFmtInt8) {
@@ -381,18 +399,18 @@ expert_pack_rows(const __grid_constant__ ExpertArgs a) {
     }
     const int lane = int(threadIdx.x & 31);
     for (Walk at(a); at.t < a.T; at.step(a)) {
-        const int64_t t = at.t;
         const int col0 = at.s * kSpan;
-        const Lane8<S> v = load_span<S, VW>(a.tokens, t * a.token_stride, a.col_stride, col0,
+        Slots slots(a, at.t, 0, lane, false);
+        const Lane8<S> v = load_span<S, VW>(a.tokens, at.t * a.token_stride, a.col_stride, col0,
                                             a.M, lane);
         for (int k0 = 0; k0 < a.K; k0 += 32) {
-            const int rows = slot_rows(a, t, k0, lane);
+            if (k0 > 0) slots = Slots(a, at.t, k0, lane, false);
             for (int j = 0; j < min(32, a.K - k0); ++j) {
-                const int r = __shfl_sync(kAll, rows, j);
+                const int r = __shfl_sync(kAll, slots.row, j);
                 if (r >= 0) store_span<S, VW>(a.packed, int64_t(r) * a.M, 1, col0, a.M, lane, v);
             }
         }
-        if constexpr (FMT != 0) checkpoint_span<VW, FMT>(a, tab, t, col0, lane, v);
+        if constexpr (FMT != 0) checkpoint_span<VW, FMT>(a, tab, at.t, col0, lane, v);
     }
 }
 
@@ -407,11 +425,11 @@ expert_restore_rows(const __grid_constant__ ExpertArgs a) {
     }
     const int lane = int(threadIdx.x & 31);
     for (Walk at(a); at.t < a.T; at.step(a)) {
-        const int64_t t = at.t;
         const int col0 = at.s * kSpan;
-        const KeptLane<VW> q = load_kept<VW>(a, t, col0, lane);
+        Slots slots(a, at.t, 0, lane, false);
+        const KeptLane<VW> q = load_kept<VW>(a, at.t, col0, lane);
         float f[8];
-        code_values<FMT>(q.code, f);
+        code_values<FMT>(q.words(), f);
 #pragma unroll
         for (int i = 0; i < 8; ++i) f[i] = __fmul_rn(f[i], q.scale[i / VW]);
         Lane8<uint16_t> v = round_span<Bf16>(f);
@@ -421,9 +439,9 @@ expert_restore_rows(const __grid_constant__ ExpertArgs a) {
             if (lost_scale(q.scale[i / VW]))
                 reinterpret_cast<uint16_t *>(v.w)[i] = uint16_t(kLostValue2 & 0xFFFFu);
         for (int k0 = 0; k0 < a.K; k0 += 32) {
-            const int rows = slot_rows(a, t, k0, lane);
+            if (k0 > 0) slots = Slots(a, at.t, k0, lane, false);
             for (int j = 0; j < min(32, a.K - k0); ++j) {
-                const int r = __shfl_sync(kAll, rows, j);
+                const int r = __shfl_sync(kAll, slots.row, j);
                 if (r >= 0)
                     store_span<uint16_t, VW>(a.packed, int64_t(r) * a.M, 1, col0, a.M, lane, v);
             }
@@ -432,38 +450,43 @@ expert_restore_rows(const __grid_constant__ ExpertArgs a) {
 }
 
 // Merge; FMT != 0 also keeps the packed rows' checkpoint (a row belongs to one
-// slot, so it is read once).  Walks (token, span); KU rows' loads are in
-// flight at a time.
-template <class E, int VW, int FMT, int KU>
-__global__ void __launch_bounds__(kExpertThreads)
+// slot, so it is read once).  Walks (token, span).
+template <class E, int VW, int FMT>
+__global__ void __launch_bounds__(kExpertThreads, VW * sizeof(typename E::S) < 16 ? 2 : kMergeResident)
 expert_merge_rows(const __grid_constant__ ExpertArgs a) {
     using S = typename E::S;
+    constexpr int KU = kRowsInFlight<S>;
     __shared__ ScaleTable tab;
     if constexpr (FMT != 0) fill_table<FMT>(tab);
     wait_for_previous_grid();
     const int lane = int(threadIdx.x & 31);
+    const bool weighted = a.weights != nullptr;
     for (Walk at(a); at.t < a.T; at.step(a)) {
-        const int64_t t = at.t;
         const int col0 = at.s * kSpan;
+        Slots slots(a, at.t, 0, lane, weighted);
         float acc[8] = {};
         for (int k0 = 0; k0 < a.K; k0 += KU) {
-            const int rows = slot_rows(a, t, k0, lane);
-            const float weights = slot_weights(a, t, k0, lane, rows);
+            if (k0 > 0 && k0 % 32 == 0) slots = Slots(a, at.t, k0, lane, weighted);
             Lane8<S> v[KU];
             int r[KU];
 #pragma unroll
             for (int j = 0; j < KU; ++j) {
-                r[j] = __shfl_sync(kAll, rows, j);
+                r[j] = __shfl_sync(kAll, slots.row, k0 % 32 + j);
                 v[j] = load_span<S, VW>(a.packed, int64_t(r[j]) * a.M, 1, col0, a.M, lane,
                                         r[j] >= 0);
             }
 #pragma unroll
             for (int j = 0; j < KU; ++j) {
-                const float w = __shfl_sync(kAll, weights, j);
+                const float w = __shfl_sync(kAll, slots.weight, k0 % 32 + j);
                 float f[8];
                 widen_span<E>(v[j], f);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) acc[i] = __fmaf_rn(w, f[i], acc[i]);
+                for (int i = 0; i < 8; i += 2) {
+                    const float2 sum = fma2_rn(make_float2(w, w), make_float2(f[i], f[i + 1]),
+                                               make_float2(acc[i], acc[i + 1]));
+                    acc[i] = sum.x;
+                    acc[i + 1] = sum.y;
+                }
             }
             if constexpr (FMT != 0) {
 #pragma unroll
@@ -471,7 +494,7 @@ expert_merge_rows(const __grid_constant__ ExpertArgs a) {
                     if (r[j] >= 0) checkpoint_span<VW, FMT>(a, tab, r[j], col0, lane, v[j]);
             }
         }
-        store_span<S, VW>(a.tokens, t * a.token_stride, a.col_stride, col0, a.M, lane,
+        store_span<S, VW>(a.tokens, at.t * a.token_stride, a.col_stride, col0, a.M, lane,
                           round_span<E>(acc));
     }
 }
@@ -505,10 +528,11 @@ __device__ __forceinline__ float warp_sums(float (&v)[N], int lane) {
 // a.token_warps warps share a token's spans and add their parts of each
 // weight's gradient up in shared memory, in warp order.  KU rows' loads are in
 // flight at a time.
-template <class E, int VW, int FMT, int KU>
-__global__ void __launch_bounds__(kExpertThreads)
+template <class E, int VW, int FMT>
+__global__ void __launch_bounds__(kExpertThreads, VW * sizeof(typename E::S) < 16 ? 2 : 4)
 expert_merge_backward_rows(const __grid_constant__ ExpertArgs a) {
     using S = typename E::S;
+    constexpr int KU = kRowsInFlight<S>;
     __shared__ float parts[kExpertWarps][KU];
     wait_for_previous_grid();
     if (blockIdx.x >= a.row_blocks) {
@@ -516,15 +540,14 @@ expert_merge_backward_rows(const __grid_constant__ ExpertArgs a) {
         return;
     }
     const int lane = int(threadIdx.x & 31), warp = int(threadIdx.x >> 5);
-    const int tokens = kExpertWarps / a.token_warps;             // of a block at a time
+    const int tokens = int(blockDim.x >> 5) / a.token_warps;     // of a block at a time
     const int part = warp % a.token_warps;
     for (int64_t t0 = int64_t(blockIdx.x) * tokens; t0 < a.T;    // block-uniform
          t0 += int64_t(a.row_blocks) * tokens) {
         const int64_t t = t0 + warp / a.token_warps;
         for (int k0 = 0; k0 < a.K; k0 += KU) {
-            const int rows = t < a.T ? slot_rows(a, t, k0, lane) : -1;
-            const float weights = slot_weights(a, t, k0, lane, rows);
-            float dot[KU] = {};
+            const Slots slots(a, t, k0, lane, true);
+            float2 dots[KU] = {};                                // of even and odd columns
             for (int s = t < a.T ? part : a.spans; s < a.spans; s += a.token_warps) {
                 const int col0 = s * kSpan;
                 const Lane8<S> gv = load_span<S, VW>(a.tokens, t * a.token_stride, a.col_stride,
@@ -534,7 +557,7 @@ expert_merge_backward_rows(const __grid_constant__ ExpertArgs a) {
                 int r[KU];
 #pragma unroll
                 for (int j = 0; j < KU; ++j) {
-                    r[j] = __shfl_sync(kAll, rows, j);
+                    r[j] = __shfl_sync(kAll, slots.row, j);
                     if constexpr (FMT != 0)
                         q[j] = load_kept<VW>(a, r[j], col0, lane, r[j] >= 0);
                     else
@@ -545,30 +568,43 @@ expert_merge_backward_rows(const __grid_constant__ ExpertArgs a) {
                 widen_span<E>(gv, g);
 #pragma unroll
                 for (int j = 0; j < KU; ++j) {
-                    const float w = __shfl_sync(kAll, weights, j);
+                    const float w = __shfl_sync(kAll, slots.weight, j);
                     float y[8], d[8];
-                    if constexpr (FMT != 0) {
-                        code_values<FMT>(q[j].code, y);
+                    if constexpr (FMT != 0) code_values<FMT>(q[j].words(), y);
+                    else widen_span<E>(v[j], y);
 #pragma unroll
-                        for (int u = 0; u < 8 / VW; ++u) {
-                            float sum = 0.0f;                    // of codes; the scale once
+                    for (int u = 0; u < 8 / VW; ++u) {
+                        // a checkpoint's unit: of the codes, and their scale once
+                        float2 sum = FMT != 0 ? make_float2(0.0f, 0.0f) : dots[j];
 #pragma unroll
-                            for (int i = 0; i < VW; ++i)
-                                sum = __fmaf_rn(g[u * VW + i], y[u * VW + i], sum);
-                            dot[j] = __fmaf_rn(finite_or_nan(q[j].scale[u]), sum, dot[j]);
+                        for (int i = u * VW; i < (u + 1) * VW; i += 2) {
+                            if constexpr (VW == 1)
+                                (i & 1 ? sum.y : sum.x) =
+                                    __fmaf_rn(g[i], y[i], i & 1 ? sum.y : sum.x);
+                            else
+                                sum = fma2_rn(make_float2(g[i], g[i + 1]),
+                                              make_float2(y[i], y[i + 1]), sum);
                         }
-                    } else {
-                        widen_span<E>(v[j], y);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) dot[j] = __fmaf_rn(g[i], y[i], dot[j]);
+                        if constexpr (FMT != 0) {
+                            const float scale = finite_or_nan(q[j].scale[u]);
+                            sum = fma2_rn(make_float2(scale, scale), sum, dots[j]);
+                        }
+                        dots[j] = sum;
                     }
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) d[i] = w * g[i];
+                    for (int i = 0; i < 8; i += 2) {
+                        const float2 p = mul2_rn(make_float2(w, w), make_float2(g[i], g[i + 1]));
+                        d[i] = p.x;
+                        d[i + 1] = p.y;
+                    }
                     if (r[j] >= 0)
                         store_span<S, VW>(a.grad_packed, int64_t(r[j]) * a.M, 1, col0, a.M, lane,
                                           round_span<E>(d));
                 }
             }
+            float dot[KU];
+#pragma unroll
+            for (int j = 0; j < KU; ++j) dot[j] = dots[j].x + dots[j].y;
             const float sum = warp_sums<KU>(dot, lane);
             __syncthreads();                                     // parts is free again
             if (lane < KU) parts[warp][lane] = sum;
@@ -592,16 +628,28 @@ struct PlanArgs {
     int32_t K, E, align, slots, rows;
     int32_t tile;                 // slots of a block, a multiple of 32 * warps
     int32_t warps;                // warps that sort; each keeps E counters
+    int32_t flat;                 // the view is contiguous: no division per slot
 };
 
-// Expert of slot i, or -1 when the slot is dropped (or i is past the end).
+// Experts of slots i, i + step, ...: their loads are issued together.  -1 for a
+// dropped slot and past the end.
+constexpr int kPlanLoads = 4;
+
 template <class I>
-__device__ __forceinline__ int slot_expert(const PlanArgs &a, int i, int end) {
-    if (i >= end) return -1;
-    const int t = i / a.K;
-    const I e = static_cast<const I *>(a.experts)[t * a.token_stride +
-                                                  int64_t(i - t * a.K) * a.slot_stride];
-    return e >= 0 && e < I(a.E) ? int(e) : -1;
+__device__ __forceinline__ void slot_experts(const PlanArgs &a, int i, int step, int end,
+                                             int (&e)[kPlanLoads]) {
+    I v[kPlanLoads];
+#pragma unroll
+    for (int u = 0; u < kPlanLoads; ++u) {
+        const int j = i + u * step;
+        v[u] = I(-1);
+        if (j >= end) continue;
+        const int t = a.flat ? 0 : j / a.K;
+        v[u] = static_cast<const I *>(
+            a.experts)[t * a.token_stride + int64_t(j - t * a.K) * a.slot_stride];
+    }
+#pragma unroll
+    for (int u = 0; u < kPlanLoads; ++u) e[u] = v[u] >= 0 && v[u] < I(a.E) ? int(v[u]) : -1;
 }
 
 // Counts of each expert in the block's tile.
@@ -609,42 +657,69 @@ template <class I>
 __global__ void __launch_bounds__(kPlanThreads)
 expert_plan_counts(const __grid_constant__ PlanArgs a) {
     extern __shared__ int32_t cnt[];                       // [E]
-    wait_for_previous_grid();
-    for (int e = int(threadIdx.x); e < a.E; e += kPlanThreads) cnt[e] = 0;
+    const int threads = int(blockDim.x);
+    for (int e = int(threadIdx.x); e < a.E; e += threads) cnt[e] = 0;
     __syncthreads();
+    wait_for_previous_grid();
     const int first = int(blockIdx.x) * a.tile;
     const int end = min(a.slots, first + a.tile);
-    for (int i = first + int(threadIdx.x); i < end; i += kPlanThreads) {
-        const int e = slot_expert<I>(a, i, end);
-        if (e >= 0) atomicAdd(&cnt[e], 1);
+    for (int i = first + int(threadIdx.x); i < end; i += kPlanLoads * threads) {
+        int e[kPlanLoads];
+        slot_experts<I>(a, i, threads, end, e);
+#pragma unroll
+        for (int u = 0; u < kPlanLoads; ++u)
+            if (e[u] >= 0) atomicAdd(&cnt[e[u]], 1);
     }
     __syncthreads();
-    for (int e = int(threadIdx.x); e < a.E; e += kPlanThreads)
+    for (int e = int(threadIdx.x); e < a.E; e += threads)
         a.block_counts[int64_t(blockIdx.x) * a.E + e] = cnt[e];
 }
 
-// Inclusive prefix sum over the block's threads; `total` gets the sum.
-__device__ __forceinline__ int block_scan(int v, int *warp_sums, int *total) {
+// Inclusive prefix sum over the block's threads (whole warps); `total` gets the
+// sum.
+__device__ __forceinline__ int block_scan(int v, int *warp_totals, int *total) {
     const int lane = int(threadIdx.x & 31), warp = int(threadIdx.x >> 5);
+    const int warps = int(blockDim.x >> 5);
     for (int o = 1; o < 32; o <<= 1) {
         const int up = __shfl_up_sync(kAll, v, o);
         if (lane >= o) v += up;
     }
-    if (lane == 31) warp_sums[warp] = v;
+    if (lane == 31) warp_totals[warp] = v;
     __syncthreads();
     if (warp == 0) {
-        int s = warp_sums[lane];
+        int s = lane < warps ? warp_totals[lane] : 0;
         for (int o = 1; o < 32; o <<= 1) {
             const int up = __shfl_up_sync(kAll, s, o);
             if (lane >= o) s += up;
         }
-        warp_sums[lane] = s;
+        if (lane < warps) warp_totals[lane] = s;
     }
     __syncthreads();
-    if (warp > 0) v += warp_sums[warp - 1];
-    *total = warp_sums[31];
+    if (warp > 0) v += warp_totals[warp - 1];
+    *total = warp_totals[warps - 1];
     __syncthreads();
     return v;
+}
+
+// Sums of expert e's counts over the blocks before `mine` (added to *before) and
+// over all blocks (to *all), blocks first, first + step, ...; eight loads at a
+// time.
+__device__ __forceinline__ void sum_blocks(const PlanArgs &a, int e, int first, int step,
+                                           int mine, int *before, int *all) {
+    constexpr int N = 8;
+    for (int b0 = first; b0 < int(gridDim.x); b0 += N * step) {
+        int c[N];
+#pragma unroll
+        for (int u = 0; u < N; ++u) {
+            const int b = b0 + u * step;
+            c[u] = b < int(gridDim.x) ? a.block_counts[int64_t(b) * a.E + e] : 0;
+        }
+#pragma unroll
+        for (int u = 0; u < N; ++u) {
+            if (b0 + u * step < mine) *before += c[u];
+            *all += c[u];
+        }
+    }
 }
 
 // Rows of the slots of the block's tile.  Each of a.warps warps owns a
@@ -655,80 +730,92 @@ template <class I>
 __global__ void __launch_bounds__(kPlanThreads)
 expert_plan_rows(const __grid_constant__ PlanArgs a) {
     extern __shared__ int32_t smem[];
-    int32_t *cnt = smem;                                   // [warps][E]
-    int32_t *base = smem + a.warps * a.E;                  // [E]
-    __shared__ int32_t warp_sums[32];
-    __shared__ int32_t end_row;
-    wait_for_previous_grid();
-    const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5;
-    for (int i = tid; i < a.warps * a.E; i += kPlanThreads) cnt[i] = 0;
+    int32_t *cnt = smem;                                   // [warps][E], then first rows
+    int32_t *all = smem + a.warps * a.E;                   // [E] counts of all blocks
+    int32_t *before = all + a.E;                           // [E] of the blocks before
+    int32_t *offset = before + a.E;                        // [E]
+    __shared__ int32_t warp_totals[32];
+    const int threads = int(blockDim.x), tid = int(threadIdx.x);
+    const int lane = tid & 31, warp = tid >> 5;
+    for (int i = tid; i < (a.warps + 2) * a.E; i += threads) smem[i] = 0;
     __syncthreads();
+    wait_for_previous_grid();
     const int part = a.tile / a.warps;                     // a multiple of 32
     const int first = int(blockIdx.x) * a.tile + warp * part;
     const int end = warp < a.warps ? min(a.slots, first + part) : first;
     int32_t *mine = cnt + warp * a.E;
-    for (int i = first + lane; i < end; i += 32) {
-        const int e = slot_expert<I>(a, i, end);
-        if (e >= 0) atomicAdd(&mine[e], 1);
+    for (int i = first + lane; i < end; i += 32 * kPlanLoads) {
+        int e[kPlanLoads];
+        slot_experts<I>(a, i, 32, end, e);
+#pragma unroll
+        for (int u = 0; u < kPlanLoads; ++u)
+            if (e[u] >= 0) atomicAdd(&mine[e[u]], 1);
+    }
+    if (a.block_counts != nullptr) {
+        // threads / E threads share an expert's blocks
+        const int shares = max(1, threads / a.E);
+        for (int i = tid; i < a.E * shares; i += threads) {
+            int some_before = 0, some = 0;
+            sum_blocks(a, i % a.E, i / a.E, shares, int(blockIdx.x), &some_before, &some);
+            atomicAdd(&before[i % a.E], some_before);
+            atomicAdd(&all[i % a.E], some);
+        }
     }
     __syncthreads();
-    // offsets of the experts, and each warp's first row of every expert
     int carry = 0;
-    for (int e0 = 0; e0 < a.E; e0 += kPlanThreads) {
+    for (int e0 = 0; e0 < a.E; e0 += threads) {
         const int e = e0 + tid;
-        int before = 0, all = 0;
+        int own = 0;
         if (e < a.E) {
-            int own = 0;
             for (int w = 0; w < a.warps; ++w) {
                 const int c = cnt[w * a.E + e];
                 cnt[w * a.E + e] = own;
                 own += c;
             }
-            all = own;
-            if (a.block_counts != nullptr) {
-                all = 0;
-                for (int b = 0; b < int(gridDim.x); ++b) {
-                    if (b == int(blockIdx.x)) before = all;
-                    all += a.block_counts[int64_t(b) * a.E + e];
-                }
-            }
+            if (a.block_counts == nullptr) all[e] = own;
+            own = all[e];
         }
         // (in 64 bits: a count next to 2^31 rounded up would not fit)
-        const int padded = int((int64_t(all) + a.align - 1) / a.align * a.align);
+        const int padded = int((int64_t(own) + a.align - 1) / a.align * a.align);
         int total;
-        const int incl = block_scan(padded, warp_sums, &total);
-        const int off = carry + incl - padded;
+        const int off = carry + block_scan(padded, warp_totals, &total) - padded;
         carry += total;
         if (e < a.E) {
-            base[e] = off + before;
+            offset[e] = off;
             if (blockIdx.x == 0) {
-                a.counts[e] = all;
+                a.counts[e] = own;
                 a.offsets[e] = off;
                 if (e == a.E - 1) a.offsets[a.E] = off + padded;
             }
-            // the gap rows behind expert e belong to no slot
-            if (e % int(gridDim.x) == int(blockIdx.x))
-                for (int r = off + all; r < off + padded; ++r) a.slot_of[r] = -1;
         }
     }
-    if (tid == 0) end_row = carry;
     __syncthreads();
-    for (int64_t r = int64_t(end_row) + int64_t(blockIdx.x) * kPlanThreads + tid; r < a.rows;
-         r += int64_t(gridDim.x) * kPlanThreads)
-        a.slot_of[r] = -1;
-    for (int i0 = first; i0 < end; i0 += 32) {             // warp-uniform
-        const int i = i0 + lane;
-        const int e = slot_expert<I>(a, i, end);
-        const uint32_t same = __match_any_sync(kAll, e);
-        const int rank = __popc(same & ((1u << lane) - 1));
-        const int at = e >= 0 ? mine[e] : 0;
-        __syncwarp();
-        if (e >= 0 && rank == 0) mine[e] = at + __popc(same);
-        __syncwarp();
-        const int row = e >= 0 ? base[e] + at + rank : -1;
-        if (i < end) a.row_of[i] = row;
-        if (row >= 0) a.slot_of[row] = i;
+    for (int i0 = first; i0 < end; i0 += 32 * kPlanLoads) {      // warp-uniform
+        int e[kPlanLoads];
+        slot_experts<I>(a, i0 + lane, 32, end, e);
+#pragma unroll
+        for (int u = 0; u < kPlanLoads; ++u) {
+            const int i = i0 + u * 32 + lane;
+            const uint32_t same = __match_any_sync(kAll, e[u]);
+            const int rank = __popc(same & ((1u << lane) - 1));
+            const int at = e[u] >= 0 ? mine[e[u]] : 0;
+            __syncwarp();
+            if (e[u] >= 0 && rank == 0) mine[e[u]] = at + __popc(same);
+            __syncwarp();
+            const int row = e[u] >= 0 ? offset[e[u]] + before[e[u]] + at + rank : -1;
+            if (i < end) a.row_of[i] = row;
+            if (row >= 0) a.slot_of[row] = i;
+        }
     }
+    // the rows that belong to no slot: behind each expert's last, and behind all
+    if (a.align > 1)
+        for (int e = int(blockIdx.x); e < a.E; e += int(gridDim.x)) {
+            const int stop = e + 1 < a.E ? offset[e + 1] : carry;
+            for (int r = offset[e] + all[e] + tid; r < stop; r += threads) a.slot_of[r] = -1;
+        }
+    for (int64_t r = int64_t(carry) + int64_t(blockIdx.x) * threads + tid; r < a.rows;
+         r += int64_t(gridDim.x) * threads)
+        a.slot_of[r] = -1;
 }
 
 }  // namespace vf

@@ -11,6 +11,7 @@
 
 #include "checks.h"
 #include "expert_kernel.cuh"
+#include "expert_q_kernel.cuh"
 #include "vf_relayout.h"
 
 namespace {
@@ -20,8 +21,8 @@ using namespace vfc;
 constexpr int64_t kMaxSlots = int64_t(1) << 30;     // T * K
 constexpr int64_t kMaxExperts = 4096;
 constexpr int64_t kMaxRows = INT32_MAX;
-constexpr int64_t kMaxGrid = int64_t(1) << 28;
-constexpr int64_t kTableBlocks = 152 * 8;
+constexpr int64_t kMaxGrid = int64_t(1) << 27;   // a grid's warps fit 31 bits
+constexpr int64_t kSMs = 152;
 
 cudaStream_t as_stream(vf_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
 
@@ -58,24 +59,24 @@ int check_routing(int64_t T, int64_t K, int64_t E, int64_t align, int64_t *rows)
     return *rows > kMaxRows ? VF_ERR_ARG : VF_OK;
 }
 
-// Blocks of the plan, the slots of each and the warps that sort.
+// Blocks of the plan, the slots of each, the warps that sort and the threads.
 struct PlanShape {
-    int64_t blocks, tile, warps;
+    int64_t blocks, tile, warps, threads;
 };
 
 constexpr int64_t kPlanCounters = 32768;               // int32 counters in shared memory
-constexpr int64_t kPlanBlocks = 152;
 constexpr int64_t kPlanOneBlock = 8192;                // slots that one block sorts by itself
 
 PlanShape plan_shape(int64_t slots, int64_t E) {
     PlanShape p;
+    p.blocks = slots <= kPlanOneBlock ? 1 : std::min(kSMs, ceil_div(slots, 2048));
     // a warp for every 32 slots, at most what the counters have room for
-    p.warps = std::min<int64_t>(32, std::max<int64_t>(1, ceil_div(slots, 32)));
+    p.warps = std::min<int64_t>(32, std::max<int64_t>(1, ceil_div(ceil_div(slots, p.blocks), 32)));
     p.warps = std::max<int64_t>(1, std::min(p.warps, kPlanCounters / E));
     const int64_t step = 32 * p.warps;
-    p.blocks = slots <= kPlanOneBlock ? 1 : std::min(kPlanBlocks, ceil_div(slots, 2048));
     p.tile = std::max<int64_t>(1, ceil_div(ceil_div(slots, p.blocks), step)) * step;
     p.blocks = std::max<int64_t>(1, ceil_div(slots, p.tile));
+    p.threads = std::max(step, std::min<int64_t>(vf::kPlanThreads, ceil_div(E, 32) * 32));
     return p;
 }
 
@@ -86,7 +87,7 @@ int launch_plan(const vf::PlanArgs &a, const PlanShape &p, cudaStream_t stream) 
                               size_t(a.E) * 4, stream, a);
         if (rc != VF_OK) return rc;
     }
-    const size_t smem = size_t(p.warps + 1) * size_t(a.E) * 4;
+    const size_t smem = size_t(p.warps + 3) * size_t(a.E) * 4;
     // above 48 KB the kernel has to be told; set on every call, so that no
     // state is kept per device
     if (smem > 48 * 1024 &&
@@ -95,7 +96,7 @@ int launch_plan(const vf::PlanArgs &a, const PlanShape &p, cudaStream_t stream) 
         cudaGetLastError();
         return VF_ERR_CUDA;
     }
-    return launch(vf::expert_plan_rows<I>, p.blocks, vf::kPlanThreads, smem, stream, a);
+    return launch(vf::expert_plan_rows<I>, p.blocks, int(p.threads), smem, stream, a);
 }
 
 // A range of `count` items of `size` bytes at p; false when it wraps.
@@ -227,93 +228,89 @@ vf::ExpertArgs make_args(const vf_expert_desc *d) {
     return a;
 }
 
-// Warps that share a token in the merge's backward pass: one per span, at most
-// the block's, a power of two.
-int token_warps(int64_t spans) {
-    int w = 1;
-    while (w < vf::kExpertWarps && w < spans) w *= 2;
-    return w;
-}
-
 using RowKernel = void (*)(vf::ExpertArgs);
 
-template <class S, int VW>
-RowKernel pack_kernel(int format) {
-    if constexpr (sizeof(S) == 2) {
-        if (format == VF_FORMAT_INT8) return vf::expert_pack_rows<S, VW, vf::kFmtInt8>;
-        if (format == VF_FORMAT_E4M3) return vf::expert_pack_rows<S, VW, vf::kFmtE4M3>;
-    }
-    return vf::expert_pack_rows<S, VW, 0>;
-}
-
-template <int VW>
-RowKernel restore_kernel(int format) {
-    return format == VF_FORMAT_INT8 ? vf::expert_restore_rows<VW, vf::kFmtInt8>
-                                    : vf::expert_restore_rows<VW, vf::kFmtE4M3>;
-}
-
-// Rows whose loads are in flight at a time.
-template <class E, int VW, int KU>
-RowKernel merge_kernel(int format) {
-    if constexpr (std::is_same_v<E, vf::Bf16>) {
-        if (format == VF_FORMAT_INT8) return vf::expert_merge_rows<E, VW, vf::kFmtInt8, 4>;
-        if (format == VF_FORMAT_E4M3) return vf::expert_merge_rows<E, VW, vf::kFmtE4M3, 4>;
-    }
-    return vf::expert_merge_rows<E, VW, 0, KU>;
-}
-
-template <class E, int VW, int KU>
-RowKernel backward_kernel(int format) {
-    if constexpr (std::is_same_v<E, vf::Bf16>) {
-        if (format == VF_FORMAT_INT8)
-            return vf::expert_merge_backward_rows<E, VW, vf::kFmtInt8, 4>;
-        if (format == VF_FORMAT_E4M3)
-            return vf::expert_merge_backward_rows<E, VW, vf::kFmtE4M3, 4>;
-    }
-    return vf::expert_merge_backward_rows<E, VW, 0, KU>;
-}
-
-// The kernel of a call for a type, unit width and format.
-template <class E, int VW>
-RowKernel pick(Call call, int format, int64_t K) {
-    constexpr bool wide = VW * sizeof(typename E::S) == 16;
-    constexpr int most = wide && sizeof(typename E::S) == 2 ? 8 : 4;
+// The kernels of expert_kernel.cuh: any unit width, checkpoints below 16 bytes.
+template <class E, int VW, int FMT>
+RowKernel row_kernel(Call call) {
     switch (call) {
-        case Call::kPack: return pack_kernel<typename E::S, VW>(format);
-        case Call::kRestore: return restore_kernel<VW>(format);
-        case Call::kMerge:
-            if constexpr (wide) {
-                if (K <= 2) return merge_kernel<E, VW, 2>(format);
-                if (K <= 4) return merge_kernel<E, VW, 4>(format);
-            }
-            return merge_kernel<E, VW, most>(format);
-        default:
-            if constexpr (wide) {
-                if (K <= 2) return backward_kernel<E, VW, 2>(format);
-                if (K <= 4) return backward_kernel<E, VW, 4>(format);
-            }
-            return backward_kernel<E, VW, most>(format);
+        case Call::kPack: return vf::expert_pack_rows<typename E::S, VW, FMT>;
+        case Call::kRestore:
+            if constexpr (FMT != 0) return vf::expert_restore_rows<VW, FMT>;
+            return nullptr;                                // refused by check_desc
+        case Call::kMerge: return vf::expert_merge_rows<E, VW, FMT>;
+        default: return vf::expert_merge_backward_rows<E, VW, FMT>;
     }
 }
 
-template <class E>
-RowKernel pick_width(Call call, int format, int vw, int64_t K) {
+template <class E, int FMT>
+RowKernel row_kernel(Call call, int vw) {
+    constexpr int widest = 16 / int(sizeof(typename E::S));
+    if constexpr (widest == 8 && FMT == 0)
+        if (vw == 8) return row_kernel<E, 8, FMT>(call);
     switch (vw) {
-        case 8:
-            if constexpr (sizeof(typename E::S) == 2) return pick<E, 8>(call, format, K);
-            return pick<E, 4>(call, format, K);
-        case 4: return pick<E, 4>(call, format, K);
-        case 2: return pick<E, 2>(call, format, K);
-        default: return pick<E, 1>(call, format, K);
+        case 4: return row_kernel<E, 4, FMT>(call);
+        case 2: return row_kernel<E, 2, FMT>(call);
+        default: return row_kernel<E, 1, FMT>(call);
     }
 }
 
-RowKernel pick_type(Call call, int type, int format, int vw, int64_t K) {
-    switch (type) {
-        case VF_TYPE_BF16: return pick_width<vf::Bf16>(call, format, vw, K);
-        case VF_TYPE_F16: return pick_width<vf::F16>(call, format, vw, K);
-        default: return pick_width<vf::F32>(call, format, vw, K);
+// The kernels of expert_q_kernel.cuh, NV vectors per lane.  Measured on GB300:
+// the pack and the restore take NV = 4 (112 + 82 us at T = 55,413, K = 2,
+// M = 2,048, INT8; NV = 2 113 + 85, NV = 1 136 + 95), the merge and its backward
+// pass NV = 2 (45 and 40 us at T = 4,096, K = 4, M = 4,096, E4M3; NV = 4 47 and
+// 43), which leaves them registers for more rows at once.
+template <int FMT, int GROUP>
+RowKernel tile_kernel(Call call) {
+    switch (call) {
+        case Call::kPack: return vf::expert_pack_tiles<FMT, 4, GROUP / 32>;
+        case Call::kRestore: return vf::expert_restore_tiles<FMT, 4, GROUP / 32>;
+        case Call::kMerge: return vf::expert_merge_tiles<FMT, 2, GROUP / 16>;
+        default: return vf::expert_merge_backward_tiles<FMT, 2, GROUP / 16>;
     }
+}
+
+int64_t tile_columns(Call call) {
+    return call == Call::kPack || call == Call::kRestore ? 1024 : 512;
+}
+
+template <int FMT>
+RowKernel tile_kernel(Call call, int64_t group) {
+    switch (group) {
+        case 32: return tile_kernel<FMT, 32>(call);
+        case 64: return tile_kernel<FMT, 64>(call);
+        case 128: return tile_kernel<FMT, 128>(call);
+        default: return tile_kernel<FMT, 256>(call);
+    }
+}
+
+RowKernel pick_kernel(const vf_expert_desc *d, Call call, int vw, bool tiles) {
+    if (tiles)
+        return d->format == VF_FORMAT_INT8 ? tile_kernel<vf::kFmtInt8>(call, d->group)
+                                           : tile_kernel<vf::kFmtE4M3>(call, d->group);
+    switch (d->format) {                                   // bfloat16 with a format
+        case VF_FORMAT_INT8: return row_kernel<vf::Bf16, vf::kFmtInt8>(call, vw);
+        case VF_FORMAT_E4M3: return row_kernel<vf::Bf16, vf::kFmtE4M3>(call, vw);
+        default: break;
+    }
+    switch (d->type) {
+        case VF_TYPE_BF16: return row_kernel<vf::Bf16, 0>(call, vw);
+        case VF_TYPE_F16: return row_kernel<vf::F16, 0>(call, vw);
+        default: return row_kernel<vf::F32, 0>(call, vw);
+    }
+}
+
+// Warps that share a token in the merge's backward pass, each with about the
+// same number of its spans.  A warp needs some 16 spans of rows (8 tiles) to hide
+// the block's start and the sum over its warps: at M = 2,048, K = 2 (16 spans)
+// one warp takes 181 us at T = 55,414, eight 264; at M = 4,096, K = 8 (128) one
+// takes 364 us at T = 16,384, eight 331.  Few tokens are spread over more warps.
+int token_warps(const vf::ExpertArgs &a, bool tiles) {
+    const int64_t spans = std::max(a.spans, 1);
+    int64_t w = std::max<int64_t>(1, spans * a.K / (tiles ? 8 : 16));
+    while (w < vf::kExpertWarps && a.T * w < kSMs * 32) w *= 2;
+    w = std::min<int64_t>(std::min<int64_t>(w, vf::kExpertWarps), spans);
+    return int(ceil_div(spans, ceil_div(spans, w)));
 }
 
 int run(const vf_expert_desc *d, Call call, vf_stream_t stream) {
@@ -360,22 +357,34 @@ int run(const vf_expert_desc *d, Call call, vf_stream_t stream) {
 
     vf::ExpertArgs a = make_args(d);
     const int vw = unit_width(d, tokens, packed, fmt, backward);
-    const RowKernel kernel = pick_type(call, d->type, d->format, vw, d->K);
-    a.token_warps = token_warps(a.spans);
-    int64_t blocks = backward ? ceil_div(a.T, vf::kExpertWarps / a.token_warps)
-                              : ceil_div(a.T * a.spans, vf::kExpertWarps);
-    // a checkpoint's blocks fill a table of scales first: few blocks, long ones
-    if (fmt && (call == Call::kMerge || call == Call::kPack))
-        blocks = std::min<int64_t>(blocks, kTableBlocks);
+    const bool tiles = fmt && vw == 8;
+    if (tiles) a.spans = int32_t(ceil_div(d->M, tile_columns(call)));
+    int64_t warps = vf::kExpertWarps, blocks;
+    if (backward) {
+        a.token_warps = token_warps(a, tiles);
+        warps -= warps % a.token_warps;
+        blocks = ceil_div(a.T, warps / a.token_warps);
+    } else {
+        blocks = ceil_div(a.T * a.spans, warps);
+    }
+    // The merge reads each token's rows from K places, and goes fastest with the
+    // resident blocks walking the tokens side by side: at T = 55,414, K = 8,
+    // M = 3,584 499 us, against 565 with a block for every 8 items and 650 with
+    // 5 blocks per SM, which do not all fit; with a checkpoint (K = 4) 442-447 in
+    // 2-3 rounds, 462 in one, 489 in short blocks.  The other calls run best in
+    // short blocks (the pack 517 us, 593 and more in rounds).
+    if (call == Call::kMerge)
+        blocks = std::min(blocks, kSMs * vf::kMergeResident * (tiles ? 2 : 1));
     blocks = std::min(blocks, kMaxGrid);
     a.row_blocks = uint32_t(blocks);
     if (a.spans > 0) {
-        a.step_tokens = int32_t(blocks * vf::kExpertWarps / a.spans);
-        a.step_spans = int32_t(blocks * vf::kExpertWarps % a.spans);
+        a.step_tokens = int32_t(blocks * warps / a.spans);
+        a.step_spans = int32_t(blocks * warps % a.spans);
     }
     const bool gaps = writes_rows && d->align > 1 && n_packed > 0;
-    return launch(kernel, blocks + (gaps ? int64_t(a.E) * vf::kGapBlocks : 0),
-                  vf::kExpertThreads, 0, as_stream(stream), a);
+    return launch(pick_kernel(d, call, vw, tiles),
+                  blocks + (gaps ? int64_t(a.E) * vf::kGapBlocks : 0), int(warps) * 32, 0,
+                  as_stream(stream), a);
 }
 
 }  // namespace
@@ -431,6 +440,7 @@ int vf_expert_plan(const void *experts, int index_bytes, const int64_t expert_st
     a.rows = int32_t(rows);
     a.tile = int32_t(p.tile);
     a.warps = int32_t(p.warps);
+    a.flat = expert_strides[1] == 1 && (expert_strides[0] == K || T <= 1);
     return index_bytes == 8 ? launch_plan<int64_t>(a, p, as_stream(stream))
                             : launch_plan<int32_t>(a, p, as_stream(stream));
 }
