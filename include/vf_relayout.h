@@ -413,7 +413,7 @@ int64_t vf_expert_workspace(int64_t T, int64_t K, int64_t E);
  * Writes row_of [T][K], slot_of [vf_expert_rows()], counts [E] and offsets
  * [E + 1], all int32 and contiguous.  With T = 0, counts and offsets are
  * written as zeros and slot_of and row_of hold nothing.
- * workspace: vf_expert_workspace() bytes, 4-byte aligned (may be NULL when 0);
+ * workspace: vf_expert_workspace() bytes, 16-byte aligned (may be NULL when 0);
  * calls that may run at the same time need one each.
  */
 int vf_expert_plan(const void *experts, int index_bytes, const int64_t expert_strides[2],

@@ -692,17 +692,16 @@ def expert_plan(experts: torch.Tensor, E: int, align: int = 1, out: ExpertPlan =
     words = lib().vf_expert_workspace(T, K, E) // 4
     if out is None:
         # one allocation: each costs more than the checks of a whole call
-        both = _new(stream, experts, (slots + rows + 2 * E + 1 + words,), torch.int32)
-        row_of, slot_of, counts, offsets, work = both.split_with_sizes(
-            (slots, rows, E, E + 1, words))
+        both = _new(stream, experts, (slots + rows + 2 * E + 1,), torch.int32)
+        row_of, slot_of, counts, offsets = both.split_with_sizes((slots, rows, E, E + 1))
         out = ExpertPlan(row_of.view(T, K), slot_of, counts, offsets, align)
-    else:
-        if _check_plan(out) != (T, K, rows, E) or out.align != align:
-            raise ValueError("out is a plan of other sizes")
-        work = _new(stream, experts, (words,), torch.int32)
+    elif _check_plan(out) != (T, K, rows, E) or out.align != align:
+        raise ValueError("out is a plan of other sizes")
+    work = _new(stream, experts, (words,), torch.int32) if words else None
     _call("vf_expert_plan", experts.data_ptr(), experts.element_size(), _strides(experts), T, K,
           E, align, out.row_of.data_ptr(), out.slot_of.data_ptr(), out.counts.data_ptr(),
-          out.offsets.data_ptr(), work.data_ptr(), _stream(stream, experts.device))
+          out.offsets.data_ptr(), None if work is None else work.data_ptr(),
+          _stream(stream, experts.device))
     return out
 
 

@@ -624,7 +624,8 @@ struct PlanArgs {
     const void *experts;          // [T][K] view
     int64_t token_stride, slot_stride;
     int32_t *row_of, *slot_of, *counts, *offsets;
-    int32_t *block_counts;        // [blocks][E], or null when there is one block
+    int32_t *block_counts;        // [blocks][counts_stride(E)], with more than one block
+    int32_t *warp_first;          // [blocks][warps][E], the same
     int32_t K, E, align, slots, rows;
     int32_t tile;                 // slots of a block, a multiple of 32 * warps
     int32_t warps;                // warps that sort; each keeps E counters
@@ -652,27 +653,70 @@ __device__ __forceinline__ void slot_experts(const PlanArgs &a, int i, int step,
     for (int u = 0; u < kPlanLoads; ++u) e[u] = v[u] >= 0 && v[u] < I(a.E) ? int(v[u]) : -1;
 }
 
-// Counts of each expert in the block's tile.
+// What a warp keeps of each expert while it ranks: how many slots it has seen,
+// and in which lanes of the current 32 slots it occurs.
+struct Seen {
+    uint32_t lanes;
+    int32_t count;
+};
+
+// The block's part of the slots that a warp sorts.
+struct PlanPart {
+    int first, end;
+
+    __device__ __forceinline__ explicit PlanPart(const PlanArgs &a) {
+        const int warp = int(threadIdx.x >> 5);
+        const int part = a.tile / a.warps;                 // a multiple of 32
+        first = int(blockIdx.x) * a.tile + warp * part;
+        end = warp < a.warps ? min(a.slots, first + part) : first;
+    }
+};
+
+// Each slot's rank among the slots of its expert in the warp's part, to row_of
+// (-1 for a dropped slot); seen[e].count ends as the part's number of e's slots.
+// Which lanes share an expert is found in shared memory: every lane sets its bit
+// (a match instruction, and ballots of each bit of the expert, were slower).
 template <class I>
-__global__ void __launch_bounds__(kPlanThreads)
-expert_plan_counts(const __grid_constant__ PlanArgs a) {
-    extern __shared__ int32_t cnt[];                       // [E]
-    const int threads = int(blockDim.x);
-    for (int e = int(threadIdx.x); e < a.E; e += threads) cnt[e] = 0;
-    __syncthreads();
-    wait_for_previous_grid();
-    const int first = int(blockIdx.x) * a.tile;
-    const int end = min(a.slots, first + a.tile);
-    for (int i = first + int(threadIdx.x); i < end; i += kPlanLoads * threads) {
+__device__ __forceinline__ void rank_slots(const PlanArgs &a, const PlanPart &p, Seen *seen) {
+    const int lane = int(threadIdx.x & 31);
+    for (int i0 = p.first; i0 < p.end; i0 += 32 * kPlanLoads) {  // warp-uniform
         int e[kPlanLoads];
-        slot_experts<I>(a, i, threads, end, e);
+        slot_experts<I>(a, i0 + lane, 32, p.end, e);
+#pragma unroll
+        for (int u = 0; u < kPlanLoads; ++u) {
+            if (i0 + u * 32 >= p.end) break;                     // warp-uniform
+            const int i = i0 + u * 32 + lane;
+            if (e[u] >= 0) atomicOr(&seen[e[u]].lanes, 1u << lane);
+            __syncwarp();
+            const Seen s = e[u] >= 0 ? seen[e[u]] : Seen{0u, 0};
+            const int rank = __popc(s.lanes & ((1u << lane) - 1));
+            __syncwarp();
+            if (e[u] >= 0 && rank == 0) seen[e[u]] = Seen{0u, s.count + __popc(s.lanes)};
+            __syncwarp();
+            if (i < p.end) a.row_of[i] = e[u] >= 0 ? s.count + rank : -1;
+        }
+    }
+}
+
+// Ranks to rows: base[e] is the first row of the part's slots of e.
+template <class I>
+__device__ __forceinline__ void place_slots(const PlanArgs &a, const PlanPart &p,
+                                            const int32_t *base) {
+    const int lane = int(threadIdx.x & 31);
+    for (int i0 = p.first + lane; i0 < p.end; i0 += 32 * kPlanLoads) {
+        int e[kPlanLoads], row[kPlanLoads];
 #pragma unroll
         for (int u = 0; u < kPlanLoads; ++u)
-            if (e[u] >= 0) atomicAdd(&cnt[e[u]], 1);
+            row[u] = i0 + u * 32 < p.end ? a.row_of[i0 + u * 32] : -1;
+        slot_experts<I>(a, i0, 32, p.end, e);
+#pragma unroll
+        for (int u = 0; u < kPlanLoads; ++u)
+            if (e[u] >= 0) {
+                row[u] += base[e[u]];
+                a.row_of[i0 + u * 32] = row[u];
+                a.slot_of[row[u]] = i0 + u * 32;
+            }
     }
-    __syncthreads();
-    for (int e = int(threadIdx.x); e < a.E; e += threads)
-        a.block_counts[int64_t(blockIdx.x) * a.E + e] = cnt[e];
 }
 
 // Inclusive prefix sum over the block's threads (whole warps); `total` gets the
@@ -701,113 +745,83 @@ __device__ __forceinline__ int block_scan(int v, int *warp_totals, int *total) {
     return v;
 }
 
-// Sums of expert e's counts over the blocks before `mine` (added to *before) and
-// over all blocks (to *all), blocks first, first + step, ...; eight loads at a
-// time.
-__device__ __forceinline__ void sum_blocks(const PlanArgs &a, int e, int first, int step,
-                                           int mine, int *before, int *all) {
-    constexpr int N = 8;
-    for (int b0 = first; b0 < int(gridDim.x); b0 += N * step) {
-        int c[N];
+// From the warps' counts of expert e to each warp's first rank; the sum.
+__device__ __forceinline__ int warp_firsts(const PlanArgs &a, Seen *seen, int e) {
+    int sum = 0;
+#pragma unroll 8
+    for (int w = 0; w < a.warps; ++w) {
+        const int c = seen[w * a.E + e].count;
+        seen[w * a.E + e].count = sum;
+        sum += c;
+    }
+    return sum;
+}
+
+// Stride of block_counts: whole 16-byte vectors.
+__host__ __device__ __forceinline__ int64_t counts_stride(int64_t E) { return (E + 3) / 4 * 4; }
+
+// Adds up every expert's counts of all blocks, and of those before this one, in
+// shared memory (both zero before).  A thread takes four experts of every
+// shares-th block.
+__device__ __forceinline__ void sum_blocks(const PlanArgs &a, int32_t *all, int32_t *before) {
+    constexpr int N = 8;                                   // loads at a time
+    const int quads = int(counts_stride(a.E) / 4), blocks = int(gridDim.x);
+    const int shares = max(1, int(blockDim.x) / quads);
+    const int4 *counts = reinterpret_cast<const int4 *>(a.block_counts);
+    for (int i = int(threadIdx.x); i < quads * shares; i += int(blockDim.x)) {
+        const int share = i / quads, q = i - share * quads;
+        int sum[4] = {}, some[4] = {};
+        for (int b0 = share; b0 < blocks; b0 += N * shares) {
+            int4 c[N];
 #pragma unroll
-        for (int u = 0; u < N; ++u) {
-            const int b = b0 + u * step;
-            c[u] = b < int(gridDim.x) ? a.block_counts[int64_t(b) * a.E + e] : 0;
+            for (int u = 0; u < N; ++u) {
+                const int b = b0 + u * shares;
+                c[u] = b < blocks ? counts[int64_t(b) * quads + q] : make_int4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int u = 0; u < N; ++u) {
+                const int v[4] = {c[u].x, c[u].y, c[u].z, c[u].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    sum[j] += v[j];
+                    if (b0 + u * shares < int(blockIdx.x)) some[j] += v[j];
+                }
+            }
         }
 #pragma unroll
-        for (int u = 0; u < N; ++u) {
-            if (b0 + u * step < mine) *before += c[u];
-            *all += c[u];
-        }
+        for (int j = 0; j < 4; ++j)
+            if (4 * q + j < a.E) {                          // the padding is not read
+                atomicAdd(&all[4 * q + j], sum[j]);
+                atomicAdd(&before[4 * q + j], some[j]);
+            }
     }
 }
 
-// Rows of the slots of the block's tile.  Each of a.warps warps owns a
-// contiguous part of the tile: it counts its experts, the counts of the warps
-// and blocks before it and the experts' offsets give its first row of every
-// expert, and a second walk in slot order hands the rows out.
-template <class I>
-__global__ void __launch_bounds__(kPlanThreads)
-expert_plan_rows(const __grid_constant__ PlanArgs a) {
-    extern __shared__ int32_t smem[];
-    int32_t *cnt = smem;                                   // [warps][E], then first rows
-    int32_t *all = smem + a.warps * a.E;                   // [E] counts of all blocks
-    int32_t *before = all + a.E;                           // [E] of the blocks before
-    int32_t *offset = before + a.E;                        // [E]
+// Offsets of the experts from their counts (both in shared memory; block 0 also
+// writes them out), then -1 for the rows that belong to no slot.
+__device__ __forceinline__ void offsets_and_gaps(const PlanArgs &a, const int32_t *all,
+                                                 int32_t *offset) {
     __shared__ int32_t warp_totals[32];
     const int threads = int(blockDim.x), tid = int(threadIdx.x);
-    const int lane = tid & 31, warp = tid >> 5;
-    for (int i = tid; i < (a.warps + 2) * a.E; i += threads) smem[i] = 0;
-    __syncthreads();
-    wait_for_previous_grid();
-    const int part = a.tile / a.warps;                     // a multiple of 32
-    const int first = int(blockIdx.x) * a.tile + warp * part;
-    const int end = warp < a.warps ? min(a.slots, first + part) : first;
-    int32_t *mine = cnt + warp * a.E;
-    for (int i = first + lane; i < end; i += 32 * kPlanLoads) {
-        int e[kPlanLoads];
-        slot_experts<I>(a, i, 32, end, e);
-#pragma unroll
-        for (int u = 0; u < kPlanLoads; ++u)
-            if (e[u] >= 0) atomicAdd(&mine[e[u]], 1);
-    }
-    if (a.block_counts != nullptr) {
-        // threads / E threads share an expert's blocks
-        const int shares = max(1, threads / a.E);
-        for (int i = tid; i < a.E * shares; i += threads) {
-            int some_before = 0, some = 0;
-            sum_blocks(a, i % a.E, i / a.E, shares, int(blockIdx.x), &some_before, &some);
-            atomicAdd(&before[i % a.E], some_before);
-            atomicAdd(&all[i % a.E], some);
-        }
-    }
-    __syncthreads();
     int carry = 0;
     for (int e0 = 0; e0 < a.E; e0 += threads) {
         const int e = e0 + tid;
-        int own = 0;
-        if (e < a.E) {
-            for (int w = 0; w < a.warps; ++w) {
-                const int c = cnt[w * a.E + e];
-                cnt[w * a.E + e] = own;
-                own += c;
-            }
-            if (a.block_counts == nullptr) all[e] = own;
-            own = all[e];
-        }
+        const int count = e < a.E ? all[e] : 0;
         // (in 64 bits: a count next to 2^31 rounded up would not fit)
-        const int padded = int((int64_t(own) + a.align - 1) / a.align * a.align);
+        const int padded = int((int64_t(count) + a.align - 1) / a.align * a.align);
         int total;
         const int off = carry + block_scan(padded, warp_totals, &total) - padded;
         carry += total;
         if (e < a.E) {
             offset[e] = off;
             if (blockIdx.x == 0) {
-                a.counts[e] = own;
+                a.counts[e] = count;
                 a.offsets[e] = off;
                 if (e == a.E - 1) a.offsets[a.E] = off + padded;
             }
         }
     }
     __syncthreads();
-    for (int i0 = first; i0 < end; i0 += 32 * kPlanLoads) {      // warp-uniform
-        int e[kPlanLoads];
-        slot_experts<I>(a, i0 + lane, 32, end, e);
-#pragma unroll
-        for (int u = 0; u < kPlanLoads; ++u) {
-            const int i = i0 + u * 32 + lane;
-            const uint32_t same = __match_any_sync(kAll, e[u]);
-            const int rank = __popc(same & ((1u << lane) - 1));
-            const int at = e[u] >= 0 ? mine[e[u]] : 0;
-            __syncwarp();
-            if (e[u] >= 0 && rank == 0) mine[e[u]] = at + __popc(same);
-            __syncwarp();
-            const int row = e[u] >= 0 ? offset[e[u]] + before[e[u]] + at + rank : -1;
-            if (i < end) a.row_of[i] = row;
-            if (row >= 0) a.slot_of[row] = i;
-        }
-    }
-    // the rows that belong to no slot: behind each expert's last, and behind all
     if (a.align > 1)
         for (int e = int(blockIdx.x); e < a.E; e += int(gridDim.x)) {
             const int stop = e + 1 < a.E ? offset[e + 1] : carry;
@@ -816,6 +830,96 @@ expert_plan_rows(const __grid_constant__ PlanArgs a) {
     for (int64_t r = int64_t(carry) + int64_t(blockIdx.x) * threads + tid; r < a.rows;
          r += int64_t(gridDim.x) * threads)
         a.slot_of[r] = -1;
+}
+
+// Fills `n` counters of a warp's experts with zeros.
+__device__ __forceinline__ void zero_seen(Seen *seen, int n) {
+    for (int i = int(threadIdx.x); i < n; i += int(blockDim.x)) seen[i] = Seen{0u, 0};
+}
+
+// The plan by one block.  Each of a.warps warps ranks a contiguous part of the
+// slots; a prefix sum over the warps and over the experts makes rows of ranks.
+template <class I>
+__global__ void __launch_bounds__(kPlanThreads)
+expert_plan_one(const __grid_constant__ PlanArgs a) {
+    extern __shared__ int2 smem[];
+    Seen *seen = reinterpret_cast<Seen *>(smem);           // [warps][E]
+    int32_t *base = reinterpret_cast<int32_t *>(smem);     // the same, first rows
+    int32_t *all = base + 2 * a.warps * a.E;               // [E]
+    int32_t *offset = all + a.E;                           // [E]
+    const int threads = int(blockDim.x), lane = int(threadIdx.x & 31);
+    const int warp = int(threadIdx.x >> 5);
+    zero_seen(seen, a.warps * a.E);
+    __syncthreads();
+    wait_for_previous_grid();
+    const PlanPart p(a);
+    rank_slots<I>(a, p, seen + warp * a.E);
+    __syncthreads();
+    for (int e = int(threadIdx.x); e < a.E; e += threads) all[e] = warp_firsts(a, seen, e);
+    __syncthreads();
+    offsets_and_gaps(a, all, offset);
+    if (warp < a.warps) {
+        // a warp's own first ranks become first rows, over the first half of its
+        // counters
+        Seen *mine = seen + warp * a.E;
+        int32_t *rows = reinterpret_cast<int32_t *>(mine);
+        for (int e0 = 0; e0 < a.E; e0 += 32) {
+            const int e = e0 + lane;
+            const int row = e < a.E ? mine[e].count + offset[e] : 0;
+            __syncwarp();
+            if (e < a.E) rows[e] = row;
+            __syncwarp();
+        }
+        place_slots<I>(a, p, rows);
+    }
+}
+
+// The plan by many blocks, in two grids.  The first ranks the slots within each
+// warp's part of its block's tile ...
+template <class I>
+__global__ void __launch_bounds__(kPlanThreads)
+expert_plan_rank(const __grid_constant__ PlanArgs a) {
+    extern __shared__ int2 smem[];
+    Seen *seen = reinterpret_cast<Seen *>(smem);           // [warps][E]
+    const int threads = int(blockDim.x), tid = int(threadIdx.x);
+    zero_seen(seen, a.warps * a.E);
+    __syncthreads();
+    wait_for_previous_grid();
+    const PlanPart p(a);
+    rank_slots<I>(a, p, seen + (tid >> 5) * a.E);
+    __syncthreads();
+    int32_t *counts = a.block_counts + int64_t(blockIdx.x) * counts_stride(a.E);
+    for (int e = tid; e < a.E; e += threads) counts[e] = warp_firsts(a, seen, e);
+    __syncthreads();
+    int32_t *out = a.warp_first + int64_t(blockIdx.x) * a.warps * a.E;
+    for (int i = tid; i < a.warps * a.E; i += threads) out[i] = seen[i].count;
+}
+
+// ... and the second adds what lies before: each block sums the counts of all
+// blocks by itself (152 x E numbers from L2, which is cheaper than a third grid).
+template <class I>
+__global__ void __launch_bounds__(kPlanThreads)
+expert_plan_place(const __grid_constant__ PlanArgs a) {
+    extern __shared__ int2 smem[];
+    int32_t *base = reinterpret_cast<int32_t *>(smem);     // [warps][E]
+    int32_t *all = base + a.warps * a.E;                   // [E] counts of all blocks
+    int32_t *offset = all + a.E;                           // [E]
+    int32_t *before = offset + a.E;                        // [E] of the blocks before
+    const int threads = int(blockDim.x), lane = int(threadIdx.x & 31);
+    const int warp = int(threadIdx.x >> 5);
+    for (int e = int(threadIdx.x); e < a.E; e += threads) all[e] = before[e] = 0;
+    __syncthreads();
+    wait_for_previous_grid();
+    sum_blocks(a, all, before);
+    __syncthreads();
+    offsets_and_gaps(a, all, offset);
+    if (warp < a.warps) {
+        int32_t *rows = base + warp * a.E;
+        const int32_t *firsts = a.warp_first + (int64_t(blockIdx.x) * a.warps + warp) * a.E;
+        for (int e = lane; e < a.E; e += 32) rows[e] = firsts[e] + offset[e] + before[e];
+        __syncwarp();
+        place_slots<I>(a, PlanPart(a), rows);
+    }
 }
 
 }  // namespace vf

@@ -64,7 +64,7 @@ struct PlanShape {
     int64_t blocks, tile, warps, threads;
 };
 
-constexpr int64_t kPlanCounters = 32768;               // int32 counters in shared memory
+constexpr int64_t kPlanCounters = 24576;               // 8-byte counters in shared memory
 constexpr int64_t kPlanOneBlock = 8192;                // slots that one block sorts by itself
 
 PlanShape plan_shape(int64_t slots, int64_t E) {
@@ -80,23 +80,32 @@ PlanShape plan_shape(int64_t slots, int64_t E) {
     return p;
 }
 
-template <class I>
-int launch_plan(const vf::PlanArgs &a, const PlanShape &p, cudaStream_t stream) {
-    if (p.blocks > 1) {
-        const int rc = launch(vf::expert_plan_counts<I>, p.blocks, vf::kPlanThreads,
-                              size_t(a.E) * 4, stream, a);
-        if (rc != VF_OK) return rc;
-    }
-    const size_t smem = size_t(p.warps + 3) * size_t(a.E) * 4;
-    // above 48 KB the kernel has to be told; set on every call, so that no
-    // state is kept per device
-    if (smem > 48 * 1024 &&
-        cudaFuncSetAttribute(vf::expert_plan_rows<I>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+// int32 numbers of workspace: the blocks' counts and their warps' first ranks.
+int64_t plan_workspace(const PlanShape &p, int64_t E) {
+    return p.blocks > 1 ? p.blocks * (p.warps * E + vf::counts_stride(E)) : 0;
+}
+
+int launch_plan_kernel(void (*kernel)(vf::PlanArgs), const vf::PlanArgs &a, const PlanShape &p,
+                       int64_t arrays, cudaStream_t stream) {
+    const size_t smem = size_t(arrays) * size_t(a.E) * 4;
+    // above 48 KB, the kernel's own arrays included, it has to be told; set on
+    // every call, so that no state is kept per device
+    if (smem > 47 * 1024 &&
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              int(smem)) != cudaSuccess) {
         cudaGetLastError();
         return VF_ERR_CUDA;
     }
-    return launch(vf::expert_plan_rows<I>, p.blocks, int(p.threads), smem, stream, a);
+    return launch(kernel, p.blocks, int(p.threads), smem, stream, a);
+}
+
+template <class I>
+int launch_plan(const vf::PlanArgs &a, const PlanShape &p, cudaStream_t stream) {
+    if (p.blocks == 1)
+        return launch_plan_kernel(vf::expert_plan_one<I>, a, p, 2 * p.warps + 2, stream);
+    const int rc = launch_plan_kernel(vf::expert_plan_rank<I>, a, p, 2 * p.warps, stream);
+    return rc != VF_OK ? rc : launch_plan_kernel(vf::expert_plan_place<I>, a, p, p.warps + 3,
+                                                 stream);
 }
 
 // A range of `count` items of `size` bytes at p; false when it wraps.
@@ -402,7 +411,7 @@ int64_t vf_expert_workspace(int64_t T, int64_t K, int64_t E) {
     const int rc = check_routing(T, K, E, 1, &rows);
     if (rc != VF_OK) return rc;
     const PlanShape p = plan_shape(T * K, E);
-    return p.blocks > 1 ? p.blocks * E * 4 : 0;
+    return plan_workspace(p, E) * 4;
 }
 
 int vf_expert_plan(const void *experts, int index_bytes, const int64_t expert_strides[2],
@@ -420,7 +429,9 @@ int vf_expert_plan(const void *experts, int index_bytes, const int64_t expert_st
     rs.add(slot_of, rows, 4, true);
     rs.add(counts, E, 4, true);
     rs.add(offsets, E + 1, 4, true);
-    if (p.blocks > 1) rs.add(workspace, p.blocks * E, 4, true);
+    const int64_t words = plan_workspace(p, E);
+    rs.add(workspace, words, 4, true);
+    if (words > 0 && reinterpret_cast<uintptr_t>(workspace) % 16) return VF_ERR_ARG;
     if ((rc = rs.check()) != VF_OK) return rc;
 
     vf::PlanArgs a;
@@ -432,7 +443,8 @@ int vf_expert_plan(const void *experts, int index_bytes, const int64_t expert_st
     a.slot_of = slot_of;
     a.counts = counts;
     a.offsets = offsets;
-    a.block_counts = p.blocks > 1 ? static_cast<int32_t *>(workspace) : nullptr;
+    a.block_counts = static_cast<int32_t *>(workspace);
+    if (p.blocks > 1) a.warp_first = a.block_counts + p.blocks * vf::counts_stride(E);
     a.K = int32_t(K);
     a.E = int32_t(E);
     a.align = int32_t(align);
