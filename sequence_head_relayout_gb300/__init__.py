@@ -590,7 +590,7 @@ def _new(stream, like, shape, dtype):
     if like.device.type != "cuda":
         return torch.empty(shape, dtype=dtype, pin_memory=True)
     if stream is None:
-        return like.new_empty(shape, dtype=dtype)
+        return torch.empty(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=like.device)
 
@@ -687,14 +687,14 @@ def expert_plan(experts: torch.Tensor, E: int, align: int = 1, out: ExpertPlan =
     if experts.dtype not in (torch.int32, torch.int64) or experts.dim() != 2:
         raise ValueError("experts must be an int32 or int64 view of shape [T,K]")
     T, K = experts.shape
-    slots = T * K
     rows = expert_rows(T, K, E, align)
     words = lib().vf_expert_workspace(T, K, E) // 4
     if out is None:
-        # one allocation: each costs more than the checks of a whole call
-        both = _new(stream, experts, (slots + rows + 2 * E + 1,), torch.int32)
-        row_of, slot_of, counts, offsets = both.split_with_sizes((slots, rows, E, E + 1))
-        out = ExpertPlan(row_of.view(T, K), slot_of, counts, offsets, align)
+        # (views of one allocation take longer to make than four allocations)
+        out = ExpertPlan(_new(stream, experts, (T, K), torch.int32),
+                         _new(stream, experts, (rows,), torch.int32),
+                         _new(stream, experts, (E,), torch.int32),
+                         _new(stream, experts, (E + 1,), torch.int32), align)
     elif _check_plan(out) != (T, K, rows, E) or out.align != align:
         raise ValueError("out is a plan of other sizes")
     work = _new(stream, experts, (words,), torch.int32) if words else None
