@@ -156,18 +156,43 @@ template <int VW>
 __device__ __forceinline__ int unit_col(int u, int lane) { return u * 32 * VW + lane * VW; }
 
 // The lane's units of a row's span; units past the row's end, and all of them
-// where `there` is false, are zeros.
-template <class S, int VW>
+// where `there` is false, are zeros.  Small units are loaded from a
+// column clamped into the row (and from row 0 where there is none: the caller
+// sees to it that a row exists) and zeroed afterwards: with a condition each, the
+// loads of a span waited for one another (the merge of 20,000 tokens, K = 4,
+// M = 2,049 took 662 us, 186 so).  kClampBelow: the unit size from which on the
+// loads are predicated instead.
+template <class S, int VW, int kClampBelow = 16>
 __device__ __forceinline__ Lane8<S> load_span(const void *base, int64_t offset, int64_t stride,
                                               int col0, int M, int lane,
                                               bool there = true) {
-    const S *row = static_cast<const S *>(base) + offset;
-    Lane8<S> v = {};
+    using B = typename UnitBits<int(sizeof(S)) * VW>::T;
+    constexpr int U = 8 / VW;
+    B b[U] = {};
+    if constexpr (sizeof(B) >= kClampBelow) {
+        const S *row = static_cast<const S *>(base) + offset;
 #pragma unroll
-    for (int u = 0; u < 8 / VW; ++u) {
-        const int c = col0 + unit_col<VW>(u, lane);
-        if (there && c < M)
-            load_unit<S, VW>(row + int64_t(c) * stride, reinterpret_cast<S *>(v.w) + u * VW);
+        for (int u = 0; u < U; ++u) {
+            const int c = col0 + unit_col<VW>(u, lane);
+            if (there && c < M) b[u] = *reinterpret_cast<const B *>(row + int64_t(c) * stride);
+        }
+    } else {
+        const S *row = static_cast<const S *>(base) + (there ? offset : 0);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int c = min(col0 + unit_col<VW>(u, lane), M - VW);
+            b[u] = *reinterpret_cast<const B *>(row + int64_t(c) * stride);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (!there || col0 + unit_col<VW>(u, lane) >= M) b[u] = B{};
+    }
+    Lane8<S> v;
+    if constexpr (sizeof(B) >= 4) {
+        memcpy(v.w, b, sizeof(v.w));
+    } else {
+#pragma unroll
+        for (int i = 0; i < kWords<S>; ++i) v.w[i] = uint32_t(b[2 * i]) | uint32_t(b[2 * i + 1]) << 16;
     }
     return v;
 }
@@ -298,44 +323,63 @@ __device__ __forceinline__ void checkpoint_span(const ExpertArgs &a, const Scale
     static_assert(VW < 8, "expert_q_kernel.cuh has the form for 16-byte accesses");
     constexpr int U = 8 / VW;
     const int lanes = min(32, (1 << a.group_log2) / VW);        // of a unit that share a group
+    const int units = max(1, (1 << a.group_log2) / (32 * VW));  // that share a group
     const uint16_t *h = reinterpret_cast<const uint16_t *>(v.w);
     uint32_t m[U];
+    float inv[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         m[u] = 0;
 #pragma unroll
         for (int i = 0; i < VW; ++i) m[u] = max(m[u], uint32_t(h[u * VW + i]) & 0x7FFFu);
-        for (int o = lanes >> 1; o > 0; o >>= 1) m[u] = max(m[u], __shfl_xor_sync(kAll, m[u], o));
+    }
+    // over the units that share a group, then over the lanes, once per group
+#pragma unroll
+    for (int o = 1; o < U; o <<= 1)
+        if (o < units) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (!(u & o)) m[u] = m[u | o] = max(m[u], m[u | o]);
+        }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        if ((u & (units - 1)) == 0) {
+            for (int o = lanes >> 1; o > 0; o >>= 1)
+                m[u] = max(m[u], __shfl_xor_sync(kAll, m[u], o));
+            inv[u] = group_inverse(tab, m[u]);
+        } else {                                                // as its group's first unit
+            m[u] = m[u & (u - 1)];
+            inv[u] = inv[u & (u - 1)];
+        }
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int c = col0 + unit_col<VW>(u, lane);
-        uint32_t top_mag = m[u];                                // over the units that share it
-#pragma unroll
-        for (int w = 0; w < U; ++w)
-            if ((w * 32 * VW) >> a.group_log2 == (u * 32 * VW) >> a.group_log2)
-                top_mag = max(top_mag, m[w]);
         if (c >= a.M) continue;
         if ((c & ((1 << a.group_log2) - 1)) == 0)
-            a.scales[row * a.groups + (c >> a.group_log2)] = group_scale(tab, top_mag);
+            a.scales[row * a.groups + (c >> a.group_log2)] = group_scale(tab, m[u]);
         uint16_t x[VW];
         uint8_t code[VW];
 #pragma unroll
         for (int i = 0; i < VW; ++i) x[i] = h[u * VW + i];
-        encode<VW, FMT>(x, group_inverse(tab, top_mag), live_group(top_mag), code);
+        encode<VW, FMT>(x, inv[u], live_group(m[u]), code);
         store_unit<uint8_t, VW>(a.codes + row * a.M + c, code);
     }
 }
 
-// The lane's codes of a span of a checkpointed row and the scales of its units
-// (NaN where a stored scale is not finite); zeros where there are none.
+// The lane's codes of a span of a checkpointed row and the scales of its units;
+// zeros where there are none (loads as in load_span).
 template <int VW> struct KeptLane {
-    uint8_t code[8];
+    typename UnitBits<VW>::T code[8 / VW];
     float scale[8 / VW];
 
     __device__ __forceinline__ uint2 words() const {
-        uint2 w;
-        memcpy(&w, code, 8);
+        uint2 w = make_uint2(0, 0);
+#pragma unroll
+        for (int u = 0; u < 8 / VW; ++u) {
+            const uint32_t x = uint32_t(code[u]) << (8 * (u * VW % 4));
+            (u * VW < 4 ? w.x : w.y) |= x;
+        }
         return w;
     }
 };
@@ -343,15 +387,22 @@ template <int VW> struct KeptLane {
 template <int VW>
 __device__ __forceinline__ KeptLane<VW> load_kept(const ExpertArgs &a, int64_t row, int col0,
                                                   int lane, bool there = true) {
-    KeptLane<VW> q = {};
+    using B = typename UnitBits<VW>::T;
+    constexpr int U = 8 / VW;
+    KeptLane<VW> q;
+    if (!there) row = 0;
 #pragma unroll
-    for (int u = 0; u < 8 / VW; ++u) {
-        const int c = col0 + unit_col<VW>(u, lane);
-        if (there && c < a.M) {
-            load_unit<uint8_t, VW>(a.codes + row * a.M + c, q.code + u * VW);
-            q.scale[u] = a.scales[row * a.groups + (c >> a.group_log2)];
-        }
+    for (int u = 0; u < U; ++u) {
+        const int c = min(col0 + unit_col<VW>(u, lane), a.M - VW);
+        q.code[u] = *reinterpret_cast<const B *>(a.codes + row * a.M + c);
+        q.scale[u] = a.scales[row * a.groups + (c >> a.group_log2)];
     }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (!there || col0 + unit_col<VW>(u, lane) >= a.M) {
+            q.code[u] = B(0);
+            q.scale[u] = 0.0f;
+        }
     return q;
 }
 
@@ -472,8 +523,10 @@ expert_merge_rows(const __grid_constant__ ExpertArgs a) {
 #pragma unroll
             for (int j = 0; j < KU; ++j) {
                 r[j] = __shfl_sync(kAll, slots.row, k0 % 32 + j);
-                v[j] = load_span<S, VW>(a.packed, int64_t(r[j]) * a.M, 1, col0, a.M, lane,
-                                        r[j] >= 0);
+                // (8-byte units at M = 2,052: 75 us predicated, 109 clamped; with a
+                // checkpoint 325 and 295)
+                v[j] = load_span<S, VW, FMT ? 16 : 8>(a.packed, int64_t(r[j]) * a.M, 1, col0,
+                                                      a.M, lane, r[j] >= 0);
             }
 #pragma unroll
             for (int j = 0; j < KU; ++j) {
@@ -548,7 +601,9 @@ expert_merge_backward_rows(const __grid_constant__ ExpertArgs a) {
         for (int k0 = 0; k0 < a.K; k0 += KU) {
             const Slots slots(a, t, k0, lane, true);
             float2 dots[KU] = {};                                // of even and odd columns
-            for (int s = t < a.T ? part : a.spans; s < a.spans; s += a.token_warps) {
+            // (with no packed rows at all, every slot is dropped)
+            for (int s = t < a.T && a.rows > 0 ? part : a.spans; s < a.spans;
+                 s += a.token_warps) {
                 const int col0 = s * kSpan;
                 const Lane8<S> gv = load_span<S, VW>(a.tokens, t * a.token_stride, a.col_stride,
                                                      col0, a.M, lane);
@@ -822,7 +877,8 @@ __device__ __forceinline__ void offsets_and_gaps(const PlanArgs &a, const int32_
     if (a.align > 1)
         for (int e = int(blockIdx.x); e < a.E; e += int(gridDim.x)) {
             const int stop = e + 1 < a.E ? offset[e + 1] : carry;
-            for (int r = offset[e] + all[e] + tid; r < stop; r += threads) a.slot_of[r] = -1;
+            for (int64_t r = int64_t(offset[e]) + all[e] + tid; r < stop; r += threads)
+                a.slot_of[r] = -1;
         }
     for (int64_t r = int64_t(carry) + int64_t(blockIdx.x) * threads + tid; r < a.rows;
          r += int64_t(gridDim.x) * threads)

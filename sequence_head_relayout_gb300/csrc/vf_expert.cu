@@ -367,6 +367,7 @@ int run(const vf_expert_desc *d, Call call, vf_stream_t stream) {
     if ((rc = rs.check()) != VF_OK) return rc;
 
     vf::ExpertArgs a = make_args(d);
+    if (call == Call::kMerge && a.rows == 0) a.K = 0;      // no rows: every slot is dropped
     const int vw = unit_width(d, tokens, packed, fmt, backward);
     const bool tiles = fmt && vw == 8;
     if (tiles) a.spans = int32_t(ceil_div(d->M, tile_columns(call)));

@@ -453,6 +453,38 @@ def test_merge_q_and_backward(M, group, fmt):
         within(torch.where(fits.to(DEV), gw, 0), torch.where(fits, gw_want, 0), b2)
 
 
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("M", [100, 101, 256])
+def test_checkpoints_from_elsewhere(M, fmt):
+    """Any code and scale bits: scales of zero, infinity and NaN, every code (but
+    E4M3's NaN, whose payload is unspecified)."""
+    T, K, E, group = 30, 2, 4, 32
+    plan = make_plan(routing(T, K, E, 1, "all"), E)
+    n, groups = plan.slot_of.numel(), -(-M // group)
+    g = gen(M)
+    codes = torch.randint(0, 256, (n, M), generator=g).to(torch.uint8)
+    if fmt == "e4m3":
+        codes[(codes & 0x7F) == 0x7F] = 0
+    scales = torch.randn(n, groups, generator=g).abs() * 2.0 ** torch.randint(
+        -40, 40, (n, groups), generator=g)
+    scales[::5], scales[1::7], scales[2::9] = 0, float("inf"), float("nan")
+    code_type = torch.int8 if fmt == "int8" else torch.float8_e4m3fn
+    dc, ds = codes.view(code_type).to(DEV), scales.to(DEV)
+    got = vf.expert_restore_q(dc[:T].contiguous(), ds[:T].contiguous(), plan, fmt, group)
+    rows = X.restore(codes[:T], scales[:T], FMT[fmt], group)
+    token = (plan.slot_of // K).long().cpu()
+    assert torch.equal(got.cpu().view(torch.int16), rows[token].view(torch.int16))
+    grad, w = rows_like(T, M, BF16, 2), weights_for(T, K, 3)
+    values = X.values(codes, scales, FMT[fmt], group)
+    before = torch.zeros(n, M, dtype=BF16)
+    want, gw_want, mag = X.merge_backward(grad, values, plan.row_of.cpu(), plan.offsets.cpu(), w,
+                                          before)
+    gp, gw = vf.expert_merge_backward_q(grad.to(DEV), dc, ds, plan, w.to(DEV), fmt, group)
+    b1, b2 = backward_bounds(want, grad, mag, BF16, M, extra=1)
+    within(gp, want, b1)
+    within(gw, gw_want, b2)
+
+
 def test_merge_q_leaves_unowned_rows():
     plan = make_plan(torch.tensor([[0, -1], [1, 0]]), 2, 4)
     n, M = plan.slot_of.numel(), 96
