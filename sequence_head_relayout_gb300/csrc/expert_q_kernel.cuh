@@ -255,6 +255,12 @@ expert_merge_backward_tiles(const __grid_constant__ ExpertArgs a) {
                     r[j] = __shfl_sync(kAll, slots.row, j);
                     scale[j] = load_codes<NV, L>(a, r[j], s, lane, c, r[j] >= 0, q[j]);
                 }
+#pragma unroll
+                for (int j = 0; j < KU; ++j) {
+#pragma unroll
+                    for (int i = 0; i < NV; ++i) loaded(q[j][i]);
+                    loaded(scale[j]);
+                }
                 float g[NV][8];
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
@@ -269,13 +275,15 @@ expert_merge_backward_tiles(const __grid_constant__ ExpertArgs a) {
                     if (r[j] < 0) continue;                      // warp-uniform
                     uint16_t *out = static_cast<uint16_t *>(a.grad_packed) +
                                     int64_t(r[j]) * a.M + c;
-                    float sum = 0.0f;                            // of the codes; the scale once
+                    float2 sum = make_float2(0.0f, 0.0f);        // of the codes; the scale once
 #pragma unroll
                     for (int i = 0; i < NV; ++i) {
                         float y[8], d[8];
                         code_values<FMT>(q[j][i], y);
 #pragma unroll
-                        for (int p = 0; p < 8; ++p) sum = __fmaf_rn(g[i][p], y[p], sum);
+                        for (int p = 0; p < 8; p += 2)
+                            sum = fma2_rn(make_float2(g[i][p], g[i][p + 1]),
+                                          make_float2(y[p], y[p + 1]), sum);
 #pragma unroll
                         for (int p = 0; p < 8; ++p) d[p] = __fmul_rn(w, g[i][p]);
                         if (c + i * Tile<NV, L>::kStep < a.M)
@@ -283,7 +291,7 @@ expert_merge_backward_tiles(const __grid_constant__ ExpertArgs a) {
                                 make_uint4(Bf16::round(d), Bf16::round(d + 2),
                                            Bf16::round(d + 4), Bf16::round(d + 6));
                     }
-                    dot[j] = __fmaf_rn(finite_or_nan(scale[j]), sum, dot[j]);
+                    dot[j] = __fmaf_rn(finite_or_nan(scale[j]), sum.x + sum.y, dot[j]);
                 }
             }
             const float sum = warp_sums<KU>(dot, lane);

@@ -311,16 +311,19 @@ RowKernel pick_kernel(const vf_expert_desc *d, Call call, int vw, bool tiles) {
     }
 }
 
-// Warps that share a token in the merge's backward pass, each with about the
-// same number of its spans.  A warp needs some 16 spans of rows (8 tiles) to hide
-// the block's start and the sum over its warps: at M = 2,048, K = 2 (16 spans)
-// one warp takes 181 us at T = 55,414, eight 264; at M = 4,096, K = 8 (128) one
-// takes 364 us at T = 16,384, eight 331.  Few tokens are spread over more warps.
+// Warps that share a token in the merge's backward pass.  A warp needs some 16
+// spans of rows (8 tiles) to hide the block's start and the sum over its warps:
+// at M = 2,048, K = 2 (16 spans) one warp takes 181 us at T = 55,414, eight 264;
+// at M = 4,096, K = 8 (128) one takes 364 us at T = 16,384, eight 331.  They get
+// the same number of spans, or nearly: with a checkpoint at M = 3,584, K = 4
+// (7 tiles) one warp takes 475 us, three 540.  Few tokens are spread over more
+// warps, even or not.
 int token_warps(const vf::ExpertArgs &a, bool tiles) {
     const int64_t spans = std::max(a.spans, 1);
-    int64_t w = std::max<int64_t>(1, spans * a.K / (tiles ? 8 : 16));
-    while (w < vf::kExpertWarps && a.T * w < kSMs * 32) w *= 2;
-    w = std::min<int64_t>(std::min<int64_t>(w, vf::kExpertWarps), spans);
+    int64_t w = std::min<int64_t>({spans * a.K / (tiles ? 8 : 16), spans, vf::kExpertWarps});
+    while (w > 1 && 10 * spans < 9 * w * ceil_div(spans, w)) --w;
+    w = std::max<int64_t>(w, 1);
+    while (w < vf::kExpertWarps && w < spans && a.T * w < kSMs * 32) ++w;
     return int(ceil_div(spans, ceil_div(spans, w)));
 }
 
