@@ -375,8 +375,8 @@ int64_t vf_scale_count(int op, int64_t T, int64_t H, int64_t D, int64_t P, int64
  *
  * Tokens are [T][M] views with any non-negative element strides (row, column);
  * a view that is written must not overlap itself.  Element types: vf_type.
- * Arithmetic is in float32, each output rounded once, to nearest even; sums
- * run over k in order, so results do not depend on the launch.
+ * Arithmetic is in float32, each output rounded once, to nearest even; every sum
+ * has a fixed order (over k from 0 up), so equal calls give equal bits.
  * Rows named by row_of outside [0, rows) are treated as dropped, so no
  * content of a plan makes a kernel read or write out of bounds; a plan that
  * names a row twice gives unspecified rows.

@@ -12,7 +12,13 @@
 // All of the row kernels are bound by HBM: they move whole rows and do a few
 // operations per element.  They walk the token side, so a token row is read
 // (or written) once, whatever K is, and every packed row is read (or written)
-// once as a whole; the row index is one 4-byte load per slot.
+// once as a whole; the row index is one 4-byte load per slot.  Measured on GB300
+// (bf16, device time, bytes that cannot be avoided over it):
+//   pack            T = 55,414, K = 8, M = 3,584   516 us   6.71 TB/s
+//   merge           the same                       498 us   6.96 TB/s
+//   merge backward  T = 4,096, K = 8, M = 4,096     85 us   6.53 TB/s
+//   plan            1.6 M slots, 256 experts        23 us   bound by latency: two
+//                   grids, each a walk of some 300 slots per warp in slot order
 //
 // Work split: a warp takes one span, kSpan consecutive columns of one token.
 // A lane holds 8 columns of it as 8 / VW units of VW elements; unit u of lane
@@ -106,13 +112,6 @@ template <> struct UnitBits<2> { using T = uint16_t; };
 template <> struct UnitBits<1> { using T = uint8_t; };
 
 template <class S, int VW>
-__device__ __forceinline__ void load_unit(const S *p, S *v) {
-    using B = typename UnitBits<int(sizeof(S)) * VW>::T;
-    const B b = *reinterpret_cast<const B *>(p);
-    memcpy(v, &b, sizeof(b));
-}
-
-template <class S, int VW>
 __device__ __forceinline__ void store_unit(S *p, const S *v) {
     using B = typename UnitBits<int(sizeof(S)) * VW>::T;
     B b;
@@ -179,7 +178,7 @@ __device__ __forceinline__ int unit_col(int u, int lane) { return u * 32 * VW + 
 // column clamped into the row (and from row 0 where there is none: the caller
 // sees to it that a row exists) and zeroed afterwards: with a condition each, the
 // loads of a span waited for one another (the merge of 20,000 tokens, K = 4,
-// M = 2,049 took 662 us, 186 so).  kClampBelow: the unit size from which on the
+// M = 2,049 took 662 us, 154 so).  kClampBelow: the unit size from which on the
 // loads are predicated instead.
 template <class S, int VW, int kClampBelow = 16>
 __device__ __forceinline__ Lane8<S> load_span(const void *base, int64_t offset, int64_t stride,
@@ -520,9 +519,13 @@ expert_restore_rows(const __grid_constant__ ExpertArgs a) {
 }
 
 // Merge; FMT != 0 also keeps the packed rows' checkpoint (a row belongs to one
-// slot, so it is read once).  Walks (token, span).
+// slot, so it is read once).  Walks (token, span).  Four resident blocks with
+// four rows in flight (64 registers) were faster than three with eight (499 and
+// 539 us at T = 55,414, K = 8, M = 3,584); loading the next item's routing ahead
+// made the warps drift apart and cost more than it hid (750 us and up).
 template <class E, int VW, int FMT>
-__global__ void __launch_bounds__(kExpertThreads, VW * sizeof(typename E::S) < 16 ? 2 : kMergeResident)
+__global__ void __launch_bounds__(kExpertThreads,
+                                  VW * sizeof(typename E::S) < 16 ? 2 : kMergeResident)
 expert_merge_rows(const __grid_constant__ ExpertArgs a) {
     using S = typename E::S;
     constexpr int KU = kRowsInFlight<S>;
@@ -605,7 +608,8 @@ __device__ __forceinline__ float warp_sums(float (&v)[N], int lane) {
 // Gradients of the merge; FMT != 0: the packed rows come from a checkpoint.
 // a.token_warps warps share a token's spans and add their parts of each
 // weight's gradient up in shared memory, in warp order.  KU rows' loads are in
-// flight at a time.
+// flight at a time: four, in four resident blocks, 85 us at T = 4,096, K = 8,
+// M = 4,096; eight in three 89, eight in two 129.
 template <class E, int VW, int FMT>
 __global__ void __launch_bounds__(kExpertThreads, VW * sizeof(typename E::S) < 16 ? 2 : 4)
 expert_merge_backward_rows(const __grid_constant__ ExpertArgs a) {
