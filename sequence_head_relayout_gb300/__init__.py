@@ -687,8 +687,10 @@ def expert_plan(experts: torch.Tensor, E: int, align: int = 1, out: ExpertPlan =
     if experts.dtype not in (torch.int32, torch.int64) or experts.dim() != 2:
         raise ValueError("experts must be an int32 or int64 view of shape [T,K]")
     T, K = experts.shape
-    rows = expert_rows(T, K, E, align)
     words = lib().vf_expert_workspace(T, K, E) // 4
+    rows = T * K + min(E, T * K) * (align - 1)             # without another library call
+    if words < 0 or align < 1 or rows > 0x7FFFFFFF:
+        rows = expert_rows(T, K, E, align)                 # raises VFError
     if out is None:
         # (views of one allocation take longer to make than four allocations)
         out = ExpertPlan(_new(stream, experts, (T, K), torch.int32),
