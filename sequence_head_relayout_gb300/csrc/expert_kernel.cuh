@@ -40,7 +40,6 @@ constexpr int kExpertThreads = 256;      // threads per block of the row kernels
 constexpr int kExpertWarps = kExpertThreads / 32;
 constexpr int kPlanThreads = 1024;
 constexpr int kMergeResident = 4;        // blocks of the merge that fit an SM
-constexpr int kGapBlocks = 4;            // blocks that zero one expert's gap rows
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 
 // Element types: storage S; exact widening to float32 and one rounding back,
@@ -143,7 +142,8 @@ struct ExpertArgs {
     int32_t groups;               // ceil(M / group)
     int32_t step_tokens, step_spans;     // row_blocks * kExpertWarps items, as Walk counts
     int32_t token_warps;          // merge backward: warps that share a token
-    uint32_t row_blocks;          // blocks of the row part; the rest zero the gap rows
+    uint32_t row_blocks;          // blocks of the row part; the rest zero the gap rows,
+    int32_t gap_blocks;           // so many of them to an expert
 };
 
 // The (token, span) items of the row blocks, one per warp at a time, spans
@@ -278,14 +278,15 @@ struct Slots {
     }
 };
 
-// Zeros for the gap rows of every expert: block `b` of kGapBlocks * E.
+// Zeros for the gap rows of every expert: block `b` of a.gap_blocks * E.
 template <class S, int VW>
 __device__ __forceinline__ void zero_gaps(const ExpertArgs &a, void *packed, uint32_t b) {
-    const int e = int(b / kGapBlocks);
-    const int64_t first = int64_t(a.offsets[e]) + a.counts[e] + b % kGapBlocks;
+    const uint32_t shares = uint32_t(a.gap_blocks);
+    const int e = int(b / shares);
+    const int64_t first = int64_t(a.offsets[e]) + a.counts[e] + b % shares;
     const int64_t end = min(int64_t(a.offsets[e + 1]), int64_t(a.rows));
     const S zero[VW] = {};
-    for (int64_t r = max(first, int64_t(0)); r < end; r += kGapBlocks) {
+    for (int64_t r = max(first, int64_t(0)); r < end; r += shares) {
         S *row = static_cast<S *>(packed) + r * a.M;
         for (int64_t c = int64_t(threadIdx.x) * VW; c < a.M; c += int64_t(blockDim.x) * VW)
             store_unit<S, VW>(row + c, zero);

@@ -201,3 +201,23 @@ def test_binding_refusals(L):
         vf.expert_merge_backward_q(x.half(), None, None, plan, None)
     with pytest.raises(ValueError, match="fmt"):
         vf.expert_restore_q(x, None, plan, fmt="fp4")
+
+
+def test_descriptor_layout_matches_the_header(tmp_path):
+    """The ctypes descriptor against the C compiler's view of the header."""
+    import os
+    import subprocess
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    names = [f[0] for f in vf._ExpertDesc._fields_]
+    src = tmp_path / "layout.c"
+    src.write_text('#include <stddef.h>\n#include <stdio.h>\n#include "vf_relayout.h"\n'
+                   "int main(void) {\n" +
+                   "".join('printf("%%zu ", offsetof(vf_expert_desc, %s));\n' % n for n in names) +
+                   'printf("%zu\\n", sizeof(vf_expert_desc));\nreturn 0;\n}\n')
+    exe = tmp_path / "layout"
+    subprocess.run(["gcc", "-std=c99", "-Wall", "-Werror", "-I", os.path.join(root, "include"),
+                    "-o", str(exe), str(src)], check=True)
+    got = [int(x) for x in subprocess.run([str(exe)], check=True, capture_output=True,
+                                          text=True).stdout.split()]
+    assert got == [getattr(vf._ExpertDesc, n).offset for n in names] + \
+        [ctypes.sizeof(vf._ExpertDesc)]
