@@ -14,7 +14,7 @@
 // (or written) once, whatever K is, and every packed row is read (or written)
 // once as a whole; the row index is one 4-byte load per slot.  Measured on GB300
 // (bf16, device time, bytes that cannot be avoided over it):
-//   pack            T = 55,414, K = 8, M = 3,584   516 us   6.71 TB/s
+//   pack            T = 55,414, K = 8, M = 3,584   510 us   6.79 TB/s
 //   merge           the same                       498 us   6.96 TB/s
 //   merge backward  T = 4,096, K = 8, M = 4,096     85 us   6.53 TB/s
 //   plan            1.6 M slots, 256 experts        23 us   bound by latency: two

@@ -20,6 +20,7 @@ using namespace vfc;
 
 constexpr int64_t kMaxSlots = int64_t(1) << 30;     // T * K
 constexpr int64_t kMaxExperts = 4096;
+constexpr int64_t kMaxAlign = 65536;
 constexpr int64_t kMaxRows = INT32_MAX;
 constexpr int64_t kMaxGrid = int64_t(1) << 27;   // a grid's warps fit 31 bits
 constexpr int64_t kSMs = 152;
@@ -51,10 +52,10 @@ int launch(void (*kernel)(Args), int64_t blocks, int threads, size_t smem, cudaS
 
 int check_routing(int64_t T, int64_t K, int64_t E, int64_t align, int64_t *rows) {
     if (T < 0 || K < 1 || E < 1 || align < 1) return VF_ERR_ARG;
-    if (T > kMaxExtent || K > kMaxExtent || E > kMaxExperts || align > kMaxExtent)
+    if (T > kMaxExtent || K > kMaxExtent || E > kMaxExperts || align > kMaxAlign)
         return VF_ERR_ARG;
     if (T * K > kMaxSlots) return VF_ERR_ARG;              // both at most 2^30
-    // at most 2^30 + 2^12 * 2^30
+    // at most 2^30 + 2^12 * 2^16
     *rows = T * K + std::min(E, T * K) * (align - 1);
     return *rows > kMaxRows ? VF_ERR_ARG : VF_OK;
 }
@@ -186,7 +187,7 @@ int check_desc(const vf_expert_desc *d, Call call) {
     int64_t most;
     const int rc = check_routing(d->T, d->K, d->E, 1, &most);
     if (rc != VF_OK) return rc;
-    if (d->align < 1 || d->align > kMaxExtent || d->M < 0 || d->M > kMaxExtent ||
+    if (d->align < 1 || d->align > kMaxAlign || d->M < 0 || d->M > kMaxExtent ||
         d->rows < 0 || d->rows > kMaxRows)
         return VF_ERR_ARG;
     return VF_OK;
@@ -387,7 +388,7 @@ int run(const vf_expert_desc *d, Call call, vf_stream_t stream) {
     // M = 3,584 499 us, against 565 with a block for every 8 items and 650 with
     // 5 blocks per SM, which do not all fit; with a checkpoint (K = 4) 442-447 in
     // 2-3 rounds, 462 in one, 489 in short blocks.  The other calls run best in
-    // short blocks (the pack 517 us, 593 and more in rounds).
+    // short blocks (the pack 510 us, 590 and more in rounds).
     if (call == Call::kMerge)
         blocks = std::min(blocks, kSMs * vf::kMergeResident * (tiles ? 2 : 1));
     blocks = std::min(blocks, kMaxGrid);

@@ -35,7 +35,7 @@ def test_rows(L):
     assert vf.expert_rows(1 << 27, 8, 4096, 1) == 1 << 30
     for bad in ((-1, 2, 8, 1), (1, 0, 8, 1), (1, 2, 0, 1), (1, 2, 8, 0), (1, 2, 4097, 1),
                 ((1 << 30) + 1, 1, 8, 1), (1 << 28, 8, 8, 1), (1 << 30, 1, 4096, 1 << 20),
-                (1, 2, 8, 1 << 31)):
+                (1, 2, 8, 65537), (1, 2, 8, 1 << 31)):
         assert L.vf_expert_rows(*bad) == ARG, bad
         with pytest.raises(vf.VFError):
             vf.expert_rows(*bad)
@@ -104,7 +104,7 @@ def _call(L, fn, **kw):
 def test_row_call_refusals(L, fn):
     assert getattr(L, fn)(None, None) == ARG
     for bad in (dict(type=3), dict(type=-1), dict(T=-1), dict(K=0), dict(M=-1), dict(E=0),
-                dict(rows=-1), dict(rows=1 << 31), dict(align=0), dict(format=3), dict(format=-1),
+                dict(rows=-1), dict(rows=1 << 31), dict(align=0), dict(align=65537), dict(format=3), dict(format=-1),
                 dict(format=1, group=48), dict(format=2, group=0), dict(format=1, type=1),
                 dict(format=1, type=2), dict(row_of=None), dict(row_of=A["row_of"] + 2),
                 dict(T=1 << 30, K=2), dict(M=1 << 31)):

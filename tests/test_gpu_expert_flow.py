@@ -300,6 +300,37 @@ def test_token_view_past_31_bits():
     assert torch.equal(view, vf.expert_merge(packed, plan))
 
 
+@pytest.mark.parametrize("E", [3, 4096])
+def test_most_slots(E):
+    """T*K = 2^30, the limit: the plan is checked in full (each slot has its row, in
+    slot order within its expert), the rows of a pack and a merge at places."""
+    T, K, M = 1 << 27, 8, 8
+    e = torch.randint(0, E, (T, K), generator=gen(E), device=DEV, dtype=torch.int32)
+    plan = vf.expert_plan(e, E)
+    counts = torch.bincount(e.view(-1), minlength=E)
+    assert torch.equal(plan.counts.long(), counts)
+    assert torch.equal(plan.offsets.long()[1:], counts.cumsum(0))
+    step = 1 << 26
+    for i in range(0, T * K, step):
+        rows = plan.row_of.view(-1)[i:i + step].long()
+        assert torch.equal(plan.slot_of[rows],
+                           torch.arange(i, i + step, device=DEV, dtype=torch.int32))
+        chosen = e.view(-1)[i:i + step].long()
+        assert ((rows >= plan.offsets[chosen]) & (rows < plan.offsets[chosen + 1])).all()
+        slots = plan.slot_of[i:i + step]
+        falls = (slots[1:] < slots[:-1]).nonzero()[:, 0] + i + 1
+        assert torch.isin(falls, plan.offsets.long()).all()
+    x = torch.empty(T, M, dtype=torch.bfloat16, device=DEV).normal_(generator=gen(1))
+    packed = vf.expert_pack(x, plan)
+    some = torch.randint(0, T * K, (1 << 20,), generator=gen(2), device=DEV)
+    some[:1000] = torch.arange(T * K - 1000, T * K, device=DEV)
+    assert torch.equal(packed[some], x[(plan.slot_of[some] // K).long()])
+    merged = vf.expert_merge(packed, plan)
+    t = (some // K)
+    want = x[t].double() * K                               # eight times the same value: exact
+    within(merged[t], want, want.abs() * 2.0 ** -8)
+
+
 # ---- random cases -------------------------------------------------------------------
 
 def reference(plan, K):
