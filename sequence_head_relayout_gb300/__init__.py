@@ -177,10 +177,11 @@ def _stream(stream, device):
     """The stream to enqueue on: the given one, else the current stream of the
     tensor's device (of the current device for pinned host tensors)."""
     if stream is not None:
-        return ctypes.c_void_p(stream.cuda_stream)
+        return stream.cuda_stream
     # (the handle itself: building a Stream object costs 2 us a call)
-    index = device.index if device.type == "cuda" else torch.cuda.current_device()
-    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(index))
+    index = device.index                                   # None for host memory
+    return torch._C._cuda_getCurrentRawStream(
+        torch.cuda.current_device() if index is None else index)
 
 
 def _call(fn, *args):
@@ -571,7 +572,7 @@ def _check_plan(plan, T=None):
     row_of, slot_of, counts, offsets, _ = plan
     i32 = torch.int32
     for t in (row_of, slot_of, counts, offsets):
-        if not t.is_cuda:
+        if not (isinstance(t, torch.Tensor) and t.is_cuda):
             _gpu_addressable(t, "plan")
         if t.dtype != i32 or not t.is_contiguous():
             raise ValueError("the tensors of a plan must be contiguous and int32")
@@ -587,7 +588,7 @@ def _check_plan(plan, T=None):
 def _new(stream, like, shape, dtype):
     """An output tensor beside ``like``, allocated on the stream that fills it
     (so that its memory is not handed out while that stream still uses it)."""
-    if like.device.type != "cuda":
+    if not like.is_cuda:
         return torch.empty(shape, dtype=dtype, pin_memory=True)
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=like.device)
