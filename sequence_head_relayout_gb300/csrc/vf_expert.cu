@@ -88,14 +88,18 @@ int64_t plan_workspace(const PlanShape &p, int64_t E) {
     return p.blocks > 1 ? p.blocks * (p.warps * E + vf::counts_stride(E)) : 0;
 }
 
+// The most that a plan's kernel takes: (2 * 6 + 2) arrays of 4,096 experts.
+constexpr int kPlanShared = 14 * 4096 * 4;
+
 int launch_plan_kernel(void (*kernel)(vf::PlanArgs), const vf::PlanArgs &a, const PlanShape &p,
                        int64_t arrays, cudaStream_t stream) {
     const size_t smem = size_t(arrays) * size_t(a.E) * 4;
-    // above 48 KB, the kernel's own arrays included, it has to be told; set on
-    // every call, so that no state is kept per device
+    // above 48 KB, the kernel's own arrays included, it has to be told; on every
+    // call, so that no state is kept per device, and always the same number, since
+    // another thread may be between this and its launch
     if (smem > 47 * 1024 &&
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             int(smem)) != cudaSuccess) {
+                             kPlanShared) != cudaSuccess) {
         cudaGetLastError();
         return VF_ERR_CUDA;
     }

@@ -228,6 +228,36 @@ def test_host_threads():
         same(a, b)
 
 
+def test_host_threads_with_plans_of_all_sizes():
+    """Plans whose kernels need different amounts of shared memory, at the same time:
+    none lowers what another has asked for."""
+    sizes = [(3000, 4, 4096), (4000, 4, 900), (2000, 8, 600), (2500, 4, 2048), (60, 8, 4096),
+             (9000, 2, 1024)]
+    cases = [routing(T, K, E, i) for i, (T, K, E) in enumerate(sizes)]
+    want = [[t.clone() for t in vf.expert_plan(e, s[2])[:4]] for e, s in zip(cases, sizes)]
+    torch.cuda.synchronize()
+    wrong, errors = [], []
+
+    def work(i):
+        try:
+            s = torch.cuda.Stream(DEV)
+            with torch.cuda.stream(s):
+                for _ in range(200):
+                    got = vf.expert_plan(cases[i], sizes[i][2])
+                s.synchronize()
+                wrong.extend(i for a, b in zip(got, want[i]) if not torch.equal(a, b))
+        except Exception as ex:                       # reported by the main thread
+            errors.append(ex)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(sizes))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    assert not wrong, wrong
+
+
 def test_pinned_host_rows():
     e = routing(40, 2, 5, 1)
     plan = vf.expert_plan(e, 5)
