@@ -1,0 +1,83 @@
+"""Edges of the expert relayouts: gradients that are not finite.
+
+Bounds as in ``tests/test_gpu_expert.py``.
+"""
+import pytest
+import torch
+
+import sequence_head_relayout_gb300 as vf
+from oracle import experts as X
+
+from .test_gpu_expert import (BF16, DEV, F16, F32, FMT, backward_bounds, make_plan, packed_for,
+                              rows_like, sentinel, weights_for, within)
+
+pytestmark = [pytest.mark.gpu, pytest.mark.usefixtures("oracle_built")]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    vf.lib()
+    yield
+    torch.cuda.synchronize()
+
+
+# ---- dropped slots of gradients that are not finite -----------------------------
+
+def dropped_routing(E):
+    """Tokens with all slots dropped, some and none; both kinds of dropped index."""
+    return torch.tensor([[-1, -1, E, -1, -1], [0, -1, 1, E + 2, 2], [-1, 3, -1, 0, -1],
+                         [1, 2, 3, 0, 1], [-1, -1, -1, -1, -1], [2, -1, 2, 1, -1],
+                         [-1, -1, -1, -1, 3]])
+
+
+def not_finite(grad):
+    """Infinities and NaN in tokens 0 to 3, at both ends of the row and all over."""
+    M = grad.shape[1]
+    grad[0] = float("nan")
+    grad[1, M - 1] = float("inf")
+    grad[2, 0] = -float("inf")
+    grad[3, M // 2] = float("nan")
+    return grad
+
+
+def check_backward(call, grad, values, plan, w, dtype, extra):
+    gp = sentinel((plan.slot_of.numel(), grad.shape[1]), dtype)
+    want, gw_want, mag = X.merge_backward(grad.cpu(), values, plan.row_of.cpu(),
+                                          plan.offsets.cpu(), w, gp.cpu())
+    got, gw = call(gp)
+    dropped = plan.row_of < 0
+    assert (gw[dropped] == 0).all(), "a dropped slot's gradient is %s" % gw[dropped].tolist()
+    b1, b2 = backward_bounds(want, grad, mag, dtype, grad.shape[1], extra=extra)
+    within(got, want, b1)
+    within(gw, gw_want, b2)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("M", [1, 7, 34, 100, 264, 2048])
+def test_dropped_slots_have_no_gradient(M, dtype):
+    E = 4
+    e = dropped_routing(E)
+    for align in (1, 4):
+        plan = make_plan(e, E, align)
+        y = packed_for(plan, M, dtype, M)
+        grad = not_finite(rows_like(e.shape[0], M, dtype, M + 1)).to(DEV)
+        w = weights_for(*e.shape, M, e, E)
+        check_backward(lambda gp: vf.expert_merge_backward(grad, y, plan, w.to(DEV),
+                                                           grad_packed=gp),
+                       grad, y.cpu(), plan, w, dtype, 0)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("M", [1, 7, 34, 100, 264, 2048])
+def test_dropped_slots_have_no_gradient_from_codes(M, fmt):
+    E, group = 4, 64
+    e = dropped_routing(E)
+    plan = make_plan(e, E, 4)
+    y = packed_for(plan, M, BF16, M)
+    grad = not_finite(rows_like(e.shape[0], M, BF16, M + 1)).to(DEV)
+    w = weights_for(*e.shape, M, e, E)
+    _, codes, scales = vf.expert_merge_q(y, plan, w.to(DEV), fmt, group)
+    kept = X.checkpoint(y.cpu(), FMT[fmt], group)
+    check_backward(lambda gp: vf.expert_merge_backward_q(grad, codes, scales, plan, w.to(DEV), fmt,
+                                                         group, grad_packed=gp),
+                   grad, X.values(kept[0], kept[1], FMT[fmt], group), plan, w, BF16, 1)
