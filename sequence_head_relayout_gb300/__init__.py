@@ -7,7 +7,9 @@ sm_103a kernels.  PyTorch provides device memory and streams.  There is no
 CPU path: the library must be built (``__graft_entry__.build()``) and the
 tensors must be addressable by the GPU -- CUDA memory, or pinned host memory
 that the kernels read or write directly over the host link -- otherwise the
-calls raise.
+calls raise.  A pinned tensor, a returned one too, has to be kept until the
+stream is past the calls that use it: torch's pinned-memory allocator does not
+know of these kernels and hands its memory out again at once.
 
 Operations ("Sol-Engine alignment on SM86 and SM89", section "What is
 enabled"):
@@ -586,14 +588,26 @@ def _check_plan(plan, T=None):
 
 
 def _new(stream, like, shape, dtype):
-    """An output tensor beside ``like``, allocated on the stream that fills it
-    (so that its memory is not handed out while that stream still uses it)."""
+    """An output tensor beside ``like``.  Device memory is allocated on the stream
+    that fills it, so that it is not handed out while that stream still uses it.
+    Pinned host memory has no such order: whoever holds the tensor keeps it until
+    the stream is done with it."""
     if not like.is_cuda:
         return torch.empty(shape, dtype=dtype, pin_memory=True)
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _workspace(stream, like, words):
+    """int32 scratch memory that a call drops when it returns: always device
+    memory, on the current device where ``like`` is host memory."""
+    device = like.device if like.is_cuda else "cuda"
+    if stream is None:
+        return torch.empty((words,), dtype=torch.int32, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty((words,), dtype=torch.int32, device=device)
 
 
 def _rows_out(t, stream, like, shape, dtype, what):
@@ -700,7 +714,7 @@ def expert_plan(experts: torch.Tensor, E: int, align: int = 1, out: ExpertPlan =
                          _new(stream, experts, (E + 1,), torch.int32), align)
     elif _check_plan(out) != (T, K, rows, E) or out.align != align:
         raise ValueError("out is a plan of other sizes")
-    work = _new(stream, experts, (words,), torch.int32) if words else None
+    work = _workspace(stream, experts, words) if words else None
     _call("vf_expert_plan", experts.data_ptr(), experts.element_size(), _strides(experts), T, K,
           E, align, out.row_of.data_ptr(), out.slot_of.data_ptr(), out.counts.data_ptr(),
           out.offsets.data_ptr(), None if work is None else work.data_ptr(),

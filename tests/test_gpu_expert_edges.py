@@ -1,4 +1,5 @@
-"""Edges of the expert relayouts: gradients that are not finite.
+"""Edges of the expert relayouts: gradients that are not finite, and indices in
+pinned host memory.
 
 Bounds as in ``tests/test_gpu_expert.py``.
 """
@@ -9,7 +10,7 @@ import sequence_head_relayout_gb300 as vf
 from oracle import experts as X
 
 from .test_gpu_expert import (BF16, DEV, F16, F32, FMT, backward_bounds, make_plan, packed_for,
-                              rows_like, sentinel, weights_for, within)
+                              rows_like, routing, sentinel, weights_for, within)
 
 pytestmark = [pytest.mark.gpu, pytest.mark.usefixtures("oracle_built")]
 
@@ -81,3 +82,32 @@ def test_dropped_slots_have_no_gradient_from_codes(M, fmt):
     check_backward(lambda gp: vf.expert_merge_backward_q(grad, codes, scales, plan, w.to(DEV), fmt,
                                                          group, grad_packed=gp),
                    grad, X.values(kept[0], kept[1], FMT[fmt], group), plan, w, BF16, 1)
+
+
+# ---- plans of pinned host indices ----------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [torch.int32, torch.int64])
+def test_plans_of_pinned_indices(dtype):
+    """Plans over many blocks, on two streams behind other work, with pinned memory
+    of the workspace's size taken and overwritten while they run."""
+    T, K, E, align = 5000, 4, 64, 8
+    words = vf.lib().vf_expert_workspace(T, K, E) // 4
+    assert words > 0
+    routings = [routing(T, K, E, seed) for seed in range(4)]
+    pinned = [e.to(dtype).pin_memory() for e in routings]
+    streams = [torch.cuda.Stream(DEV) for _ in range(2)]
+    for s in streams:
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(20_000_000)
+    plans, others = [], []
+    for i, e in enumerate(pinned):
+        plans.append(vf.expert_plan(e, E, align=align, stream=streams[i % 2]))
+        others.append(torch.empty(words, dtype=torch.int32, pin_memory=True).fill_(1 << 20))
+    torch.cuda.synchronize()
+    for e, plan in zip(routings, plans):
+        for a, b in zip(plan, X.plan(e, E, align)):
+            assert not a.is_cuda and torch.equal(a, b)
+    assert all((o == 1 << 20).all() for o in others)
+    on_current = vf.expert_plan(pinned[0], E, align=align)
+    torch.cuda.synchronize()
+    assert torch.equal(on_current.row_of, plans[0].row_of)
