@@ -791,7 +791,10 @@ __device__ __forceinline__ void rank_slots(const PlanArgs &a, const PlanPart &p,
     }
 }
 
-// Ranks to rows: base[e] is the first row of the part's slots of e.
+// Ranks to rows: base[e] is the first row of the part's slots of e.  The experts
+// are read a second time and row_of is the caller's memory, so what another writer
+// does to either meanwhile may give a row that does not exist: such a slot is
+// dropped, and nothing is stored outside slot_of.
 template <class I, int N>
 __device__ __forceinline__ void place_slots(const PlanArgs &a, const PlanPart &p,
                                             const int32_t *base) {
@@ -805,9 +808,10 @@ __device__ __forceinline__ void place_slots(const PlanArgs &a, const PlanPart &p
 #pragma unroll
         for (int u = 0; u < N; ++u)
             if (e[u] >= 0) {
-                row[u] += base[e[u]];
-                a.row_of[i0 + u * 32] = row[u];
-                a.slot_of[row[u]] = i0 + u * 32;
+                const uint32_t r = uint32_t(row[u]) + uint32_t(base[e[u]]);
+                const bool there = r < uint32_t(a.rows);
+                a.row_of[i0 + u * 32] = there ? int(r) : -1;
+                if (there) a.slot_of[r] = i0 + u * 32;
             }
     }
 }

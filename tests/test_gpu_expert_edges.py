@@ -111,3 +111,34 @@ def test_plans_of_pinned_indices(dtype):
     on_current = vf.expert_plan(pinned[0], E, align=align)
     torch.cuda.synchronize()
     assert torch.equal(on_current.row_of, plans[0].row_of)
+
+
+@pytest.mark.parametrize("T", [700, 5000])
+def test_indices_that_change_during_the_plan(T):
+    """Both forms of the plan while the host rewrites its indices, all slots moving
+    between the first and the last expert: any plan may come out, but every row it
+    names exists, and nothing outside its tensors is written."""
+    K, E = 4, 64
+    assert (vf.lib().vf_expert_workspace(T, K, E) > 0) == (T == 5000)
+    e = torch.zeros(T, K, dtype=torch.int64).pin_memory()
+    rows, guard = vf.expert_rows(T, K, E), 1 << 18
+    i32 = dict(dtype=torch.int32, device=DEV)
+    wide = [torch.full((n + 2 * guard,), 12345, **i32) for n in (T * K, rows)]
+    row_of, slot_of = (b[guard:-guard] for b in wide)
+    plan = vf.ExpertPlan(row_of.view(T, K), slot_of, torch.empty(E, **i32),
+                         torch.empty(E + 1, **i32))
+    stream, done = torch.cuda.Stream(DEV), torch.cuda.Event()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for _ in range(10):
+            vf.expert_plan(e, E, out=plan, stream=stream)
+        done.record(stream)
+        while not done.query():
+            e.fill_(E - 1)
+            e.fill_(0)
+        assert ((row_of >= -1) & (row_of < rows)).all()
+        for b in wide:
+            assert (b[:guard] == 12345).all() and (b[-guard:] == 12345).all()
+    vf.expert_plan(e, E, out=plan)
+    for a, b in zip(plan, X.plan(e, E)):
+        assert torch.equal(a.cpu(), b)
