@@ -661,27 +661,18 @@ expert_merge_backward_rows(const __grid_constant__ ExpertArgs a) {
                 for (int j = 0; j < KU; ++j) {
                     const float w = __shfl_sync(kAll, slots.weight, j);
                     float y[8], d[8];
-                    if constexpr (FMT != 0) code_values<FMT>(q[j].words(), y);
-                    else widen_span<E>(v[j], y);
+                    if constexpr (FMT != 0) {
+                        code_values<FMT>(q[j].words(), y);
 #pragma unroll
-                    for (int u = 0; u < 8 / VW; ++u) {
-                        // a checkpoint's unit: of the codes, and their scale once
-                        float2 sum = FMT != 0 ? make_float2(0.0f, 0.0f) : dots[j];
-#pragma unroll
-                        for (int i = u * VW; i < (u + 1) * VW; i += 2) {
-                            if constexpr (VW == 1)
-                                (i & 1 ? sum.y : sum.x) =
-                                    __fmaf_rn(g[i], y[i], i & 1 ? sum.y : sum.x);
-                            else
-                                sum = fma2_rn(make_float2(g[i], g[i + 1]),
-                                              make_float2(y[i], y[i + 1]), sum);
-                        }
-                        if constexpr (FMT != 0) {
-                            const float scale = finite_or_nan(q[j].scale[u]);
-                            sum = fma2_rn(make_float2(scale, scale), sum, dots[j]);
-                        }
-                        dots[j] = sum;
+                        for (int i = 0; i < 8; ++i)
+                            y[i] = __fmul_rn(y[i], finite_or_nan(q[j].scale[i / VW]));
+                    } else {
+                        widen_span<E>(v[j], y);
                     }
+#pragma unroll
+                    for (int i = 0; i < 8; i += 2)
+                        dots[j] = fma2_rn(make_float2(g[i], g[i + 1]),
+                                          make_float2(y[i], y[i + 1]), dots[j]);
 #pragma unroll
                     for (int i = 0; i < 8; i += 2) {
                         const float2 p = mul2_rn(make_float2(w, w), make_float2(g[i], g[i + 1]));

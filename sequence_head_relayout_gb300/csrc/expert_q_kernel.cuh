@@ -282,15 +282,21 @@ expert_merge_backward_tiles(const __grid_constant__ ExpertArgs a) {
                     if (r[j] < 0) continue;                      // warp-uniform
                     uint16_t *out = static_cast<uint16_t *>(a.grad_packed) +
                                     int64_t(r[j]) * a.M + c;
-                    float2 sum = make_float2(0.0f, 0.0f);        // of the codes; the scale once
+                    // each code times its scale before the gradient: a sum of g * code
+                    // can leave float32 where the row's values do not (scaling
+                    // the lane's sum instead took the same 414 us at the long case)
+                    const float s1 = finite_or_nan(scale[j]);
+                    float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
                     for (int i = 0; i < NV; ++i) {
                         float y[8], d[8];
                         code_values<FMT>(q[j][i], y);
 #pragma unroll
-                        for (int p = 0; p < 8; p += 2)
-                            sum = fma2_rn(make_float2(g[i][p], g[i][p + 1]),
-                                          make_float2(y[p], y[p + 1]), sum);
+                        for (int p = 0; p < 8; p += 2) {
+                            const float2 v = mul2_rn(make_float2(s1, s1),
+                                                     make_float2(y[p], y[p + 1]));
+                            sum = fma2_rn(make_float2(g[i][p], g[i][p + 1]), v, sum);
+                        }
 #pragma unroll
                         for (int p = 0; p < 8; ++p) d[p] = __fmul_rn(w, g[i][p]);
                         if (c + i * Tile<NV, L>::kStep < a.M)
@@ -298,7 +304,7 @@ expert_merge_backward_tiles(const __grid_constant__ ExpertArgs a) {
                                 make_uint4(Bf16::round(d), Bf16::round(d + 2),
                                            Bf16::round(d + 4), Bf16::round(d + 6));
                     }
-                    dot[j] = __fmaf_rn(finite_or_nan(scale[j]), sum.x + sum.y, dot[j]);
+                    dot[j] += sum.x + sum.y;
                 }
             }
             const float sum = warp_sums<KU>(dot, lane);

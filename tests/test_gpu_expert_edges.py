@@ -1,4 +1,5 @@
-"""Edges of the expert relayouts: gradients that are not finite, and indices in
+"""Edges of the expert relayouts: gradients that are not finite, or whose
+products with codes leave float32 unless the scale comes first, and indices in
 pinned host memory.
 
 Bounds as in ``tests/test_gpu_expert.py``.
@@ -9,8 +10,8 @@ import torch
 import sequence_head_relayout_gb300 as vf
 from oracle import experts as X
 
-from .test_gpu_expert import (BF16, DEV, F16, F32, FMT, backward_bounds, make_plan, packed_for,
-                              rows_like, routing, sentinel, weights_for, within)
+from .test_gpu_expert import (BF16, DEV, F16, F32, FMT, backward_bounds, gen, make_plan,
+                              packed_for, rows_like, routing, sentinel, weights_for, within)
 
 pytestmark = [pytest.mark.gpu, pytest.mark.usefixtures("oracle_built")]
 
@@ -82,6 +83,32 @@ def test_dropped_slots_have_no_gradient_from_codes(M, fmt):
     check_backward(lambda gp: vf.expert_merge_backward_q(grad, codes, scales, plan, w.to(DEV), fmt,
                                                          group, grad_packed=gp),
                    grad, X.values(kept[0], kept[1], FMT[fmt], group), plan, w, BF16, 1)
+
+
+# ---- gradients and scales at opposite ends of float32 ------------------------------
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("M", [33, 34, 100, 256, 1024, 1003])
+@pytest.mark.parametrize("powers", [(118, -90), (122, -95), (-130, 100)])
+def test_backward_takes_code_times_scale(M, fmt, powers):
+    """Each row is its codes times its scales: with huge gradients of tiny rows a
+    sum of gradient times code would leave float32, with tiny gradients of huge
+    rows it would lose bits, where the products with the row do neither."""
+    T, K, E, group = 9, 3, 5, 128
+    e = torch.randint(0, E, (T, K), generator=gen(M))
+    plan = make_plan(e, E)
+    y = (rows_like(T * K, M, F32, M) * 2.0 ** powers[1]).to(BF16).to(DEV)
+    grad = (rows_like(T, M, F32, M + 1) * 2.0 ** powers[0]).to(BF16).to(DEV)
+    w = weights_for(T, K, M)
+    _, codes, scales = vf.expert_merge_q(y, plan, w.to(DEV), fmt, group)
+    kept = X.checkpoint(y.cpu(), FMT[fmt], group)
+    values = X.values(kept[0], kept[1], FMT[fmt], group)
+    _, want, mag = X.merge_backward(grad.cpu(), values, plan.row_of.cpu(), plan.offsets.cpu(), w,
+                                    y.cpu())
+    assert torch.isfinite(grad).all() and mag.max() < 2.0 ** 60 and mag.min() > 2.0 ** -60
+    check_backward(lambda gp: vf.expert_merge_backward_q(grad, codes, scales, plan, w.to(DEV), fmt,
+                                                         group, grad_packed=gp),
+                   grad, values, plan, w, BF16, 1)
 
 
 # ---- plans of pinned host indices ----------------------------------------------------
