@@ -39,7 +39,9 @@ routing slots by expert, :func:`expert_pack` moves token rows to expert-major
 rows, :func:`expert_merge` takes them back with the routing weights and
 :func:`expert_merge_backward` gives its gradients.  With 8-bit checkpoints for
 the backward pass: :func:`expert_pack_q`, :func:`expert_restore_q`,
-:func:`expert_merge_q` and :func:`expert_merge_backward_q`.
+:func:`expert_merge_q` and :func:`expert_merge_backward_q`.  None of the calls
+records an autograd graph: the gradients are calls of their own, and the packs
+and merges refuse a tensor that requires a gradient while grad mode is on.
 """
 import ctypes
 import os
@@ -568,6 +570,16 @@ def _rows_type(t: torch.Tensor, what: str) -> int:
     return f
 
 
+def _unrecorded(t: torch.Tensor, what: str, gradient: str):
+    """Refuse a tensor whose gradient autograd would expect to be recorded: the
+    result of these calls has none, and it would be lost without a word."""
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError("%s requires a gradient, which this call does not record: pass "
+                         "%s.detach() or call it under torch.no_grad() (or in a "
+                         "torch.autograd.Function), with %s as its gradient"
+                         % (what, what, gradient))
+
+
 def _check_plan(plan, T=None):
     """(T, K, rows, E) of a plan whose tensors have the types and shapes that
     the kernels take; what they hold is checked by the kernels."""
@@ -729,9 +741,11 @@ def expert_pack(x: torch.Tensor, plan: ExpertPlan, out: torch.Tensor = None,
 
     Gap rows (``plan.align``) are written as zeros, rows behind the last expert
     are left as they were.  The gradient of ``x`` is :func:`expert_merge` of the
-    gradient of the result.
+    gradient of the result.  No graph is recorded: an ``x`` that requires a
+    gradient is refused while grad mode is on.
     """
     typ = _rows_type(x, "x")
+    _unrecorded(x, "x", "expert_merge")
     T, M = _matrix(x, "x")
     dims = _check_plan(plan, T)
     out = _rows_out(out, stream, x, (dims[2], M), x.dtype, "out")
@@ -750,9 +764,11 @@ def expert_merge(packed: torch.Tensor, plan: ExpertPlan, weights: torch.Tensor =
 
     ``out`` may be any non-overlapping [T,M] view.  The gradient of ``packed``
     without weights is :func:`expert_pack` of the gradient of the result; with
-    weights see :func:`expert_merge_backward`.
+    weights see :func:`expert_merge_backward`.  No graph is recorded: rows or
+    weights that require a gradient are refused while grad mode is on.
     """
     typ = _rows_type(packed, "packed")
+    _unrecorded(packed, "packed", "expert_pack" if weights is None else "expert_merge_backward")
     rows, M = _matrix(packed, "packed")
     dims = _check_plan(plan)
     T, K = dims[:2]
@@ -761,6 +777,8 @@ def expert_merge(packed: torch.Tensor, plan: ExpertPlan, weights: torch.Tensor =
     d = _expert_desc(typ, plan, dims, M)
     _set_tokens(d, out)
     _set_weights(d, weights, T, K)
+    if weights is not None:
+        _unrecorded(weights, "weights", "expert_merge_backward")
     d.packed = packed.data_ptr()
     _expert_call("vf_expert_merge", d, stream, packed)
     return out
@@ -821,6 +839,7 @@ def expert_pack_q(x: torch.Tensor, plan: ExpertPlan, fmt="e4m3", group: int = 12
     the lossy transport.
     """
     T, M = _bf16_matrix(x, "x")
+    _unrecorded(x, "x", "expert_merge")
     f = _fmt(fmt)
     dims = _check_plan(plan, T)
     codes, scales = _kept(codes, scales, stream, x, T, M, f, group)
@@ -861,6 +880,8 @@ def expert_merge_q(packed: torch.Tensor, plan: ExpertPlan, weights: torch.Tensor
     for :func:`expert_merge_backward_q` -> (merged [T,M], codes [rows,M],
     scales [rows, ceil(M/group)]).  Rows that no slot owns are not written."""
     rows, M = _bf16_matrix(packed, "packed")
+    _unrecorded(packed, "packed", "expert_pack" if weights is None else
+                "expert_merge_backward_q")
     f = _fmt(fmt)
     dims = _check_plan(plan)
     T, K = dims[:2]
@@ -870,6 +891,8 @@ def expert_merge_q(packed: torch.Tensor, plan: ExpertPlan, weights: torch.Tensor
     d = _expert_desc(0, plan, dims, M)
     _set_tokens(d, out)
     _set_weights(d, weights, T, K)
+    if weights is not None:
+        _unrecorded(weights, "weights", "expert_merge_backward_q")
     _set_kept(d, codes, scales, f, group)
     d.packed = packed.data_ptr()
     _expert_call("vf_expert_merge", d, stream, packed)

@@ -39,3 +39,49 @@ def test_plan_workspace_is_device_memory(monkeypatch):
     assert [m[0] for m in seen.made] == outs + [(words,)]
     assert all(m[1:] == ("cpu", True) for m in seen.made[:4])      # beside the indices
     assert seen.made[4][1:] == ("cuda", False)
+
+
+def _calls(x, packed, w):
+    plan = vf.ExpertPlan(*(torch.zeros(s, dtype=torch.int32) for s in ((4, 2), (8,), (4,), (5,))))
+    return {"expert_pack": lambda: vf.expert_pack(x, plan),
+            "expert_pack_q": lambda: vf.expert_pack_q(x, plan),
+            "expert_merge": lambda: vf.expert_merge(packed, plan, w),
+            "expert_merge_q": lambda: vf.expert_merge_q(packed, plan, w)}
+
+
+def test_gradients_are_never_lost_silently(monkeypatch):
+    """A pack or a merge records no graph, so it refuses what autograd follows;
+    detached, without grad mode and inside a Function the same calls run."""
+    seen = Recorder(monkeypatch)
+    monkeypatch.setattr(vf, "_expert_call", lambda fn, d, stream, like: seen.calls.append(fn))
+    x = torch.zeros(4, 64, dtype=torch.bfloat16, requires_grad=True)
+    y = torch.zeros(8, 64, dtype=torch.bfloat16, requires_grad=True)
+    w = torch.zeros(4, 2, requires_grad=True)
+    live = dict(_calls(x, y, None))
+    live.update({k + " with weights": f for k, f in _calls(x, y.detach(), w).items()})
+    for name, call in live.items():
+        with pytest.raises(ValueError, match="requires a gradient.*detach.*as its gradient"):
+            call()
+            pytest.fail("%s was accepted" % name)
+    assert not seen.calls and not any(m[1] == "cuda" for m in seen.made)
+    for name, call in _calls(x.detach(), y.detach(), w.detach()).items():
+        call()
+    with torch.no_grad():
+        for name, call in live.items():
+            call()
+
+    class Pack(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x):
+            return _calls(x, None, None)["expert_pack"]()
+
+        @staticmethod
+        def backward(ctx, grad):
+            return None
+
+    Pack.apply(x)
+    # the gradients' own calls take what a graph holds: nothing follows them
+    plan = vf.ExpertPlan(*(torch.zeros(s, dtype=torch.int32) for s in ((4, 2), (8,), (4,), (5,))))
+    vf.expert_merge_backward(x.detach(), y, plan, w)
+    assert seen.calls == (["vf_expert_pack"] * 2 + ["vf_expert_merge"] * 2) * 3 + [
+        "vf_expert_pack", "vf_expert_merge_backward"]
