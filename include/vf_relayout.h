@@ -392,7 +392,8 @@ int64_t vf_scale_count(int op, int64_t T, int64_t H, int64_t D, int64_t P, int64
  * checked on the host before anything is enqueued; a written range that
  * overlaps another range of the call is VF_ERR_ALIAS.  Limits (VF_ERR_ARG):
  * K >= 1, T*K at most 2^30, rows below 2^31, 1 <= E <= 4096,
- * 1 <= align <= 65536.
+ * 1 <= align <= 65536; K at most 65536 in the calls that move rows, which take
+ * a token's slots one after the other.
  */
 typedef enum vf_type {
     VF_TYPE_BF16 = 0,

@@ -20,6 +20,10 @@ using namespace vfc;
 
 constexpr int64_t kMaxSlots = int64_t(1) << 30;     // T * K
 constexpr int64_t kMaxExperts = 4096;
+// K of the row calls, which walk a token's slots in turn: at T = 1, K = 65,536,
+// M = 4,096 the merge takes 12 ms and its backward pass 40; 2^30 slots of one token
+// would hold the GPU for minutes.
+constexpr int64_t kMaxChoices = 65536;
 constexpr int64_t kMaxAlign = 65536;
 constexpr int64_t kMaxRows = INT32_MAX;
 constexpr int64_t kMaxGrid = int64_t(1) << 27;   // a grid's warps fit 31 bits
@@ -191,8 +195,8 @@ int check_desc(const vf_expert_desc *d, Call call) {
     int64_t most;
     const int rc = check_routing(d->T, d->K, d->E, 1, &most);
     if (rc != VF_OK) return rc;
-    if (d->align < 1 || d->align > kMaxAlign || d->M < 0 || d->M > kMaxExtent ||
-        d->rows < 0 || d->rows > kMaxRows)
+    if (d->K > kMaxChoices || d->align < 1 || d->align > kMaxAlign || d->M < 0 ||
+        d->M > kMaxExtent || d->rows < 0 || d->rows > kMaxRows)
         return VF_ERR_ARG;
     return VF_OK;
 }

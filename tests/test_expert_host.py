@@ -221,3 +221,16 @@ def test_descriptor_layout_matches_the_header(tmp_path):
                                           text=True).stdout.split()]
     assert got == [getattr(vf._ExpertDesc, n).offset for n in names] + \
         [ctypes.sizeof(vf._ExpertDesc)]
+
+
+@pytest.mark.parametrize("fn", CALLS)
+def test_row_calls_limit_the_slots_of_a_token(L, fn):
+    """A token's slots are taken in turn: 2^30 of one token would run for minutes."""
+    for fmt in (0, 1):
+        if fn != "vf_expert_restore" or fmt:
+            for T, K in ((1, 65537), (1, 1 << 30), (0, 65537)):
+                assert _call(L, fn, format=fmt, T=T, K=K) == ARG, (T, K)
+            most = _call(L, fn, format=fmt, T=1, K=65536, weight_strides=(65536, 1))
+            assert most == (ARG if torch.cuda.is_available() else CUDA)  # fake pointers
+    # a plan sorts slots, however they are spread over tokens
+    assert vf.expert_rows(1, 1 << 30, 8) == 1 << 30
