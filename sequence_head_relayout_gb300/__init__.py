@@ -716,7 +716,7 @@ def expert_plan(experts: torch.Tensor, E: int, align: int = 1, out: ExpertPlan =
     T, K = experts.shape
     words = lib().vf_expert_workspace(T, K, E) // 4
     rows = T * K + min(E, T * K) * (align - 1)             # without another library call
-    if words < 0 or align < 1 or rows > 0x7FFFFFFF:
+    if words < 0 or not 1 <= align <= 65536 or rows > 0x7FFFFFFF:    # the limits of the header
         rows = expert_rows(T, K, E, align)                 # raises VFError
     if out is None:
         # (views of one allocation take longer to make than four allocations)

@@ -85,3 +85,14 @@ def test_gradients_are_never_lost_silently(monkeypatch):
     vf.expert_merge_backward(x.detach(), y, plan, w)
     assert seen.calls == (["vf_expert_pack"] * 2 + ["vf_expert_merge"] * 2) * 3 + [
         "vf_expert_pack", "vf_expert_merge_backward"]
+
+
+@pytest.mark.parametrize("T,K,E,align", [(1, 1, 4, 65537), (4096, 2, 4096, 1 << 18), (1, 1, 4, 0),
+                                         (1, 1, 4, -3), (1, 1, 0, 1), (1, 1, 4097, 1),
+                                         (0, 0, 4, 1), (0, 1, 4, 1 << 40)])
+def test_plan_refuses_sizes_before_it_allocates(monkeypatch, T, K, E, align):
+    experts = torch.zeros(T, K, dtype=torch.int64)
+    seen = Recorder(monkeypatch)
+    with pytest.raises(vf.VFError):
+        vf.expert_plan(experts, E, align=align)
+    assert not seen.made and not seen.calls
