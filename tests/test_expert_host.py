@@ -234,3 +234,37 @@ def test_row_calls_limit_the_slots_of_a_token(L, fn):
             assert most == (ARG if torch.cuda.is_available() else CUDA)  # fake pointers
     # a plan sorts slots, however they are spread over tokens
     assert vf.expert_rows(1, 1 << 30, 8) == 1 << 30
+
+
+def test_row_calls_and_ranges_that_wrap(L):
+    """The exact status of ranges that end past the address space, of huge ones that
+    cover the others, and of a view that covers itself."""
+    end = 1 << 64
+    for fn, name, size in (("vf_expert_pack", "packed", 8 * 64 * 2),
+                           ("vf_expert_pack", "tokens", 4 * 64 * 2),
+                           ("vf_expert_restore", "packed", 8 * 64 * 2),
+                           ("vf_expert_restore", "codes", 4 * 64),
+                           ("vf_expert_merge", "packed", 8 * 64 * 2),
+                           ("vf_expert_merge", "weights", 4 * 2 * 4),
+                           ("vf_expert_merge_backward", "grad_packed", 8 * 64 * 2),
+                           ("vf_expert_merge_backward", "grad_weights", 4 * 2 * 4),
+                           ("vf_expert_merge_backward", "row_of", 4 * 2 * 4)):
+        assert _call(L, fn, **{name: end - size}) == OVERFLOW, (fn, name)
+        assert _call(L, fn, **{name: end - 4 if size > 4 else end - 2}) == OVERFLOW, (fn, name)
+    assert _plan(L, T=4, work=None, row_of=end - 4 * 8 * 4) == OVERFLOW
+    assert _plan(L, T=4, work=None, strides=(1 << 61, 1)) == OVERFLOW
+    huge = dict(rows=(1 << 31) - 1, M=1 << 30, T=1 << 20)
+    # of the pack's ranges packed lies highest here: nothing is above it to be covered
+    assert _call(L, "vf_expert_pack", **huge) == (ARG if torch.cuda.is_available() else CUDA)
+    assert _call(L, "vf_expert_pack", row_of=A["grad_weights"], **huge) == ALIAS
+    assert _call(L, "vf_expert_restore", **huge) == ALIAS
+    assert _call(L, "vf_expert_merge", **huge) == ARG              # rows of 2^30, 64 apart
+    assert _call(L, "vf_expert_merge_backward", **huge) == ALIAS
+
+
+def test_pack_does_not_look_at_weights(L):
+    reached = ARG if torch.cuda.is_available() else CUDA           # fake pointers
+    assert _call(L, "vf_expert_pack", weight_strides=(2, -1), weights=1) == reached
+    assert _call(L, "vf_expert_restore", weight_strides=(2, -1), weights=1) == reached
+    assert _call(L, "vf_expert_merge", weight_strides=(2, -1)) == ARG
+    assert _call(L, "vf_expert_merge_backward", weight_strides=(2, -1)) == ARG

@@ -1,6 +1,6 @@
 """Edges of the expert relayouts: gradients that are not finite, or whose
-products with codes leave float32 unless the scale comes first, and indices in
-pinned host memory.
+products with codes leave float32 unless the scale comes first, indices in pinned
+host memory, skewed routings and the exchange between ranks.
 
 Bounds as in ``tests/test_gpu_expert.py``.
 """
@@ -169,3 +169,85 @@ def test_indices_that_change_during_the_plan(T):
     vf.expert_plan(e, E, out=plan)
     for a, b in zip(plan, X.plan(e, E)):
         assert torch.equal(a.cpu(), b)
+
+
+# ---- routings with most slots in a few experts ----------------------------------------
+
+@pytest.mark.parametrize("how", ["one", "few", "falling"])
+@pytest.mark.parametrize("T,K,E,align", [(150000, 8, 64, 128), (400001, 3, 256, 1),
+                                         (70000, 4, 4096, 16)])
+def test_skewed_plans_over_many_blocks(T, K, E, align, how):
+    g = torch.Generator(device=DEV).manual_seed(T)
+    if how == "one":
+        e = torch.full((T, K), E - 1, device=DEV)
+    elif how == "few":                       # nine of ten slots in two experts
+        e = torch.randint(0, E, (T, K), generator=g, device=DEV)
+        e[torch.rand(T, K, generator=g, device=DEV) < 0.9] = 1
+        e[::3] = E - 2
+    else:                                    # expert e about as often as 1 / (e + 1)
+        u = torch.rand(T, K, generator=g, device=DEV, dtype=torch.float64)
+        e = ((E + 1.0) ** u).long() - 1
+    assert vf.lib().vf_expert_workspace(T, K, E) > 0
+    plan = vf.expert_plan(e, E, align=align)
+    flat = e.reshape(-1)
+    counts = torch.bincount(flat, minlength=E)
+    steps = (counts + align - 1) // align * align
+    assert torch.equal(plan.counts.long(), counts)
+    assert torch.equal(plan.offsets.long()[1:], steps.cumsum(0)) and int(plan.offsets[0]) == 0
+    order = torch.argsort(flat, stable=True)
+    at = torch.arange(T * K, device=DEV) - (counts.cumsum(0) - counts)[flat[order]]
+    row = plan.offsets.long()[flat[order]] + at
+    assert torch.equal(plan.row_of.reshape(-1)[order].long(), row)
+    slots = torch.full_like(plan.slot_of, -1)
+    slots[row] = order.int()
+    assert torch.equal(plan.slot_of, slots)
+
+
+# ---- the exchange between ranks ---------------------------------------------------------
+
+@pytest.mark.parametrize("E", [12, 10])
+def test_exchange_of_expert_rows(E):
+    """Experts spread over P ranks, all of them emulated here one after the other.
+    Source s packs by expert and sends destination p the rows offsets[p*E//P] ..
+    offsets[(p+1)*E//P]; the receiver sorts the P segments by its own experts with a
+    second plan (one slot per row) and merges them back into the order they came in;
+    the source merges with its weights.  Rows are moved and scaled by powers of two,
+    so the result is that of one rank with all experts, bit for bit."""
+    P, T, K, M = 4, 60, 3, 72
+    first = [p * E // P for p in range(P + 1)]
+    scale = 2.0 ** (torch.arange(E) % 7 - 3)
+    sent, plans, xs, ws = [], [], [], []
+    for s in range(P):
+        e = routing(T + s, K, E, 40 + s)
+        xs.append(rows_like(T + s, M, BF16, 50 + s).to(DEV))
+        ws.append(weights_for(T + s, K, 60 + s).to(DEV))
+        plans.append(vf.expert_plan(e.to(DEV), E))
+        sent.append(vf.expert_pack(xs[s], plans[s]))
+    offsets = [p.offsets.tolist() for p in plans]          # split sizes: read back once
+
+    def segment(s, p):
+        return slice(offsets[s][first[p]], offsets[s][first[p + 1]])
+
+    returned = [torch.empty_like(b) for b in sent]
+    for p in range(P):
+        recv = torch.cat([sent[s][segment(s, p)] for s in range(P)])
+        experts = torch.cat([torch.repeat_interleave(
+            torch.arange(first[p + 1] - first[p]),
+            plans[s].counts[first[p]:first[p + 1]].long().cpu()) for s in range(P)])
+        local = vf.expert_plan(experts.to(DEV)[:, None], first[p + 1] - first[p])
+        rows = vf.expert_pack(recv, local)
+        at = local.offsets.tolist()
+        for i in range(first[p + 1] - first[p]):
+            rows[at[i]:at[i + 1]] *= scale[first[p] + i].item()
+        back = vf.expert_merge(rows, local)
+        done = 0
+        for s in range(P):
+            n = offsets[s][first[p + 1]] - offsets[s][first[p]]
+            returned[s][segment(s, p)] = back[done:done + n]
+            done += n
+    for s in range(P):
+        whole = sent[s].clone()
+        for i in range(E):
+            whole[offsets[s][i]:offsets[s][i + 1]] *= scale[i].item()
+        got = vf.expert_merge(returned[s], plans[s], ws[s])
+        assert torch.equal(got, vf.expert_merge(whole, plans[s], ws[s]))
