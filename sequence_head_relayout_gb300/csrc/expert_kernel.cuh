@@ -12,13 +12,16 @@
 // All of the row kernels are bound by HBM: they move whole rows and do a few
 // operations per element.  They walk the token side, so a token row is read
 // (or written) once, whatever K is, and every packed row is read (or written)
-// once as a whole; the row index is one 4-byte load per slot.  Measured on GB300
-// (bf16, device time, bytes that cannot be avoided over it):
+// once as a whole; the row index is one 4-byte load per slot.  (The merge's
+// backward pass loads its token row once for every 2 or 4 slots; from the second
+// time on it comes from the caches.)  Measured on GB300 (bf16, device time, bytes
+// that cannot be avoided over it):
 //   pack            T = 55,414, K = 8, M = 3,584   510 us   6.79 TB/s
 //   merge           the same                       498 us   6.96 TB/s
 //   merge backward  T = 4,096, K = 8, M = 4,096     85 us   6.53 TB/s
 //   plan            1.6 M slots, 256 experts        23 us   bound by latency: two
-//                   grids, each a walk of some 300 slots per warp in slot order
+//                   grids, each a walk of some 300 slots per warp in slot order,
+//                   with one block of 1,024 threads to an SM (54 registers)
 //
 // Work split: a warp takes one span, kSpan consecutive columns of one token.
 // A lane holds 8 columns of it as 8 / VW units of VW elements; unit u of lane
@@ -178,8 +181,8 @@ __device__ __forceinline__ int unit_col(int u, int lane) { return u * 32 * VW + 
 // column clamped into the row (and from row 0 where there is none: the caller
 // sees to it that a row exists) and zeroed afterwards: with a condition each, the
 // loads of a span waited for one another (the merge of 20,000 tokens, K = 4,
-// M = 2,049 took 662 us, 154 so).  kClampBelow: the unit size from which on the
-// loads are predicated instead.
+// M = 2,049 took 662 us, 186 so, and 154 with the loads marked as well).
+// kClampBelow: the unit size from which on the loads are predicated instead.
 template <class S, int VW, int kClampBelow = 16>
 __device__ __forceinline__ Lane8<S> load_span(const void *base, int64_t offset, int64_t stride,
                                               int col0, int M, int lane,

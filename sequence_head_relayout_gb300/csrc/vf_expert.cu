@@ -396,7 +396,11 @@ int run(const vf_expert_desc *d, Call call, vf_stream_t stream) {
     // M = 3,584 499 us, against 565 with a block for every 8 items and 650 with
     // 5 blocks per SM, which do not all fit; with a checkpoint (K = 4) 442-447 in
     // 2-3 rounds, 462 in one, 489 in short blocks.  The other calls run best in
-    // short blocks (the pack 510 us, 590 and more in rounds).
+    // short blocks (the pack 510 us, 590 and more in rounds).  Rows of smaller units
+    // have as many blocks, in two rounds where their registers leave room for two:
+    // at T = 20,000, K = 4, M = 2,052 75 us with 4 to an SM, 120 with 2, 77 with 8;
+    // at M = 2,049 154, 152 and 153; with an E4M3 checkpoint 303, 313 and 258, and
+    // 542, 539 and 543.
     if (call == Call::kMerge)
         blocks = std::min(blocks, kSMs * vf::kMergeResident * (tiles ? 2 : 1));
     blocks = std::min(blocks, kMaxGrid);
