@@ -479,6 +479,57 @@ int vf_expert_merge(const vf_expert_desc *desc, vf_stream_t stream);
  */
 int vf_expert_merge_backward(const vf_expert_desc *desc, vf_stream_t stream);
 
+/*
+ * Expert products: the arithmetic between vf_expert_pack and vf_expert_merge, on
+ * packed rows grouped by expert.  The plan's counts and offsets say which rows are
+ * whose: expert e's are offsets[e] .. offsets[e] + counts[e] - 1.
+ *
+ *   vf_expert_product       out[r][n] = sum over m of packed[r][m] * weights[e][n][m]
+ *   vf_expert_weight_grad   grad_weights[e][n][m] = sum over e's rows r of
+ *                                                   grad[r][n] * packed[r][m]
+ * The gradient of the packed rows is vf_expert_product of the gradient with the
+ * weights' view transposed (n and m exchanged).
+ *
+ * Elements are VF_TYPE_BF16 or VF_TYPE_F16.  Products are exact and summed in
+ * float32 in an order that is fixed for given sizes (by tensor cores, whose
+ * additions may drop bits below an accumulator's last), and each output is rounded
+ * once, to nearest even.  Equal calls give equal bits.
+ * Rows that hold no slot are never read into a result.  Of out, gap rows are
+ * written as zeros and rows at and behind offsets[E] left as they were; an expert
+ * without rows gets zeros in grad_weights, and its weights are not read.
+ * Segments outside [0, rows) are cut to it, so no content of a plan makes a kernel
+ * read or write out of bounds; segments that overlap give unspecified rows.
+ *
+ * All buffers are device memory of the current device (page-locked host memory is
+ * refused).  Ownership, streams and errors as above; a written range that overlaps
+ * another range of the call is VF_ERR_ALIAS.  No workspace.  Limits (VF_ERR_ARG):
+ * as for the expert relayouts, N and M at most 2^20.
+ * Operands go through tensor maps when packed (and grad) start at a multiple of 16
+ * bytes with M (and N) multiples of 8, and the weights have unit stride along n or m
+ * with the other strides multiples of 8; others are loaded element by element.
+ * A kernel whose internal wait lasts for seconds, which only a failing device can
+ * bring about, writes NaN to what it has not stored yet.
+ */
+typedef struct vf_product_desc {
+    int32_t type;               /* VF_TYPE_BF16 or VF_TYPE_F16 */
+    int32_t out_type;           /* vf_expert_weight_grad: type, or VF_TYPE_F32 */
+    int64_t E, N, M;
+    int64_t rows;               /* rows of packed, grad and out */
+    int64_t slots;              /* T * K of the plan: steers the choice of a form only */
+    int64_t align;
+    const int32_t *counts;      /* [E] */
+    const int32_t *offsets;     /* [E + 1] */
+    const void *packed;         /* [rows][M] */
+    const void *weights;        /* [E][N][M] view, any strides */
+    int64_t weight_strides[3];
+    const void *grad;           /* [rows][N] */
+    void *out;                  /* [rows][N] */
+    void *grad_weights;         /* [E][N][M] */
+} vf_product_desc;
+
+int vf_expert_product(const vf_product_desc *desc, vf_stream_t stream);
+int vf_expert_weight_grad(const vf_product_desc *desc, vf_stream_t stream);
+
 /* Static, NUL-terminated description of a vf_status value. */
 const char *vf_status_string(int status);
 

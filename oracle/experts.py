@@ -118,3 +118,32 @@ def values(codes: torch.Tensor, scales: torch.Tensor, fmt: int, group: int) -> t
         code = table[codes.view(torch.uint8).long()]
     s = scales.double().repeat_interleave(group, dim=1)[:, :M]
     return torch.where(torch.isfinite(s), code * s, torch.full_like(s, float("nan")))
+
+
+def product(packed: torch.Tensor, weights: torch.Tensor, counts: torch.Tensor,
+            offsets: torch.Tensor, before: torch.Tensor):
+    """(packed rows times their experts' weights, with ``before``'s rows behind the
+    last expert and zeros in the gaps; sum of the magnitudes of its terms)."""
+    out = before.double().clone()
+    mag = torch.zeros_like(out)
+    out[:int(offsets[-1])] = 0
+    for e in range(counts.numel()):
+        at, n = int(offsets[e]), int(counts[e])
+        x, w = packed[at:at + n].double(), weights[e].double()
+        out[at:at + n] = x @ w.t()
+        mag[at:at + n] = x.abs() @ w.abs().t()
+    return out, mag
+
+
+def weight_grad(grad: torch.Tensor, packed: torch.Tensor, counts: torch.Tensor,
+                offsets: torch.Tensor):
+    """(gradient of the product's weights, sum of the magnitudes of its terms)."""
+    E = counts.numel()
+    out = torch.zeros((E, grad.shape[1], packed.shape[1]), dtype=torch.float64)
+    mag = torch.zeros_like(out)
+    for e in range(E):
+        at, n = int(offsets[e]), int(counts[e])
+        g, x = grad[at:at + n].double(), packed[at:at + n].double()
+        out[e] = g.t() @ x
+        mag[e] = g.abs().t() @ x.abs()
+    return out, mag

@@ -54,7 +54,7 @@ __all__ = ["qkv_pack", "qkv_pack3", "attn_split", "head_merge", "qkv_unpack", "p
            "OP_QKV_UNPACK", "qkv_pack_q", "attn_split_q", "head_merge_q", "qkv_unpack_q",
            "scale_count", "FORMATS", "ExpertPlan", "expert_rows", "expert_plan", "expert_pack",
            "expert_merge", "expert_merge_backward", "expert_pack_q", "expert_restore_q",
-           "expert_merge_q", "expert_merge_backward_q"]
+           "expert_merge_q", "expert_merge_backward_q", "expert_product", "expert_weight_grad"]
 
 OP_QKV_PACK, OP_ATTN_SPLIT, OP_HEAD_MERGE, OP_QKV_UNPACK = 0, 1, 2, 3
 ORDERS = {"chunk_major": 0, "slot_major": 1}
@@ -86,6 +86,15 @@ class _ExpertDesc(ctypes.Structure):
                 ("tokens", _P), ("token_strides", _I64 * 2), ("packed", _P),
                 ("weights", _P), ("weight_strides", _I64 * 2), ("codes", _P), ("scales", _P),
                 ("grad_packed", _P), ("grad_weights", _P)]
+
+
+class _ProductDesc(ctypes.Structure):
+    """vf_product_desc of the C ABI."""
+    _fields_ = [("type", ctypes.c_int32), ("out_type", ctypes.c_int32),
+                ("E", _I64), ("N", _I64), ("M", _I64), ("rows", _I64), ("slots", _I64),
+                ("align", _I64), ("counts", _P), ("offsets", _P), ("packed", _P),
+                ("weights", _P), ("weight_strides", _I64 * 3), ("grad", _P), ("out", _P),
+                ("grad_weights", _P)]
 
 
 class VFError(RuntimeError):
@@ -153,6 +162,10 @@ def lib():
                      "vf_expert_merge_backward"):
             f = getattr(l, name)
             f.argtypes = [ctypes.POINTER(_ExpertDesc), _P]
+            f.restype = ctypes.c_int
+        for name in ("vf_expert_product", "vf_expert_weight_grad"):
+            f = getattr(l, name)
+            f.argtypes = [ctypes.POINTER(_ProductDesc), _P]
             f.restype = ctypes.c_int
         l.vf_status_string.argtypes = [ctypes.c_int]
         l.vf_status_string.restype = ctypes.c_char_p
@@ -917,3 +930,90 @@ def expert_merge_backward_q(grad: torch.Tensor, codes: torch.Tensor, scales: tor
     _set_kept(d, codes, scales, f, group)
     _expert_call("vf_expert_merge_backward", d, stream, grad)
     return grad_packed, grad_weights
+
+
+# ---- expert products -------------------------------------------------------------
+
+def _product_rows(t, what):
+    """vf_type of contiguous packed rows that a product takes."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % what)
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % what)
+    f = _TYPES.get(t.dtype)
+    if f is None or f == 2:
+        raise ValueError("%s must hold bfloat16 or float16 values" % what)
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % what)
+    return f
+
+
+def _product_desc(typ, plan, dims, rows, N, M):
+    if rows != dims[2]:
+        raise ValueError("plan is for %d packed rows, not %d" % (dims[2], rows))
+    d = _ProductDesc(typ, typ, dims[3], N, M, rows, dims[0] * dims[1], plan[4])
+    d.counts, d.offsets = plan[2].data_ptr(), plan[3].data_ptr()
+    return d
+
+
+def expert_product(rows: torch.Tensor, weights: torch.Tensor, plan: ExpertPlan,
+                   out: torch.Tensor = None, stream: torch.cuda.Stream = None) -> torch.Tensor:
+    """Expert-major rows [rows,M] times their experts' weights, an [E,N,M] view
+    of any strides -> [rows,N]: ``out[r] = weights[e(r)] @ rows[r]``, bfloat16 or
+    float16, summed in float32 and rounded once.
+
+    Gap rows (``plan.align``) are written as zeros, rows behind the last expert
+    are left as they were; what such rows hold in ``rows`` does not matter.  The
+    gradient of ``rows`` is ``expert_product(grad, weights.transpose(1, 2), plan)``,
+    that of ``weights`` :func:`expert_weight_grad`.  No graph is recorded: rows
+    or weights that require a gradient are refused while grad mode is on.
+    """
+    typ = _product_rows(rows, "rows")
+    _unrecorded(rows, "rows", "expert_product with the transposed weights")
+    n, M = _matrix(rows, "rows")
+    dims = _check_plan(plan)
+    if not (isinstance(weights, torch.Tensor) and weights.is_cuda):
+        _product_rows(weights, "weights")                  # raises
+    w = weights.shape
+    if weights.dtype != rows.dtype or len(w) != 3 or w[0] != dims[3] or w[2] != M:
+        raise ValueError("weights must be a %s view of shape [%d,N,%d]"
+                         % (rows.dtype, dims[3], M))
+    _unrecorded(weights, "weights", "expert_weight_grad")
+    d = _product_desc(typ, plan, dims, n, w[1], M)
+    out = _rows_out(out, stream, rows, (n, w[1]), rows.dtype, "out")
+    d.packed, d.weights, d.out = rows.data_ptr(), weights.data_ptr(), out.data_ptr()
+    d.weight_strides = weights.stride()
+    _expert_call("vf_expert_product", d, stream, rows)
+    return out
+
+
+def expert_weight_grad(grad: torch.Tensor, rows: torch.Tensor, plan: ExpertPlan,
+                       out: torch.Tensor = None, dtype: torch.dtype = None,
+                       stream: torch.cuda.Stream = None) -> torch.Tensor:
+    """The gradient of :func:`expert_product`'s weights [E,N,M], given the
+    gradient ``grad`` [rows,N] of its result: for each expert the sum over its
+    rows of the outer products of ``grad[r]`` and ``rows[r]``; zeros for an expert
+    without rows.
+
+    ``dtype`` is the result's: that of ``rows`` (default) or float32.  Gap rows
+    and the rows behind the last expert are not read into it.
+    """
+    typ = _product_rows(grad, "grad")
+    if _product_rows(rows, "rows") != typ:
+        raise ValueError("grad and rows must have one type")
+    n, N = _matrix(grad, "grad")
+    n_rows, M = _matrix(rows, "rows")
+    if n_rows != n:
+        raise ValueError("grad and rows must have the same number of rows")
+    if dtype is None:
+        dtype = rows.dtype if out is None else out.dtype
+    if dtype not in (rows.dtype, torch.float32):
+        raise ValueError("dtype must be that of rows or torch.float32")
+    dims = _check_plan(plan)
+    d = _product_desc(typ, plan, dims, n, N, M)
+    out = _rows_out(out, stream, rows, (dims[3], N, M), dtype, "out")
+    if dtype == torch.float32:
+        d.out_type = 2
+    d.packed, d.grad, d.grad_weights = rows.data_ptr(), grad.data_ptr(), out.data_ptr()
+    _expert_call("vf_expert_weight_grad", d, stream, grad)
+    return out

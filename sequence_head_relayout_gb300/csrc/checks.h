@@ -65,7 +65,8 @@ inline bool overlap(const Range &a, const Range &b) {
     return a.lo < b.lo + b.len && b.lo < a.lo + a.len;
 }
 
-inline int check_pointer(const void *p) {
+// `device`: page-locked host memory is refused too.
+inline int check_pointer(const void *p, bool device = false) {
     cudaPointerAttributes at;
     if (cudaPointerGetAttributes(&at, p) != cudaSuccess) {
         cudaGetLastError();
@@ -73,7 +74,7 @@ inline int check_pointer(const void *p) {
     }
     if (at.type == cudaMemoryTypeUnregistered) return VF_ERR_ARG;
     // page-locked host memory must be mapped at the same address on the device
-    if (at.type == cudaMemoryTypeHost && at.devicePointer != p) return VF_ERR_ARG;
+    if (at.type == cudaMemoryTypeHost && (device || at.devicePointer != p)) return VF_ERR_ARG;
     if (at.type == cudaMemoryTypeDevice) {
         int dev = -1;
         if (cudaGetDevice(&dev) != cudaSuccess) {

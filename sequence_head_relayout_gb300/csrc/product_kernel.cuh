@@ -1,0 +1,764 @@
+// Device side of the experts' products (include/vf_relayout.h, "Expert
+// products"): products of 16-bit rows grouped by expert, on the fifth-generation
+// tensor cores.
+//
+// rows     out[r, n] = sum_m packed[r, m] * weights[e(r), n, m]
+// weights  grad_weights[e, n, m] = sum over e's rows r of grad[r, n] * packed[r, m]
+//
+// Both are D[i, j] = sum_k A[i, k] * B[j, k] for each expert.  A holds output
+// features: the weights [n][m], or the gradient's columns.  B holds the expert's
+// rows [r][m], or the packed rows' columns.  With the features on the
+// instruction's M side (128 rows of a CTA) and the rows on its N side (16 to 256
+// of them, chosen tile by tile) an expert with few rows wastes no tensor work
+// beyond a multiple of 16 rows, and one that has none reads no weights.
+//
+// A CTA is a pipeline of warps over its tiles: producers fill a ring of stages
+// (64 k of A and of B, 128-byte swizzle), one thread issues the products into one of
+// two accumulators in tensor memory, and four warps round the other one and store
+// it.  The segments are read from the plan on the device; every role walks the
+// tiles for itself.
+//
+// No wait is without an end: a role that waits for kWaitNs gives up, sets the
+// CTA's flag, and what is still to be stored is stored as NaN.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cstdint>
+
+namespace vfp {
+
+constexpr int kBlockK = 64;                    // k of a stage: 128 bytes of 16-bit elements
+constexpr int kTileM = 128;                    // features of a CTA's tile
+constexpr int kStageA = kTileM * kBlockK * 2;  // bytes
+constexpr int kMaxStages = 12;
+constexpr int kEpilogueWarps = 4;
+constexpr int kStagingBytes = 4608;            // per epilogue warp: 32 rows of 144 bytes
+constexpr int kFillWarps = 8;                  // producers of operands that TMA cannot take
+constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr uint64_t kDrainNs = 100000000ull;
+constexpr uint32_t kAll = 0xFFFFFFFFu;
+
+struct ProductArgs {
+    CUtensorMap a_map, b_map;     // not used by the fill producers
+    const int32_t *counts, *offsets;
+    const uint16_t *a, *b;        // the fill producers' operands and element strides
+    int64_t a_expert, a_i, a_k, b_i, b_k;
+    void *out;                    // rows: [rows][feat]; weights: [E][feat][cols]
+    int32_t E, rows;
+    int32_t feat, cols, red;      // features; weights: columns; rows: length of the sums
+    int32_t feat_tiles, col_tiles;
+    int32_t tile_n;               // most rows (columns) of a tile
+    int32_t box;                  // rows of one copy of B (rows form)
+    int32_t stages, stage_bytes;
+    int32_t acc_stride, tmem_cols;
+    int32_t bf16, gaps, vec, out32;
+};
+
+// ---- synchronisation -----------------------------------------------------------
+
+__device__ __forceinline__ uint32_t smem_addr(const void *p) {
+    return uint32_t(__cvta_generic_to_shared(p));
+}
+
+__device__ __forceinline__ uint64_t now_ns() {
+    uint64_t t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    return t;
+}
+
+__device__ __forceinline__ void barrier_init(uint32_t bar, int count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+
+__device__ __forceinline__ bool barrier_try(uint32_t bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(done) : "r"(bar), "r"(parity) : "memory");
+    return done != 0;
+}
+
+// Waits for the phase of the given parity to end, for kWaitNs at most (and more_ns
+// for what may be due in between); false when it gave up, or another role did.
+__device__ __forceinline__ bool barrier_wait(uint32_t bar, uint32_t parity, volatile int *failed,
+                                             uint64_t more_ns = 0) {
+    for (int i = 0; i < 64; ++i)
+        if (barrier_try(bar, parity)) return true;
+    const uint64_t start = now_ns();
+    while (!barrier_try(bar, parity)) {
+        if (*failed) return false;
+        if (now_ns() - start > kWaitNs + more_ns) {
+            *failed = 1;
+            return false;
+        }
+    }
+    return true;
+}
+
+__device__ __forceinline__ void barrier_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// Arrival at the barrier of the pair's first CTA.
+__device__ __forceinline__ void barrier_arrive_first(uint32_t bar) {
+    asm volatile("{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %0, 0;\n\t"
+                 "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [r];\n\t}"
+                 ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void barrier_expect(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;"
+                 ::"r"(bar), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// ---- copies --------------------------------------------------------------------
+
+// The barrier of a pair's copies is that of its first CTA.
+template <int CTAS>
+__device__ __forceinline__ uint32_t first_barrier(uint32_t bar) {
+    if constexpr (CTAS == 1) return bar;
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(bar));
+    return r;
+}
+
+template <int CTAS>
+__device__ __forceinline__ void copy_2d(uint32_t dst, const CUtensorMap *map, uint32_t bar,
+                                        int x, int y) {
+    if constexpr (CTAS == 1)
+        asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile"
+                     ".mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];"
+                     ::"r"(dst), "l"(map), "r"(bar), "r"(x), "r"(y) : "memory");
+    else
+        asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile"
+                     ".mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];"
+                     ::"r"(dst), "l"(map), "r"(bar), "r"(x), "r"(y) : "memory");
+}
+
+template <int CTAS>
+__device__ __forceinline__ void copy_3d(uint32_t dst, const CUtensorMap *map, uint32_t bar,
+                                        int x, int y, int z) {
+    if constexpr (CTAS == 1)
+        asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile"
+                     ".mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];"
+                     ::"r"(dst), "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z) : "memory");
+    else
+        asm volatile("cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile"
+                     ".mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];"
+                     ::"r"(dst), "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z) : "memory");
+}
+
+// ---- tensor cores --------------------------------------------------------------
+
+template <int CTAS>
+__device__ __forceinline__ void tmem_alloc(uint32_t dst, uint32_t cols) {
+    if constexpr (CTAS == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                     ::"r"(dst), "r"(cols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
+                     ::"r"(dst), "r"(cols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+}
+
+template <int CTAS>
+__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
+    if constexpr (CTAS == 1)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;"
+                     ::"r"(addr), "r"(cols) : "memory");
+    else
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;"
+                     ::"r"(addr), "r"(cols) : "memory");
+}
+
+template <int CTAS>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t instr,
+                                    bool accumulate) {
+    if constexpr (CTAS == 1)
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                     "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+                     ::"r"(d), "l"(a), "l"(b), "r"(instr), "r"(uint32_t(accumulate)) : "memory");
+    else
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                     "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+                     ::"r"(d), "l"(a), "l"(b), "r"(instr), "r"(uint32_t(accumulate)) : "memory");
+}
+
+// The barrier (of both CTAs of a pair) is arrived at when the products issued so
+// far are done.
+template <int CTAS>
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+    if constexpr (CTAS == 1)
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+                     ::"r"(bar) : "memory");
+    else
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster"
+                     ".multicast::cluster.b64 [%0], %1;"
+                     ::"r"(bar), "h"(uint16_t(3)) : "memory");
+}
+
+__device__ __forceinline__ void fence_before() {
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void fence_after() {
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+
+// 32 columns of the warp's 32 lanes: lane l's float of column c in v[c].
+__device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+          "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]),
+          "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]),
+          "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+          "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]),
+          "=r"(v[31])
+        : "r"(addr) : "memory");
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+// Descriptor of an operand in shared memory, 128-byte swizzle.  k contiguous: rows of
+// 128 bytes, groups of 8 rows 1,024 bytes apart.  i contiguous: 64 i to a row of 128
+// bytes, one row for each k, groups of 8 k 1,024 bytes apart and the next 64 i
+// 64 rows on.
+constexpr uint64_t kDescBase = (uint64_t(1) << 46) | (uint64_t(2) << 61) |
+                               (uint64_t(1024 >> 4) << 32) |
+                               (uint64_t((kBlockK * 128) >> 4) << 16);
+
+__device__ __forceinline__ uint64_t operand(uint32_t addr) {
+    return kDescBase | uint64_t((addr & 0x3FFFF) >> 4);
+}
+
+// Bytes from one step of 16 k to the next.
+template <bool MN> constexpr uint32_t kStepBytes = MN ? 16 * 128 : 32;
+
+// ---- tiles ---------------------------------------------------------------------
+
+struct Tile {
+    int e, f0;         // expert, first feature
+    int row0, valid;   // rows: first row and rows of the tile; weights: of the expert
+    int c0;            // weights: first column
+    int n;             // rows or columns of the product, a multiple of 16 CTAS
+    int kblocks;
+    int gap;           // rows to be written as zeros behind the tile
+};
+
+// The CTA's (pair's) tiles, by all lanes of a warp together.  Rows form: the
+// experts' tiles in order, an expert's row tiles fastest (they share a tile of
+// weights), each expert's rows cut into equal tiles.  A lane holds four experts, a
+// warp 128 at a time.
+template <int CTAS, bool WEIGHTS>
+struct Tiles {
+    static constexpr int kStep = 16 * CTAS;
+    const ProductArgs &a;
+    int lane;
+    int64_t t, step;              // this tile, and what is added for the next
+    // rows form
+    int base = -128;              // first expert of the warp's 128
+    int64_t before = 0;           // tiles before it
+    int64_t total = 0;            // tiles of the 128
+    int64_t first = 0;            // tiles of the 128 before the lane's four experts
+    int count[4], begin[4];
+
+    __device__ __forceinline__ explicit Tiles(const ProductArgs &args)
+        : a(args), lane(int(threadIdx.x & 31)), t(blockIdx.x / CTAS), step(gridDim.x / CTAS) {}
+
+    // Rows of an expert that exist, whatever the plan says.
+    __device__ __forceinline__ void segment(int e, int &begin_, int &count_) const {
+        begin_ = min(max(a.offsets[e], 0), a.rows);
+        count_ = min(max(a.counts[e], 0), a.rows - begin_);
+    }
+
+    __device__ __forceinline__ int64_t tiles_of(int n) const {
+        return int64_t((n + a.tile_n - 1) / a.tile_n) * a.feat_tiles;
+    }
+
+    __device__ bool next(Tile &o) {
+        const bool there = WEIGHTS ? next_weights(o) : next_rows(o);
+        t += step;
+        return there;
+    }
+
+    __device__ bool next_weights(Tile &o) {
+        const int64_t each = int64_t(a.feat_tiles) * a.col_tiles;
+        if (t >= each * a.E) return false;
+        o.e = int(t / each);
+        const int in = int(t - o.e * each);
+        o.f0 = in % a.feat_tiles * (kTileM * CTAS);
+        o.c0 = in / a.feat_tiles * a.tile_n;
+        o.n = (min(a.tile_n, a.cols - o.c0) + kStep - 1) / kStep * kStep;
+        segment(o.e, o.row0, o.valid);
+        o.kblocks = (o.valid + kBlockK - 1) / kBlockK;
+        o.gap = 0;
+        return true;
+    }
+
+    __device__ bool next_rows(Tile &o) {
+        while (t >= before + total) {
+            base += 128;
+            if (base >= a.E) return false;
+            before += total;
+            int64_t sum = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int e = base + 4 * lane + i;
+                count[i] = begin[i] = 0;
+                if (e < a.E) segment(e, begin[i], count[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum += tiles_of(count[i]);
+            first = sum;
+#pragma unroll
+            for (int o2 = 1; o2 < 32; o2 <<= 1) {
+                const int64_t other = __shfl_up_sync(kAll, first, o2);
+                if (lane >= o2) first += other;
+            }
+            total = __shfl_sync(kAll, first, 31);
+            first -= sum;
+        }
+        // the last lane whose experts start at or before the tile holds it
+        const int64_t at = t - before;
+        const int owner = 31 - __clz(__ballot_sync(kAll, first <= at));
+        int64_t rest = at - first;
+        int i = 0, c = count[0], b = begin[0];
+#pragma unroll
+        for (int j = 1; j < 4; ++j)
+            if (i == j - 1 && rest >= tiles_of(c)) {
+                rest -= tiles_of(c);
+                i = j;
+                c = count[j];
+                b = begin[j];
+            }
+        c = __shfl_sync(kAll, c, owner);
+        b = __shfl_sync(kAll, b, owner);
+        rest = __shfl_sync(kAll, rest, owner);
+        o.e = base + 4 * owner + __shfl_sync(kAll, i, owner);
+        const int row_tiles = (c + a.tile_n - 1) / a.tile_n;
+        const int part = ((c + row_tiles - 1) / row_tiles + kStep - 1) / kStep * kStep;
+        const int f = int(rest / row_tiles), r = int(rest - int64_t(f) * row_tiles);
+        o.f0 = f * (kTileM * CTAS);
+        o.row0 = b + r * part;
+        o.valid = min(part, c - r * part);
+        o.n = (o.valid + kStep - 1) / kStep * kStep;
+        o.c0 = 0;
+        o.kblocks = (a.red + kBlockK - 1) / kBlockK;
+        o.gap = 0;
+        if (a.gaps && r == row_tiles - 1)
+            o.gap = max(0, min(a.offsets[o.e + 1], a.rows) - (b + c));
+        return true;
+    }
+};
+
+// ---- producers -----------------------------------------------------------------
+
+// Fills 128 rows of 64 k of an operand, k contiguous, from any element strides;
+// zeros past i_end and k_end.  By the kFillWarps warps; `warp` is the number among
+// them.  The lanes lie along the dimension with the smaller stride.
+__device__ __forceinline__ void fill(uint8_t *dst, const uint16_t *src, int64_t s_i, int64_t s_k,
+                                     int i_end, int k_end, int warp, int lane) {
+    if (s_k <= s_i) {
+        constexpr int kRows = kTileM / kFillWarps;
+        uint16_t lo[kRows], hi[kRows];
+        const int k = 2 * lane;
+#pragma unroll
+        for (int j = 0; j < kRows; ++j) {
+            const int i = j * kFillWarps + warp;
+            const uint16_t *p = src + i * s_i + k * s_k;
+            lo[j] = i < i_end && k < k_end ? p[0] : uint16_t(0);
+            hi[j] = i < i_end && k + 1 < k_end ? p[s_k] : uint16_t(0);
+        }
+#pragma unroll
+        for (int j = 0; j < kRows; ++j) {
+            const int i = j * kFillWarps + warp;
+            *reinterpret_cast<uint32_t *>(dst + i * 128 + (((k >> 3) ^ (i & 7)) << 4) +
+                                          (k & 7) * 2) = uint32_t(lo[j]) | uint32_t(hi[j]) << 16;
+        }
+    } else {
+        static_assert(kFillWarps == kBlockK / 8, "a warp for every 8 k");
+#pragma unroll
+        for (int j = 0; j < kTileM / 32; ++j) {
+            const int i = j * 32 + lane;
+            uint16_t v[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const int k = warp * 8 + q;
+                v[q] = i < i_end && k < k_end ? src[i * s_i + k * s_k] : uint16_t(0);
+            }
+            uint4 w;
+            w.x = uint32_t(v[0]) | uint32_t(v[1]) << 16;
+            w.y = uint32_t(v[2]) | uint32_t(v[3]) << 16;
+            w.z = uint32_t(v[4]) | uint32_t(v[5]) << 16;
+            w.w = uint32_t(v[6]) | uint32_t(v[7]) << 16;
+            *reinterpret_cast<uint4 *>(dst + i * 128 + ((warp ^ (i & 7)) << 4)) = w;
+        }
+    }
+}
+
+// ---- epilogue ------------------------------------------------------------------
+
+__device__ __forceinline__ uint32_t round2(float lo, float hi, bool bf16) {
+    if (bf16) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&b);
+    }
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// Rows form: v[c] is row c of 32 from `row` on (`valid` of them exist), feature f +
+// lane.  Through shared memory, so that a row's 32 features leave as 64 bytes.
+__device__ __forceinline__ void store_rows(const ProductArgs &a, const uint32_t (&v)[32],
+                                           int64_t row, int valid, int f, int lane,
+                                           uint8_t *staging) {
+    uint16_t *out = static_cast<uint16_t *>(a.out);
+    uint32_t w[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+        w[j] = round2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]), a.bf16);
+    if (!a.vec) {
+        if (f + lane >= a.feat) return;
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (j < valid)
+                out[(row + j) * a.feat + f + lane] = uint16_t(w[j / 2] >> (j % 2 * 16));
+        return;
+    }
+    uint16_t *s = reinterpret_cast<uint16_t *>(staging);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) s[j * 32 + lane] = uint16_t(w[j / 2] >> (j % 2 * 16));
+    __syncwarp();
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const int j = q * 8 + lane / 4, c = f + lane % 4 * 8;
+        if (j < valid && c < a.feat)
+            *reinterpret_cast<uint4 *>(out + (row + j) * a.feat + c) =
+                *reinterpret_cast<const uint4 *>(s + j * 32 + lane % 4 * 8);
+    }
+    __syncwarp();
+}
+
+// Zeros for rows row .. row + n - 1, 32 features from f on.
+__device__ __forceinline__ void zero_rows(const ProductArgs &a, int64_t row, int n, int f,
+                                          int lane) {
+    uint16_t *out = static_cast<uint16_t *>(a.out);
+    if (!a.vec) {
+        if (f + lane < a.feat)
+            for (int j = 0; j < n; ++j) out[(row + j) * a.feat + f + lane] = 0;
+        return;
+    }
+    const int c = f + lane % 4 * 8;
+    if (c < a.feat)
+        for (int j = lane / 4; j < n; j += 8)
+            *reinterpret_cast<uint4 *>(out + (row + j) * a.feat + c) = make_uint4(0, 0, 0, 0);
+}
+
+// Weights form: v[c] is column c0 + c of feature f + lane of expert e.
+__device__ __forceinline__ void store_weights(const ProductArgs &a, const uint32_t (&v)[32],
+                                              int e, int f, int c0, int lane,
+                                              uint8_t *staging) {
+    const int64_t first = (int64_t(e) * a.feat + f) * a.cols + c0;
+    const int rows = min(32, a.feat - f), cols = min(32, a.cols - c0);
+    if (a.out32) {
+        // rows of 144 bytes: both sides of the exchange without bank conflicts
+        float *out = static_cast<float *>(a.out) + first;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<uint4 *>(staging + lane * 144 + j * 16) =
+                make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+        __syncwarp();
+        if (a.vec) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const int r = q * 4 + lane / 8, c = lane % 8 * 4;
+                if (r < rows && c < cols)
+                    *reinterpret_cast<uint4 *>(out + int64_t(r) * a.cols + c) =
+                        *reinterpret_cast<const uint4 *>(staging + r * 144 + c * 4);
+            }
+        } else if (lane < cols) {
+#pragma unroll 8
+            for (int r = 0; r < rows; ++r)
+                out[int64_t(r) * a.cols + lane] =
+                    *reinterpret_cast<const float *>(staging + r * 144 + lane * 4);
+        }
+    } else {
+        uint16_t *out = static_cast<uint16_t *>(a.out) + first;
+        uint32_t w[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            w[j] = round2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]), a.bf16);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<uint4 *>(staging + lane * 80 + j * 16) =
+                make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+        __syncwarp();
+        if (a.vec) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int r = q * 8 + lane / 4, c = lane % 4 * 8;
+                if (r < rows && c < cols)
+                    *reinterpret_cast<uint4 *>(out + int64_t(r) * a.cols + c) =
+                        *reinterpret_cast<const uint4 *>(staging + r * 80 + c * 2);
+            }
+        } else if (lane < cols) {
+#pragma unroll 8
+            for (int r = 0; r < rows; ++r)
+                out[int64_t(r) * a.cols + lane] =
+                    *reinterpret_cast<const uint16_t *>(staging + r * 80 + lane * 2);
+        }
+    }
+    __syncwarp();
+}
+
+// ---- the kernel ----------------------------------------------------------------
+
+struct Control {
+    uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2];
+    uint32_t tmem;
+    int failed;
+};
+
+// Shared memory: stages, staging, Control; 1,024 more for the alignment.
+__host__ __device__ constexpr int64_t shared_bytes(int stages, int stage_bytes) {
+    return int64_t(stages) * stage_bytes + kEpilogueWarps * kStagingBytes +
+           int64_t(sizeof(Control)) + 1024;
+}
+
+// CTAS     CTAs that share a tile (2: a pair, 256 features, each CTA holds half of B)
+// WEIGHTS  the weights' gradient, else the rows' product
+// A_MN     the first operand is stored with i contiguous
+// FILL     operands come by plain loads, k contiguous in shared memory
+template <int CTAS, bool WEIGHTS, bool A_MN, bool FILL>
+__global__ void __launch_bounds__(FILL ? 512 : 256, 1)
+expert_product(const __grid_constant__ ProductArgs a) {
+    static_assert(!FILL || (CTAS == 1 && !A_MN), "fill producers: single CTAs, k contiguous");
+    constexpr bool B_MN = WEIGHTS && !FILL;
+    extern __shared__ uint8_t raw[];
+    uint8_t *const smem = raw + (1024 - (smem_addr(raw) & 1023)) % 1024;
+    uint8_t *const staging = smem + a.stages * a.stage_bytes;
+    Control &ctl = *reinterpret_cast<Control *>(staging + kEpilogueWarps * kStagingBytes);
+    volatile int *const failed = &ctl.failed;
+    const int warp = int(threadIdx.x >> 5), lane = int(threadIdx.x & 31);
+    const uint32_t rank = CTAS == 1 ? 0 : cluster_rank();
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < a.stages; ++s) {
+            barrier_init(smem_addr(&ctl.full[s]), FILL ? kFillWarps : 1);
+            barrier_init(smem_addr(&ctl.empty[s]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            barrier_init(smem_addr(&ctl.acc_full[i]), 1);
+            barrier_init(smem_addr(&ctl.acc_empty[i]), kEpilogueWarps * CTAS);
+        }
+        ctl.failed = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 2) tmem_alloc<CTAS>(smem_addr(&ctl.tmem), uint32_t(a.tmem_cols));
+    fence_before();
+    __syncthreads();
+    if constexpr (CTAS > 1) cluster_sync();
+    fence_after();
+    const uint32_t tmem = ctl.tmem;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    Tile o;
+    int s = 0;                                       // stage and its phase
+    uint32_t phase = 0;
+    const auto advance = [&] {
+        if (++s == a.stages) {
+            s = 0;
+            phase ^= 1;
+        }
+    };
+
+    if (!FILL && warp == 0) {
+        // copies: A's half and B's half of every k block
+        Tiles<CTAS, WEIGHTS> tiles(a);
+        bool ok = true;
+        while (ok && tiles.next(o)) {
+            const int half = o.n / CTAS;             // this CTA's share of B
+            const int boxes = WEIGHTS ? (half + 63) / 64 : (half + a.box - 1) / a.box;
+            const uint32_t bytes =
+                uint32_t(CTAS * (kStageA + boxes * (WEIGHTS ? 64 : a.box) * 128));
+            const int fa = o.f0 + int(rank) * kTileM;
+            if (lane == 0) {
+                for (int kb = 0; kb < o.kblocks; ++kb) {
+                    ok = barrier_wait(smem_addr(&ctl.empty[s]), phase ^ 1, failed);
+                    if (!ok) break;
+                    const uint32_t bar = first_barrier<CTAS>(smem_addr(&ctl.full[s]));
+                    const uint32_t da = smem_addr(smem + s * a.stage_bytes), db = da + kStageA;
+                    if (rank == 0) barrier_expect(smem_addr(&ctl.full[s]), bytes);
+                    if constexpr (WEIGHTS) {
+                        // The last block's rows lie at its end, behind zeros: the
+                        // maps' second coordinate runs over the same rows as the third,
+                        // so that what lies before it is outside the tensor.
+                        const int y = min(0, o.valid - (kb + 1) * kBlockK);
+                        const int z = o.row0 + kb * kBlockK;
+                        for (int j = 0; j < 2; ++j)
+                            copy_3d<CTAS>(da + j * 8192, &a.a_map, bar, fa + j * 64, y, z);
+                        for (int j = 0; j < boxes; ++j)
+                            copy_3d<CTAS>(db + j * 8192, &a.b_map, bar,
+                                          o.c0 + int(rank) * half + j * 64, y, z);
+                    } else {
+                        const int k = kb * kBlockK;
+                        if constexpr (A_MN) {
+                            for (int j = 0; j < 2; ++j)
+                                copy_3d<CTAS>(da + j * 8192, &a.a_map, bar, fa + j * 64, k, o.e);
+                        } else {
+                            copy_3d<CTAS>(da, &a.a_map, bar, k, fa, o.e);
+                        }
+                        for (int j = 0; j < boxes; ++j)
+                            copy_2d<CTAS>(db + j * a.box * 128, &a.b_map, bar, k,
+                                          o.row0 + int(rank) * half + j * a.box);
+                    }
+                    advance();
+                }
+            }
+            ok = __shfl_sync(kAll, int(ok), 0);
+        }
+    } else if (warp == 1 && rank == 0) {
+        // products; one thread issues them
+        const uint32_t instr = (1u << 4) | (a.bf16 ? (1u << 7) | (1u << 10) : 0u) |
+                               (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u) |
+                               (uint32_t(kTileM * CTAS / 16) << 24);
+        Tiles<CTAS, WEIGHTS> tiles(a);
+        uint32_t it = 0;
+        bool ok = true;
+        while (ok && tiles.next(o)) {
+            if (o.kblocks == 0) continue;
+            if (lane == 0) {
+                const uint32_t acc = it & 1, acc_phase = it >> 1 & 1;
+                ok = barrier_wait(smem_addr(&ctl.acc_empty[acc]), acc_phase ^ 1, failed);
+                fence_after();
+                const uint32_t d = tmem + acc * uint32_t(a.acc_stride);
+                const uint32_t in = instr | (uint32_t(o.n / 8) << 17);
+                for (int kb = 0; ok && kb < o.kblocks; ++kb) {
+                    ok = barrier_wait(smem_addr(&ctl.full[s]), phase, failed);
+                    if (!ok) break;
+                    fence_after();
+                    const uint32_t at = smem_addr(smem + s * a.stage_bytes);
+#pragma unroll
+                    for (int q = 0; q < kBlockK / 16; ++q)
+                        mma<CTAS>(d, operand(at + q * kStepBytes<A_MN>),
+                                  operand(at + kStageA + q * kStepBytes<B_MN>), in,
+                                  kb > 0 || q > 0);
+                    mma_commit<CTAS>(smem_addr(&ctl.empty[s]));
+                    advance();
+                }
+                if (ok) mma_commit<CTAS>(smem_addr(&ctl.acc_full[acc]));
+            }
+            ok = __shfl_sync(kAll, int(ok), 0);
+            ++it;
+        }
+    } else if (warp >= 4 && warp < 4 + kEpilogueWarps) {
+        Tiles<CTAS, WEIGHTS> tiles(a);
+        const int quarter = warp - 4;
+        uint8_t *const mine = staging + quarter * kStagingBytes;
+        uint32_t it = 0;
+        while (tiles.next(o)) {
+            const uint32_t acc = it & 1, acc_phase = it >> 1 & 1;
+            bool ok = true;
+            if (o.kblocks > 0) {
+                // (a sum of 2^20 blocks takes a second)
+                ok = barrier_wait(smem_addr(&ctl.acc_full[acc]), acc_phase, failed,
+                                  uint64_t(o.kblocks) * 8192);
+                ok = __all_sync(kAll, int(ok));
+                fence_after();
+                ++it;
+            }
+            const int f = o.f0 + int(rank) * kTileM + quarter * 32;
+            const uint32_t d = tmem + acc * uint32_t(a.acc_stride) + (uint32_t(quarter * 32) << 16);
+            const int n = WEIGHTS ? min(o.n, a.cols - o.c0) : o.valid;
+            for (int c = 0; c < n; c += 32) {
+                uint32_t v[32];
+                if (o.kblocks > 0 && ok) {
+                    tmem_load(d + uint32_t(c), v);
+                } else {
+                    // an empty sum, or one that was given up: NaN
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = ok ? 0u : 0x7FC00000u;
+                }
+                if (f >= a.feat) continue;           // all lanes alike
+                if constexpr (WEIGHTS)
+                    store_weights(a, v, o.e, f, o.c0 + c, lane, mine);
+                else
+                    store_rows(a, v, int64_t(o.row0) + c, n - c, f, lane, mine);
+            }
+            if (o.kblocks > 0 && ok) {
+                fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (CTAS == 1) barrier_arrive(smem_addr(&ctl.acc_empty[acc]));
+                    else barrier_arrive_first(smem_addr(&ctl.acc_empty[acc]));
+                }
+            }
+            if (!WEIGHTS && o.gap > 0 && f < a.feat)
+                zero_rows(a, int64_t(o.row0) + o.valid, o.gap, f, lane);
+        }
+    } else if (FILL && warp >= 8) {
+        Tiles<CTAS, WEIGHTS> tiles(a);
+        const int w = warp - 8;
+        bool ok = true;
+        while (ok && tiles.next(o)) {
+            const uint16_t *pa, *pb;
+            int k_end;
+            if constexpr (WEIGHTS) {
+                pa = a.a + o.row0 * a.a_k + o.f0 * a.a_i;
+                pb = a.b + o.row0 * a.b_k + o.c0 * a.b_i;
+                k_end = o.valid;
+            } else {
+                pa = a.a + o.e * a.a_expert + o.f0 * a.a_i;
+                pb = a.b + o.row0 * a.b_i;
+                k_end = a.red;
+            }
+            const int b_end = WEIGHTS ? min(o.n, a.cols - o.c0) : o.valid;
+            for (int kb = 0; ok && kb < o.kblocks; ++kb) {
+                ok = barrier_wait(smem_addr(&ctl.empty[s]), phase ^ 1, failed);
+                ok = __all_sync(kAll, int(ok));
+                if (!ok) break;
+                uint8_t *da = smem + s * a.stage_bytes;
+                const int k = kb * kBlockK;
+                fill(da, pa + k * a.a_k, a.a_i, a.a_k, a.feat - o.f0, k_end - k, w, lane);
+                fill(da + kStageA, pb + k * a.b_k, a.b_i, a.b_k, b_end, k_end - k, w, lane);
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) barrier_arrive(smem_addr(&ctl.full[s]));
+                advance();
+            }
+        }
+    }
+
+    __syncthreads();
+    if (*failed) {
+        // copies and products that were on their way when a role gave up land first
+        const uint64_t start = now_ns();
+        while (now_ns() - start < kDrainNs) {}
+    }
+    fence_before();
+    __syncthreads();
+    if constexpr (CTAS > 1) cluster_sync();
+    fence_after();
+    if (warp == 2) tmem_free<CTAS>(tmem, uint32_t(a.tmem_cols));
+}
+
+}  // namespace vfp

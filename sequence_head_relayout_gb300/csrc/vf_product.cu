@@ -1,0 +1,233 @@
+// Host side of the experts' products (include/vf_relayout.h, "Expert products"):
+// argument checks, the choice of a form, the tensor maps and the launches.  The
+// kernel is in product_kernel.cuh.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <cstring>
+
+#include "call.h"
+#include "checks.h"
+#include "product_kernel.cuh"
+#include "vf_relayout.h"
+
+namespace {
+
+using namespace vfc;
+
+constexpr int64_t kMaxFeatures = int64_t(1) << 20;       // N and M
+constexpr int64_t kMaxAlign = 65536;
+constexpr int64_t kSharedMemory = 227 * 1024;
+
+using EncodeTiled = decltype(&cuTensorMapEncodeTiled);
+
+// The driver's encoder; it has no device state, and is looked up once.
+EncodeTiled encoder() {
+    static const EncodeTiled fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
+                                             cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            return EncodeTiled(nullptr);
+        }
+        return reinterpret_cast<EncodeTiled>(p);
+    }();
+    return fn;
+}
+
+// A map of 16-bit elements, innermost dimension contiguous; strides in elements
+// from the second dimension on; boxes of 64 elements (128 bytes, swizzled).
+int make_map(CUtensorMap *map, bool bf16, int nd, const void *base, const int64_t *ext,
+             const int64_t *str, int64_t box1) {
+    const EncodeTiled fn = encoder();
+    if (fn == nullptr) return VF_ERR_CUDA;
+    cuuint64_t dims[3], strides[2];
+    cuuint32_t box[3] = {64, cuuint32_t(box1), 1};
+    const cuuint32_t steps[3] = {1, 1, 1};
+    for (int i = 0; i < nd; ++i) {
+        dims[i] = cuuint64_t(ext[i]);
+        if (i > 0) strides[i - 1] = cuuint64_t(str[i]) * 2;
+    }
+    const CUresult r =
+        fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+           cuuint32_t(nd), const_cast<void *>(base), dims, strides, box, steps,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? VF_OK : VF_ERR_CUDA;
+}
+
+bool aligned16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+// A stride (elements) that a map takes; those of one item are not used.
+bool map_stride(int64_t ext, int64_t *str, int64_t row) {
+    if (ext <= 1) {
+        *str = ceil_div(row, 8) * 8;
+        return true;
+    }
+    return *str > 0 && *str % 8 == 0 && *str < (int64_t(1) << 39);
+}
+
+int check_desc(const vf_product_desc *d) {
+    if (d == nullptr || (d->type != VF_TYPE_BF16 && d->type != VF_TYPE_F16)) return VF_ERR_ARG;
+    if (d->E < 1 || d->E > kMaxExperts || d->rows < 0 || d->rows > kMaxRows || d->slots < 0 ||
+        d->slots > kMaxSlots || d->align < 1 || d->align > kMaxAlign || d->N < 0 ||
+        d->N > kMaxFeatures || d->M < 0 || d->M > kMaxFeatures)
+        return VF_ERR_ARG;
+    return VF_OK;
+}
+
+// The dimensions of one of the kernel's forms.
+struct Form {
+    int64_t ctas, tile_n, box;
+};
+
+void set_form(vfp::ProductArgs *a, const Form &f, bool fill) {
+    const int64_t b_rows = f.tile_n / f.ctas;
+    a->tile_n = int32_t(f.tile_n);
+    a->box = int32_t(f.box);
+    a->stage_bytes = int32_t(vfp::kStageA + (fill ? vfp::kTileM : b_rows) * 128);
+    a->stages = 0;
+    while (a->stages < vfp::kMaxStages &&
+           vfp::shared_bytes(a->stages + 1, a->stage_bytes) <= kSharedMemory)
+        ++a->stages;
+    a->acc_stride = int32_t(std::max<int64_t>(32, f.tile_n));
+    a->tmem_cols = 64;
+    while (a->tmem_cols < 2 * a->acc_stride) a->tmem_cols *= 2;
+    a->feat_tiles = int32_t(ceil_div(a->feat, vfp::kTileM * f.ctas));
+    a->col_tiles = int32_t(ceil_div(a->cols, f.tile_n));
+}
+
+using Kernel = void (*)(vfp::ProductArgs);
+
+int launch_product(Kernel kernel, const vfp::ProductArgs &a, int64_t ctas, int64_t tiles,
+                   int threads, cudaStream_t stream) {
+    if (tiles == 0) return VF_OK;
+    // on every call, so that no state is kept per device, and always the same number
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             int(kSharedMemory)) != cudaSuccess) {
+        cudaGetLastError();
+        return VF_ERR_CUDA;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(std::min(kSMs / ctas, tiles) * ctas), 1, 1);
+    cfg.blockDim = dim3(unsigned(threads), 1, 1);
+    cfg.dynamicSmemBytes = size_t(vfp::shared_bytes(a.stages, a.stage_bytes));
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = unsigned(ctas);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    if (cudaLaunchKernelEx(&cfg, kernel, a) != cudaSuccess) {
+        cudaGetLastError();
+        return VF_ERR_CUDA;
+    }
+    return VF_OK;
+}
+
+vfp::ProductArgs make_args(const vf_product_desc *d) {
+    vfp::ProductArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.counts = d->counts;
+    a.offsets = d->offsets;
+    a.E = int32_t(d->E);
+    a.rows = int32_t(d->rows);
+    a.feat = int32_t(d->N);
+    a.bf16 = d->type == VF_TYPE_BF16;
+    a.gaps = d->align > 1;
+    return a;
+}
+
+int product(const vf_product_desc *d, cudaStream_t stream) {
+    int rc = check_desc(d);
+    if (rc != VF_OK) return rc;
+    int64_t n_packed, n_out, w_span;
+    const int64_t ext[3] = {d->E, d->N, d->M};
+    if (!mul_ok(d->rows, d->M, &n_packed) || !mul_ok(d->rows, d->N, &n_out))
+        return VF_ERR_OVERFLOW;
+    if ((rc = max_offset(ext, d->weight_strides, 3, &w_span)) != VF_OK) return rc;
+    if (n_out == 0) return VF_OK;                          // nothing to write
+    Ranges rs;
+    rs.add(d->counts, d->E, 4, false);
+    rs.add(d->offsets, d->E + 1, 4, false);
+    rs.add(d->packed, n_packed, 2, false);
+    if (!add_ok(w_span, 1, &w_span)) return VF_ERR_OVERFLOW;
+    if (d->M > 0) rs.add(d->weights, w_span, 2, false);
+    rs.add(d->out, n_out, 2, true);
+    if ((rc = rs.check(true)) != VF_OK) return rc;
+
+    vfp::ProductArgs a = make_args(d);
+    a.red = int32_t(d->M);
+    a.out = d->out;
+    a.vec = d->N % 8 == 0 && aligned16(d->out);
+    const int64_t most = std::min(d->E, d->rows);          // experts that have rows
+    a.a = static_cast<const uint16_t *>(d->weights);
+    a.b = static_cast<const uint16_t *>(d->packed);
+    a.a_expert = d->weight_strides[0];
+    a.a_i = d->weight_strides[1];
+    a.a_k = d->weight_strides[2];
+    a.b_i = d->M;
+    a.b_k = 1;
+    const Form f = {1, 128, 0};
+    set_form(&a, f, true);
+    const int64_t tiles = a.feat_tiles * (most + d->rows / f.tile_n);
+    return launch_product(vfp::expert_product<1, false, false, true>, a, f.ctas, tiles, 512,
+                          stream);
+}
+
+int weight_grad(const vf_product_desc *d, cudaStream_t stream) {
+    int rc = check_desc(d);
+    if (rc != VF_OK) return rc;
+    if (d->out_type != d->type && d->out_type != VF_TYPE_F32) return VF_ERR_ARG;
+    const int64_t size = type_size(d->out_type);
+    int64_t n_packed, n_grad, n_out;
+    if (!mul_ok(d->rows, d->M, &n_packed) || !mul_ok(d->rows, d->N, &n_grad) ||
+        !mul_ok(d->N * d->M, d->E, &n_out))                // N * M at most 2^40
+        return VF_ERR_OVERFLOW;
+    if (n_out == 0) return VF_OK;
+    Ranges rs;
+    rs.add(d->counts, d->E, 4, false);
+    rs.add(d->offsets, d->E + 1, 4, false);
+    rs.add(d->packed, n_packed, 2, false);
+    rs.add(d->grad, n_grad, 2, false);
+    rs.add(d->grad_weights, n_out, size, true);
+    if ((rc = rs.check(true)) != VF_OK) return rc;
+
+    vfp::ProductArgs a = make_args(d);
+    a.cols = int32_t(d->M);
+    a.out = d->grad_weights;
+    a.out32 = d->out_type == VF_TYPE_F32;
+    a.vec = d->M % (16 / size) == 0 && aligned16(d->grad_weights);
+    a.a = static_cast<const uint16_t *>(d->grad);
+    a.b = static_cast<const uint16_t *>(d->packed);
+    a.a_i = a.b_i = 1;
+    a.a_k = d->N;
+    a.b_k = d->M;
+    const Form f = {1, 128, 0};
+    set_form(&a, f, true);
+    const int64_t tiles = int64_t(a.feat_tiles) * a.col_tiles * a.E;
+    return launch_product(vfp::expert_product<1, true, false, true>, a, f.ctas, tiles, 512,
+                          stream);
+}
+
+}  // namespace
+
+extern "C" {
+
+int vf_expert_product(const vf_product_desc *d, vf_stream_t stream) {
+    return product(d, as_stream(stream));
+}
+
+int vf_expert_weight_grad(const vf_product_desc *d, vf_stream_t stream) {
+    return weight_grad(d, as_stream(stream));
+}
+
+}  // extern "C"
