@@ -146,6 +146,27 @@ vfp::ProductArgs make_args(const vf_product_desc *d) {
     return a;
 }
 
+// How tensor maps take the operands of a product: 0 not at all, 1 the weights with
+// unit stride along m, 2 along n.
+int weight_maps(const vf_product_desc *d) {
+    if (d->M == 0 || d->M % 8 || !aligned16(d->packed) || !aligned16(d->weights)) return 0;
+    int64_t e = d->weight_strides[0], n = d->weight_strides[1], m = d->weight_strides[2];
+    if (!map_stride(d->E, &e, 8)) return 0;
+    if ((m == 1 || d->M == 1) && map_stride(d->N, &n, 8)) return 1;
+    if ((n == 1 || d->N == 1) && map_stride(d->M, &m, 8)) return 2;
+    return 0;
+}
+
+// Rows of a tile, by the rows that an expert has on average.
+Form rows_form(const vf_product_desc *d, bool maps) {
+    if (!maps) return {1, 128, 0};
+    const int64_t mean = ceil_div(d->slots, d->E);
+    if (mean <= 8) return {1, 32, 16};
+    if (mean <= 32) return {1, 64, 16};
+    if (mean <= 96 || d->N <= 128) return {1, 128, 32};
+    return {2, 256, 32};
+}
+
 int product(const vf_product_desc *d, cudaStream_t stream) {
     int rc = check_desc(d);
     if (rc != VF_OK) return rc;
@@ -176,11 +197,28 @@ int product(const vf_product_desc *d, cudaStream_t stream) {
     a.a_k = d->weight_strides[2];
     a.b_i = d->M;
     a.b_k = 1;
-    const Form f = {1, 128, 0};
-    set_form(&a, f, true);
+    const int maps = weight_maps(d);
+    const Form f = rows_form(d, maps != 0);
+    set_form(&a, f, maps == 0);
     const int64_t tiles = a.feat_tiles * (most + d->rows / f.tile_n);
-    return launch_product(vfp::expert_product<1, false, false, true>, a, f.ctas, tiles, 512,
-                          stream);
+    if (maps == 0)
+        return launch_product(vfp::expert_product<1, false, false, true>, a, f.ctas, tiles, 512,
+                              stream);
+    const bool mn = maps == 2;
+    int64_t dims[3] = {mn ? d->N : d->M, mn ? d->M : d->N, d->E};
+    int64_t str[3] = {1, d->weight_strides[mn ? 2 : 1], d->weight_strides[0]};
+    map_stride(dims[1], &str[1], dims[0]);
+    map_stride(dims[2], &str[2], dims[0]);
+    if ((rc = make_map(&a.a_map, a.bf16, 3, d->weights, dims, str, mn ? 64 : 128)) != VF_OK)
+        return rc;
+    const int64_t b_dims[2] = {d->M, d->rows}, b_str[2] = {1, d->M};
+    if ((rc = make_map(&a.b_map, a.bf16, 2, d->packed, b_dims, b_str, f.box)) != VF_OK) return rc;
+    const Kernel kernel =
+        f.ctas == 2 ? (mn ? vfp::expert_product<2, false, true, false>
+                          : vfp::expert_product<2, false, false, false>)
+                    : (mn ? vfp::expert_product<1, false, true, false>
+                          : vfp::expert_product<1, false, false, false>);
+    return launch_product(kernel, a, f.ctas, tiles, 256, stream);
 }
 
 int weight_grad(const vf_product_desc *d, cudaStream_t stream) {
@@ -211,10 +249,21 @@ int weight_grad(const vf_product_desc *d, cudaStream_t stream) {
     a.a_i = a.b_i = 1;
     a.a_k = d->N;
     a.b_k = d->M;
-    const Form f = {1, 128, 0};
-    set_form(&a, f, true);
+    const bool maps = d->rows > 0 && d->N % 8 == 0 && d->M % 8 == 0 && aligned16(d->grad) &&
+                      aligned16(d->packed);
+    const Form f = maps ? Form{2, 256, 0} : Form{1, 128, 0};
+    set_form(&a, f, !maps);
     const int64_t tiles = int64_t(a.feat_tiles) * a.col_tiles * a.E;
-    return launch_product(vfp::expert_product<1, true, false, true>, a, f.ctas, tiles, 512,
+    if (!maps)
+        return launch_product(vfp::expert_product<1, true, false, true>, a, f.ctas, tiles, 512,
+                              stream);
+    // the second dimension steps over the rows as the third does (see the kernel)
+    const int64_t a_dims[3] = {d->N, 64, d->rows}, a_str[3] = {1, d->N, d->N};
+    const int64_t b_dims[3] = {d->M, 64, d->rows}, b_str[3] = {1, d->M, d->M};
+    if ((rc = make_map(&a.a_map, a.bf16, 3, d->grad, a_dims, a_str, 64)) != VF_OK ||
+        (rc = make_map(&a.b_map, a.bf16, 3, d->packed, b_dims, b_str, 64)) != VF_OK)
+        return rc;
+    return launch_product(vfp::expert_product<2, true, true, false>, a, f.ctas, tiles, 256,
                           stream);
 }
 
