@@ -530,6 +530,97 @@ typedef struct vf_product_desc {
 int vf_expert_product(const vf_product_desc *desc, vf_stream_t stream);
 int vf_expert_weight_grad(const vf_product_desc *desc, vf_stream_t stream);
 
+/*
+ * Gated activation of packed rows, between an expert's two products:
+ *   vf_expert_glu           out = silu(gate) * up,  silu(g) = g / (1 + exp(-g))
+ *   vf_expert_glu_backward  grad_gate = grad * up * s * (1 + gate * (1 - s)),
+ *                           grad_up = grad * gate * s,  s = 1 / (1 + exp(-gate))
+ * gate, up, grad and the results are [rows][F] views with any non-negative element
+ * strides (row, column); gate and up are usually the halves of one product's rows,
+ * and grad_gate and grad_up may be the halves of one buffer.  Arithmetic in float32,
+ * one rounding to the type.  Rows at and behind offsets[E] are left as they were,
+ * rows below it that hold no slot (slot_of negative) are written as zeros whatever
+ * they hold.  Ownership, streams, pointers and errors as for the expert relayouts.
+ */
+typedef struct vf_glu_desc {
+    int32_t type;               /* vf_type of all views */
+    int64_t E, rows, F;
+    const int32_t *slot_of;     /* [rows] */
+    const int32_t *offsets;     /* [E + 1] */
+    const void *gate;
+    int64_t gate_strides[2];
+    const void *up;
+    int64_t up_strides[2];
+    void *out;                  /* vf_expert_glu */
+    int64_t out_strides[2];
+    const void *grad;           /* the rest: vf_expert_glu_backward */
+    int64_t grad_strides[2];
+    void *grad_gate;
+    int64_t grad_gate_strides[2];
+    void *grad_up;
+    int64_t grad_up_strides[2];
+} vf_glu_desc;
+
+int vf_expert_glu(const vf_glu_desc *desc, vf_stream_t stream);
+int vf_expert_glu_backward(const vf_glu_desc *desc, vf_stream_t stream);
+
+/*
+ * Root-mean-square norm of token rows, with the residual's addition:
+ *   total = x + residual, rounded to the type (residual NULL: total is x, and is
+ *   not written), r = 1 / sqrt(mean(total^2) + eps),
+ *   out = total * r * weight.
+ * Sums and arithmetic in float32, one rounding to the type.  x, residual, total and
+ * out are [T][M] views with any non-negative element strides; weight is M contiguous
+ * elements of the type or float32.
+ * With a format (VF_TYPE_BF16 only), the float32 values of out are written as codes
+ * [T][M] and scales [T][ceil(M / group)] instead, each group of `group` columns
+ * (32, 64, 128 or 256) in the lossy transport's format: what vf_expert_restore
+ * takes.  A group that holds a NaN or an infinity is lost, as there.
+ *
+ * vf_rms_norm_backward: given x (the total), grad [T][M], the gradient of out, and
+ * grad_total (or NULL), that of the total by other paths,
+ *   grad_x = r * (w * grad - total * r^2 * mean(w * grad * total)) + grad_total,
+ *   grad_weight[m] = sum over t of grad * total * r    (float32),
+ * in a fixed order.  grad_x is the gradient of x and of residual.  With T = 0
+ * grad_weight is written as zeros.  workspace: vf_rms_norm_workspace() bytes,
+ * 16-byte aligned; calls that may run at the same time need one each.
+ *
+ * Limits (VF_ERR_ARG): T at most 2^30, M at most 2^24, eps finite and not negative.
+ * Ownership, streams, pointers and errors as for the expert relayouts.
+ */
+typedef struct vf_norm_desc {
+    int32_t type, weight_type;
+    int32_t format;             /* 0, or the vf_format of codes */
+    float eps;
+    int64_t T, M, group;
+    const void *x;
+    int64_t x_strides[2];
+    const void *weight;
+    const void *residual;
+    int64_t residual_strides[2];
+    void *total;                /* with a residual */
+    int64_t total_strides[2];
+    void *out;                  /* without a format */
+    int64_t out_strides[2];
+    void *codes;
+    float *scales;
+    const void *grad;           /* the rest: vf_rms_norm_backward */
+    int64_t grad_strides[2];
+    const void *grad_total;
+    int64_t grad_total_strides[2];
+    void *grad_x;
+    int64_t grad_x_strides[2];
+    float *grad_weight;
+    void *workspace;
+} vf_norm_desc;
+
+/* Bytes of workspace of vf_rms_norm_backward; or a negative vf_status.  Pure host
+ * function. */
+int64_t vf_rms_norm_workspace(int64_t T, int64_t M);
+
+int vf_rms_norm(const vf_norm_desc *desc, vf_stream_t stream);
+int vf_rms_norm_backward(const vf_norm_desc *desc, vf_stream_t stream);
+
 /* Static, NUL-terminated description of a vf_status value. */
 const char *vf_status_string(int status);
 

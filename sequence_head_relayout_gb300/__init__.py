@@ -54,7 +54,8 @@ __all__ = ["qkv_pack", "qkv_pack3", "attn_split", "head_merge", "qkv_unpack", "p
            "OP_QKV_UNPACK", "qkv_pack_q", "attn_split_q", "head_merge_q", "qkv_unpack_q",
            "scale_count", "FORMATS", "ExpertPlan", "expert_rows", "expert_plan", "expert_pack",
            "expert_merge", "expert_merge_backward", "expert_pack_q", "expert_restore_q",
-           "expert_merge_q", "expert_merge_backward_q", "expert_product", "expert_weight_grad"]
+           "expert_merge_q", "expert_merge_backward_q", "expert_product", "expert_weight_grad",
+           "expert_glu", "expert_glu_backward", "rms_norm", "rms_norm_q", "rms_norm_backward"]
 
 OP_QKV_PACK, OP_ATTN_SPLIT, OP_HEAD_MERGE, OP_QKV_UNPACK = 0, 1, 2, 3
 ORDERS = {"chunk_major": 0, "slot_major": 1}
@@ -95,6 +96,27 @@ class _ProductDesc(ctypes.Structure):
                 ("align", _I64), ("counts", _P), ("offsets", _P), ("packed", _P),
                 ("weights", _P), ("weight_strides", _I64 * 3), ("grad", _P), ("out", _P),
                 ("grad_weights", _P)]
+
+
+class _GluDesc(ctypes.Structure):
+    """vf_glu_desc of the C ABI."""
+    _fields_ = [("type", ctypes.c_int32), ("E", _I64), ("rows", _I64), ("F", _I64),
+                ("slot_of", _P), ("offsets", _P)]
+    for _name in ("gate", "up", "out", "grad", "grad_gate", "grad_up"):
+        _fields_ += [(_name, _P), (_name + "_strides", _I64 * 2)]
+
+
+class _NormDesc(ctypes.Structure):
+    """vf_norm_desc of the C ABI."""
+    _fields_ = [("type", ctypes.c_int32), ("weight_type", ctypes.c_int32),
+                ("format", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("T", _I64), ("M", _I64), ("group", _I64), ("x", _P), ("x_strides", _I64 * 2),
+                ("weight", _P), ("residual", _P), ("residual_strides", _I64 * 2),
+                ("total", _P), ("total_strides", _I64 * 2), ("out", _P),
+                ("out_strides", _I64 * 2), ("codes", _P), ("scales", _P), ("grad", _P),
+                ("grad_strides", _I64 * 2), ("grad_total", _P),
+                ("grad_total_strides", _I64 * 2), ("grad_x", _P), ("grad_x_strides", _I64 * 2),
+                ("grad_weight", _P), ("workspace", _P)]
 
 
 class VFError(RuntimeError):
@@ -167,6 +189,13 @@ def lib():
             f = getattr(l, name)
             f.argtypes = [ctypes.POINTER(_ProductDesc), _P]
             f.restype = ctypes.c_int
+        for name, desc in (("vf_expert_glu", _GluDesc), ("vf_expert_glu_backward", _GluDesc),
+                           ("vf_rms_norm", _NormDesc), ("vf_rms_norm_backward", _NormDesc)):
+            f = getattr(l, name)
+            f.argtypes = [ctypes.POINTER(desc), _P]
+            f.restype = ctypes.c_int
+        l.vf_rms_norm_workspace.argtypes = [_I64, _I64]
+        l.vf_rms_norm_workspace.restype = _I64
         l.vf_status_string.argtypes = [ctypes.c_int]
         l.vf_status_string.restype = ctypes.c_char_p
         _lib = l
@@ -1017,3 +1046,173 @@ def expert_weight_grad(grad: torch.Tensor, rows: torch.Tensor, plan: ExpertPlan,
     d.packed, d.grad, d.grad_weights = rows.data_ptr(), grad.data_ptr(), out.data_ptr()
     _expert_call("vf_expert_weight_grad", d, stream, grad)
     return out
+
+
+# ---- gated activation ------------------------------------------------------------
+
+def _same_view(t, like, what):
+    """Check a view of ``like``'s shape and type."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda):
+        _gpu_addressable(t, what)
+    if t.dtype != like.dtype or t.shape != like.shape:
+        raise ValueError("%s must be a %s view of shape %s" % (what, like.dtype,
+                                                               tuple(like.shape)))
+
+
+def _glu(gate, up, plan):
+    typ = _rows_type(gate, "gate")
+    n, F = _matrix(gate, "gate")
+    _same_view(up, gate, "up")
+    dims = _check_plan(plan)
+    if n != dims[2]:
+        raise ValueError("plan is for %d packed rows, not %d" % (dims[2], n))
+    d = _GluDesc(typ, dims[3], n, F, plan[1].data_ptr(), plan[3].data_ptr())
+    d.gate, d.up = gate.data_ptr(), up.data_ptr()
+    d.gate_strides, d.up_strides = gate.stride(), up.stride()
+    return d
+
+
+def expert_glu(gate: torch.Tensor, up: torch.Tensor, plan: ExpertPlan,
+               out: torch.Tensor = None, stream: torch.cuda.Stream = None) -> torch.Tensor:
+    """The gated activation of expert-major rows, ``silu(gate) * up``, of two
+    [rows,F] views (the halves of a product's rows), bfloat16, float16 or float32;
+    computed in float32 and rounded once.
+
+    Gap rows are written as zeros, rows behind the last expert are left as they
+    were.  ``out`` may be any non-overlapping [rows,F] view.  No graph is recorded
+    (the gradient is :func:`expert_glu_backward`): views that require a gradient
+    are refused while grad mode is on.
+    """
+    d = _glu(gate, up, plan)
+    _unrecorded(gate, "gate", "expert_glu_backward")
+    _unrecorded(up, "up", "expert_glu_backward")
+    out = _tokens_out(out, stream, gate, gate.shape, gate.dtype, "out")
+    d.out, d.out_strides = out.data_ptr(), out.stride()
+    _expert_call("vf_expert_glu", d, stream, gate)
+    return out
+
+
+def expert_glu_backward(grad: torch.Tensor, gate: torch.Tensor, up: torch.Tensor,
+                        plan: ExpertPlan, grad_gate: torch.Tensor = None,
+                        grad_up: torch.Tensor = None, stream: torch.cuda.Stream = None):
+    """Gradients of :func:`expert_glu`, given the gradient ``grad`` [rows,F] of its
+    result: (grad_gate, grad_up), by default the halves of one [rows,2F] buffer,
+    the rows' gradient of the product in front.  Gap rows are written as zeros, rows
+    behind the last expert are left as they were."""
+    d = _glu(gate, up, plan)
+    _same_view(grad, gate, "grad")
+    n, F = gate.shape
+    if grad_gate is None and grad_up is None:
+        both = _new(stream, gate, (n, 2 * F), gate.dtype)
+        grad_gate, grad_up = both[:, :F], both[:, F:]
+    grad_gate = _tokens_out(grad_gate, stream, gate, gate.shape, gate.dtype, "grad_gate")
+    grad_up = _tokens_out(grad_up, stream, gate, gate.shape, gate.dtype, "grad_up")
+    d.grad, d.grad_gate, d.grad_up = grad.data_ptr(), grad_gate.data_ptr(), grad_up.data_ptr()
+    d.grad_strides, d.grad_gate_strides = grad.stride(), grad_gate.stride()
+    d.grad_up_strides = grad_up.stride()
+    _expert_call("vf_expert_glu_backward", d, stream, gate)
+    return grad_gate, grad_up
+
+
+# ---- root-mean-square norm -------------------------------------------------------
+
+def _norm_desc(x, weight, eps):
+    typ = _rows_type(x, "x")
+    T, M = _matrix(x, "x")
+    if not (isinstance(weight, torch.Tensor) and weight.is_cuda):
+        _gpu_addressable(weight, "weight")
+    if weight.dtype != x.dtype and weight.dtype != torch.float32:
+        raise ValueError("weight must have the type of x or float32")
+    if weight.shape != (M,) or not weight.is_contiguous():
+        raise ValueError("weight must be contiguous with %d elements" % M)
+    d = _NormDesc(typ, _TYPES[weight.dtype], 0, eps, T, M)
+    d.x, d.x_strides, d.weight = x.data_ptr(), x.stride(), weight.data_ptr()
+    return d
+
+
+def _set_residual(d, x, residual, total, stream):
+    """The total's tensor, None without a residual."""
+    if residual is None:
+        if total is not None:
+            raise ValueError("total is written only with a residual")
+        return None
+    _same_view(residual, x, "residual")
+    _unrecorded(residual, "residual", "rms_norm_backward")
+    total = _tokens_out(total, stream, x, x.shape, x.dtype, "total")
+    d.residual, d.residual_strides = residual.data_ptr(), residual.stride()
+    d.total, d.total_strides = total.data_ptr(), total.stride()
+    return total
+
+
+def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
+             residual: torch.Tensor = None, out: torch.Tensor = None,
+             total: torch.Tensor = None, stream: torch.cuda.Stream = None):
+    """Root-mean-square norm of the rows of a [T,M] view (any strides; bfloat16,
+    float16 or float32): ``out = h / sqrt(mean(h^2) + eps) * weight``, computed in
+    float32 and rounded once.  weight: [M], of x's type or float32.
+
+    With a ``residual`` h is ``x + residual``, rounded to the type, and the call
+    returns (out, total) with h in ``total``; else h is x and it returns out.  ``out``
+    and ``total`` may be any non-overlapping [T,M] views.  No graph is recorded (the
+    gradients are :func:`rms_norm_backward`): tensors that require a gradient are
+    refused while grad mode is on.
+    """
+    d = _norm_desc(x, weight, eps)
+    _unrecorded(x, "x", "rms_norm_backward")
+    _unrecorded(weight, "weight", "rms_norm_backward")
+    total = _set_residual(d, x, residual, total, stream)
+    out = _tokens_out(out, stream, x, x.shape, x.dtype, "out")
+    d.out, d.out_strides = out.data_ptr(), out.stride()
+    _expert_call("vf_rms_norm", d, stream, x)
+    return out if total is None else (out, total)
+
+
+def rms_norm_q(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, fmt="e4m3",
+               group: int = 128, residual: torch.Tensor = None, codes: torch.Tensor = None,
+               scales: torch.Tensor = None, total: torch.Tensor = None,
+               stream: torch.cuda.Stream = None):
+    """:func:`rms_norm` of bfloat16 rows to 8 bits -> (codes [T,M], scales
+    [T, ceil(M/group)]), with a residual (codes, scales, total).  Each ``group``
+    consecutive columns of the float32 result share a scale, in the format of the
+    lossy transport: what :func:`expert_restore_q` packs to expert-major rows."""
+    T, M = _bf16_matrix(x, "x")
+    f = _fmt(fmt)
+    d = _norm_desc(x, weight, eps)
+    _unrecorded(x, "x", "rms_norm_backward")
+    _unrecorded(weight, "weight", "rms_norm_backward")
+    total = _set_residual(d, x, residual, total, stream)
+    codes, scales = _kept(codes, scales, stream, x, T, M, f, group)
+    d.format, d.group, d.codes, d.scales = f, group, codes.data_ptr(), scales.data_ptr()
+    _expert_call("vf_rms_norm", d, stream, x)
+    return (codes, scales) if total is None else (codes, scales, total)
+
+
+def rms_norm_backward(grad: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
+                      eps: float = 1e-6, grad_total: torch.Tensor = None,
+                      grad_x: torch.Tensor = None, grad_weight: torch.Tensor = None,
+                      stream: torch.cuda.Stream = None):
+    """Gradients of :func:`rms_norm` -> (grad_x [T,M], grad_weight [M] float32),
+    given the gradient ``grad`` of its result and ``x``, the rows that were normed
+    (with a residual its ``total``).
+
+    ``grad_total`` [T,M], if given, is the gradient that reaches those rows by other
+    paths (the residual stream's) and is added.  With a residual ``grad_x`` is the
+    gradient of both summands.
+    """
+    d = _norm_desc(x, weight, eps)
+    _same_view(grad, x, "grad")
+    T, M = x.shape
+    if grad_total is not None:
+        _same_view(grad_total, x, "grad_total")
+        d.grad_total, d.grad_total_strides = grad_total.data_ptr(), grad_total.stride()
+    grad_x = _tokens_out(grad_x, stream, x, x.shape, x.dtype, "grad_x")
+    grad_weight = _rows_out(grad_weight, stream, x, (M,), torch.float32, "grad_weight")
+    size = lib().vf_rms_norm_workspace(T, M)
+    if size < 0:
+        raise VFError("vf_rms_norm_workspace", size)
+    work = _workspace(stream, x, size // 4)
+    d.grad, d.grad_strides = grad.data_ptr(), grad.stride()
+    d.grad_x, d.grad_x_strides = grad_x.data_ptr(), grad_x.stride()
+    d.grad_weight, d.workspace = grad_weight.data_ptr(), work.data_ptr()
+    _expert_call("vf_rms_norm_backward", d, stream, x)
+    return grad_x, grad_weight

@@ -1,7 +1,7 @@
 """Build ``libvf_relayout.so`` in-tree with nvcc for sm_103a (GB300).
 
-Four translation units (the exact relayouts, the lossy-transport kernels, the
-expert relayouts and the experts' products) compiled in parallel, one ``-gencode``, then linked; the
+Five translation units (the exact relayouts, the lossy-transport kernels, the
+expert relayouts, the experts' products and a layer's row-wise operators) compiled in parallel, one ``-gencode``, then linked; the
 CUDA runtime is linked statically so the library needs nothing but the driver
 at load time.
 """
@@ -14,11 +14,11 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 SOURCES = [os.path.join(CSRC, n) for n in ("vf_relayout.cu", "vf_quant.cu", "vf_expert.cu",
-                                            "vf_product.cu")]
+                                            "vf_product.cu", "vf_layer.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, n) for n in ("relayout_kernel.cuh", "launch.cuh",
                                                   "tiled_kernel.cuh", "quant_kernel.cuh",
                                                   "quant.h", "checks.h", "call.h",
-                                                  "product_kernel.cuh",
+                                                  "product_kernel.cuh", "layer_kernel.cuh",
                                                   "expert_kernel.cuh", "expert_q_kernel.cuh")] \
     + [os.path.join(ROOT, "include", "vf_relayout.h")]
 LIB = os.path.join(PKG, "libvf_relayout.so")

@@ -21,11 +21,11 @@ inline cudaStream_t as_stream(vf_stream_t s) { return reinterpret_cast<cudaStrea
 
 // Launch with programmatic stream serialisation, as the other kernels do.
 template <class Args>
-int launch(void (*kernel)(Args), int64_t blocks, int threads, size_t smem, cudaStream_t stream,
+int launch(void (*kernel)(Args), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
            const Args &args) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(blocks), 1, 1);
-    cfg.blockDim = dim3(unsigned(threads), 1, 1);
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -38,6 +38,12 @@ int launch(void (*kernel)(Args), int64_t blocks, int threads, size_t smem, cudaS
         return VF_ERR_CUDA;
     }
     return VF_OK;
+}
+
+template <class Args>
+int launch(void (*kernel)(Args), int64_t blocks, int threads, size_t smem, cudaStream_t stream,
+           const Args &args) {
+    return launch(kernel, dim3(unsigned(blocks)), dim3(unsigned(threads)), smem, stream, args);
 }
 
 inline int64_t type_size(int type) { return type == VF_TYPE_F32 ? 4 : 2; }
@@ -88,11 +94,17 @@ struct Ranges {
         else add(ptr, span, size, is_written);
     }
 
+    // Ranges i and i + 1 interleave without a common element.
+    void join(int i) { joined = i; }
+    int joined = -1;
+
     int check(bool device = false) {
         if (rc != VF_OK) return rc;
         for (int i = 0; i < n; ++i)
             for (int j = i + 1; j < n; ++j)
-                if ((written[i] || written[j]) && overlap(r[i], r[j])) return VF_ERR_ALIAS;
+                if (!(i == joined && j == i + 1) &&
+                    (written[i] || written[j]) && overlap(r[i], r[j]))
+                    return VF_ERR_ALIAS;
         for (int i = 0; i < n; ++i)
             if ((rc = check_pointer(p[i], device)) != VF_OK) return rc;
         return VF_OK;
