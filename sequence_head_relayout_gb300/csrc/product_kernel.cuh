@@ -34,9 +34,11 @@ constexpr int kBlockK = 64;                    // k of a stage: 128 bytes of 16-
 constexpr int kTileM = 128;                    // features of a CTA's tile
 constexpr int kStageA = kTileM * kBlockK * 2;  // bytes
 constexpr int kMaxStages = 12;
-constexpr int kEpilogueWarps = 4;
+constexpr int kEpilogueWarps = 8;               // two for each quarter of the tile's features
 constexpr int kStagingBytes = 4608;            // per epilogue warp: 32 rows of 144 bytes
 constexpr int kFillWarps = 8;                  // producers of operands that TMA cannot take
+constexpr int kThreads = 32 * (4 + kEpilogueWarps);
+constexpr int kFillThreads = kThreads + 32 * kFillWarps;
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr uint64_t kDrainNs = 100000000ull;
 constexpr uint32_t kAll = 0xFFFFFFFFu;
@@ -54,6 +56,7 @@ struct ProductArgs {
     int32_t box;                  // rows of one copy of B (rows form)
     int32_t stages, stage_bytes;
     int32_t acc_stride, tmem_cols;
+    int32_t a_slabs, b_slabs;     // operands with i contiguous: 128 i by one copy
     int32_t bf16, gaps, vec, out32;
 };
 
@@ -161,6 +164,19 @@ __device__ __forceinline__ void copy_3d(uint32_t dst, const CUtensorMap *map, ui
         asm volatile("cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile"
                      ".mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];"
                      ::"r"(dst), "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z) : "memory");
+}
+
+template <int CTAS>
+__device__ __forceinline__ void copy_4d(uint32_t dst, const CUtensorMap *map, uint32_t bar,
+                                        int x, int y, int z, int w) {
+    if constexpr (CTAS == 1)
+        asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile"
+                     ".mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];"
+                     ::"r"(dst), "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+    else
+        asm volatile("cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile"
+                     ".mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];"
+                     ::"r"(dst), "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
 // ---- tensor cores --------------------------------------------------------------
@@ -306,7 +322,9 @@ struct Tiles {
         const int in = int(t - o.e * each);
         o.f0 = in % a.feat_tiles * (kTileM * CTAS);
         o.c0 = in / a.feat_tiles * a.tile_n;
-        o.n = (min(a.tile_n, a.cols - o.c0) + kStep - 1) / kStep * kStep;
+        // (each CTA's share of B starts at a whole slab)
+        const int multiple = a.b_slabs ? 64 * CTAS : kStep;
+        o.n = (min(a.tile_n, a.cols - o.c0) + multiple - 1) / multiple * multiple;
         segment(o.e, o.row0, o.valid);
         o.kblocks = (o.valid + kBlockK - 1) / kBlockK;
         o.gap = 0;
@@ -548,7 +566,7 @@ __host__ __device__ constexpr int64_t shared_bytes(int stages, int stage_bytes) 
 // A_MN     the first operand is stored with i contiguous
 // FILL     operands come by plain loads, k contiguous in shared memory
 template <int CTAS, bool WEIGHTS, bool A_MN, bool FILL>
-__global__ void __launch_bounds__(FILL ? 512 : 256, 1)
+__global__ void __launch_bounds__(FILL ? kFillThreads : kThreads, 1)
 expert_product(const __grid_constant__ ProductArgs a) {
     static_assert(!FILL || (CTAS == 1 && !A_MN), "fill producers: single CTAs, k contiguous");
     constexpr bool B_MN = WEIGHTS && !FILL;
@@ -591,45 +609,54 @@ expert_product(const __grid_constant__ ProductArgs a) {
         }
     };
 
-    if (!FILL && warp == 0) {
-        // copies: A's half and B's half of every k block
+    if (!FILL && (warp == 0 || warp == 3)) {
+        // copies: one warp for this CTA's A, one for its share of B
         Tiles<CTAS, WEIGHTS> tiles(a);
         bool ok = true;
         while (ok && tiles.next(o)) {
-            const int half = o.n / CTAS;             // this CTA's share of B
-            const int boxes = WEIGHTS ? (half + 63) / 64 : (half + a.box - 1) / a.box;
-            const uint32_t bytes =
-                uint32_t(CTAS * (kStageA + boxes * (WEIGHTS ? 64 : a.box) * 128));
-            const int fa = o.f0 + int(rank) * kTileM;
+            const int half = o.n / CTAS;
+            const int slabs = (half + 63) / 64;
+            const int boxes = WEIGHTS ? slabs : (half + a.box - 1) / a.box;
+            const uint32_t bytes = uint32_t(
+                CTAS * (kStageA + (WEIGHTS ? (a.b_slabs ? 2 : slabs) * 64 : boxes * a.box) * 128));
+            const int fa = o.f0 + int(rank) * kTileM, cb = o.c0 + int(rank) * half;
             if (lane == 0) {
                 for (int kb = 0; kb < o.kblocks; ++kb) {
                     ok = barrier_wait(smem_addr(&ctl.empty[s]), phase ^ 1, failed);
                     if (!ok) break;
                     const uint32_t bar = first_barrier<CTAS>(smem_addr(&ctl.full[s]));
                     const uint32_t da = smem_addr(smem + s * a.stage_bytes), db = da + kStageA;
-                    if (rank == 0) barrier_expect(smem_addr(&ctl.full[s]), bytes);
-                    if constexpr (WEIGHTS) {
-                        // The last block's rows lie at its end, behind zeros: the
-                        // maps' second coordinate runs over the same rows as the third,
-                        // so that what lies before it is outside the tensor.
-                        const int y = min(0, o.valid - (kb + 1) * kBlockK);
-                        const int z = o.row0 + kb * kBlockK;
-                        for (int j = 0; j < 2; ++j)
-                            copy_3d<CTAS>(da + j * 8192, &a.a_map, bar, fa + j * 64, y, z);
-                        for (int j = 0; j < boxes; ++j)
-                            copy_3d<CTAS>(db + j * 8192, &a.b_map, bar,
-                                          o.c0 + int(rank) * half + j * 64, y, z);
-                    } else {
-                        const int k = kb * kBlockK;
-                        if constexpr (A_MN) {
-                            for (int j = 0; j < 2; ++j)
-                                copy_3d<CTAS>(da + j * 8192, &a.a_map, bar, fa + j * 64, k, o.e);
-                        } else {
+                    const int k = kb * kBlockK;
+                    // Weights form: the last block's rows lie at its end, behind zeros:
+                    // the maps' second coordinate runs over the same rows as the third,
+                    // so that what lies before it is outside the tensor.
+                    const int y = min(0, o.valid - k - kBlockK), z = o.row0 + k;
+                    if (warp == 0) {
+                        if (rank == 0) barrier_expect(smem_addr(&ctl.full[s]), bytes);
+                        if constexpr (!A_MN) {
                             copy_3d<CTAS>(da, &a.a_map, bar, k, fa, o.e);
+                        } else if (a.a_slabs) {
+                            if constexpr (WEIGHTS)
+                                copy_4d<CTAS>(da, &a.a_map, bar, 0, y, z, fa / 64);
+                            else
+                                copy_4d<CTAS>(da, &a.a_map, bar, 0, k, fa / 64, o.e);
+                        } else {
+                            for (int j = 0; j < 2; ++j)
+                                if constexpr (WEIGHTS)
+                                    copy_3d<CTAS>(da + j * 8192, &a.a_map, bar, fa + j * 64, y, z);
+                                else
+                                    copy_3d<CTAS>(da + j * 8192, &a.a_map, bar, fa + j * 64, k,
+                                                  o.e);
                         }
+                    } else if constexpr (!WEIGHTS) {
                         for (int j = 0; j < boxes; ++j)
                             copy_2d<CTAS>(db + j * a.box * 128, &a.b_map, bar, k,
                                           o.row0 + int(rank) * half + j * a.box);
+                    } else if (a.b_slabs) {
+                        copy_4d<CTAS>(db, &a.b_map, bar, 0, y, z, cb / 64);
+                    } else {
+                        for (int j = 0; j < boxes; ++j)
+                            copy_3d<CTAS>(db + j * 8192, &a.b_map, bar, cb + j * 64, y, z);
                     }
                     advance();
                 }
@@ -672,8 +699,8 @@ expert_product(const __grid_constant__ ProductArgs a) {
         }
     } else if (warp >= 4 && warp < 4 + kEpilogueWarps) {
         Tiles<CTAS, WEIGHTS> tiles(a);
-        const int quarter = warp - 4;
-        uint8_t *const mine = staging + quarter * kStagingBytes;
+        const int quarter = warp % 4, turn = (warp - 4) / 4;
+        uint8_t *const mine = staging + (warp - 4) * kStagingBytes;
         uint32_t it = 0;
         while (tiles.next(o)) {
             const uint32_t acc = it & 1, acc_phase = it >> 1 & 1;
@@ -689,7 +716,7 @@ expert_product(const __grid_constant__ ProductArgs a) {
             const int f = o.f0 + int(rank) * kTileM + quarter * 32;
             const uint32_t d = tmem + acc * uint32_t(a.acc_stride) + (uint32_t(quarter * 32) << 16);
             const int n = WEIGHTS ? min(o.n, a.cols - o.c0) : o.valid;
-            for (int c = 0; c < n; c += 32) {
+            for (int c = 32 * turn; c < n; c += 64) {
                 uint32_t v[32];
                 if (o.kblocks > 0 && ok) {
                     tmem_load(d + uint32_t(c), v);
@@ -712,12 +739,12 @@ expert_product(const __grid_constant__ ProductArgs a) {
                     else barrier_arrive_first(smem_addr(&ctl.acc_empty[acc]));
                 }
             }
-            if (!WEIGHTS && o.gap > 0 && f < a.feat)
+            if (!WEIGHTS && o.gap > 0 && f < a.feat && turn == 0)
                 zero_rows(a, int64_t(o.row0) + o.valid, o.gap, f, lane);
         }
-    } else if (FILL && warp >= 8) {
+    } else if (FILL && warp >= 12) {
         Tiles<CTAS, WEIGHTS> tiles(a);
-        const int w = warp - 8;
+        const int w = warp - 12;
         bool ok = true;
         while (ok && tiles.next(o)) {
             const uint16_t *pa, *pb;

@@ -40,14 +40,16 @@ EncodeTiled encoder() {
 }
 
 // A map of 16-bit elements, innermost dimension contiguous; strides in elements
-// from the second dimension on; boxes of 64 elements (128 bytes, swizzled).
+// from the second dimension on; boxes of 64 elements (128 bytes, swizzled), two of
+// them along dimension `slabs`.
 int make_map(CUtensorMap *map, bool bf16, int nd, const void *base, const int64_t *ext,
-             const int64_t *str, int64_t box1) {
+             const int64_t *str, int64_t box1, int slabs = 0) {
     const EncodeTiled fn = encoder();
     if (fn == nullptr) return VF_ERR_CUDA;
-    cuuint64_t dims[3], strides[2];
-    cuuint32_t box[3] = {64, cuuint32_t(box1), 1};
-    const cuuint32_t steps[3] = {1, 1, 1};
+    cuuint64_t dims[4], strides[3];
+    cuuint32_t box[4] = {64, cuuint32_t(box1), 1, 1};
+    const cuuint32_t steps[4] = {1, 1, 1, 1};
+    if (slabs) box[slabs] = 2;
     for (int i = 0; i < nd; ++i) {
         dims[i] = cuuint64_t(ext[i]);
         if (i > 0) strides[i - 1] = cuuint64_t(str[i]) * 2;
@@ -104,7 +106,7 @@ void set_form(vfp::ProductArgs *a, const Form &f, bool fill) {
 using Kernel = void (*)(vfp::ProductArgs);
 
 int launch_product(Kernel kernel, const vfp::ProductArgs &a, int64_t ctas, int64_t tiles,
-                   int threads, cudaStream_t stream) {
+                   cudaStream_t stream, int threads = vfp::kThreads) {
     if (tiles == 0) return VF_OK;
     // on every call, so that no state is kept per device, and always the same number
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -164,7 +166,7 @@ Form rows_form(const vf_product_desc *d, bool maps) {
     if (mean <= 8) return {1, 32, 16};
     if (mean <= 32) return {1, 64, 16};
     if (mean <= 96 || d->N <= 128) return {1, 128, 32};
-    return {2, 256, 32};
+    return {2, 256, 128};
 }
 
 int product(const vf_product_desc *d, cudaStream_t stream) {
@@ -202,15 +204,21 @@ int product(const vf_product_desc *d, cudaStream_t stream) {
     set_form(&a, f, maps == 0);
     const int64_t tiles = a.feat_tiles * (most + d->rows / f.tile_n);
     if (maps == 0)
-        return launch_product(vfp::expert_product<1, false, false, true>, a, f.ctas, tiles, 512,
-                              stream);
+        return launch_product(vfp::expert_product<1, false, false, true>, a, f.ctas, tiles,
+                              stream, vfp::kFillThreads);
     const bool mn = maps == 2;
-    int64_t dims[3] = {mn ? d->N : d->M, mn ? d->M : d->N, d->E};
+    const int64_t dims[3] = {mn ? d->N : d->M, mn ? d->M : d->N, d->E};
     int64_t str[3] = {1, d->weight_strides[mn ? 2 : 1], d->weight_strides[0]};
     map_stride(dims[1], &str[1], dims[0]);
     map_stride(dims[2], &str[2], dims[0]);
-    if ((rc = make_map(&a.a_map, a.bf16, 3, d->weights, dims, str, mn ? 64 : 128)) != VF_OK)
-        return rc;
+    a.a_slabs = mn && d->N % 64 == 0;
+    if (a.a_slabs) {
+        const int64_t dims4[4] = {64, dims[1], d->N / 64, d->E}, str4[4] = {1, str[1], 64, str[2]};
+        rc = make_map(&a.a_map, a.bf16, 4, d->weights, dims4, str4, 64, 2);
+    } else {
+        rc = make_map(&a.a_map, a.bf16, 3, d->weights, dims, str, mn ? 64 : 128);
+    }
+    if (rc != VF_OK) return rc;
     const int64_t b_dims[2] = {d->M, d->rows}, b_str[2] = {1, d->M};
     if ((rc = make_map(&a.b_map, a.bf16, 2, d->packed, b_dims, b_str, f.box)) != VF_OK) return rc;
     const Kernel kernel =
@@ -218,7 +226,18 @@ int product(const vf_product_desc *d, cudaStream_t stream) {
                           : vfp::expert_product<2, false, false, false>)
                     : (mn ? vfp::expert_product<1, false, true, false>
                           : vfp::expert_product<1, false, false, false>);
-    return launch_product(kernel, a, f.ctas, tiles, 256, stream);
+    return launch_product(kernel, a, f.ctas, tiles, stream);
+}
+
+// The map of packed rows for the weights' gradient: the second dimension steps over
+// the rows as the third does (see the kernel); columns by 64 where they are whole.
+int make_row_map(CUtensorMap *map, bool bf16, const void *p, int64_t cols, int64_t rows) {
+    if (cols % 64) {
+        const int64_t dims[3] = {cols, 64, rows}, str[3] = {1, cols, cols};
+        return make_map(map, bf16, 3, p, dims, str, 64);
+    }
+    const int64_t dims[4] = {64, 64, rows, cols / 64}, str[4] = {1, cols, cols, 64};
+    return make_map(map, bf16, 4, p, dims, str, 64, 3);
 }
 
 int weight_grad(const vf_product_desc *d, cudaStream_t stream) {
@@ -255,15 +274,14 @@ int weight_grad(const vf_product_desc *d, cudaStream_t stream) {
     set_form(&a, f, !maps);
     const int64_t tiles = int64_t(a.feat_tiles) * a.col_tiles * a.E;
     if (!maps)
-        return launch_product(vfp::expert_product<1, true, false, true>, a, f.ctas, tiles, 512,
-                              stream);
-    // the second dimension steps over the rows as the third does (see the kernel)
-    const int64_t a_dims[3] = {d->N, 64, d->rows}, a_str[3] = {1, d->N, d->N};
-    const int64_t b_dims[3] = {d->M, 64, d->rows}, b_str[3] = {1, d->M, d->M};
-    if ((rc = make_map(&a.a_map, a.bf16, 3, d->grad, a_dims, a_str, 64)) != VF_OK ||
-        (rc = make_map(&a.b_map, a.bf16, 3, d->packed, b_dims, b_str, 64)) != VF_OK)
+        return launch_product(vfp::expert_product<1, true, false, true>, a, f.ctas, tiles,
+                              stream, vfp::kFillThreads);
+    a.a_slabs = d->N % 64 == 0;
+    a.b_slabs = d->M % 64 == 0;
+    if ((rc = make_row_map(&a.a_map, a.bf16, d->grad, d->N, d->rows)) != VF_OK ||
+        (rc = make_row_map(&a.b_map, a.bf16, d->packed, d->M, d->rows)) != VF_OK)
         return rc;
-    return launch_product(vfp::expert_product<2, true, true, false>, a, f.ctas, tiles, 256,
+    return launch_product(vfp::expert_product<2, true, true, false>, a, f.ctas, tiles,
                           stream);
 }
 
