@@ -34,6 +34,7 @@ constexpr int kBlockK = 64;                    // k of a stage: 128 bytes of 16-
 constexpr int kTileM = 128;                    // features of a CTA's tile
 constexpr int kStageA = kTileM * kBlockK * 2;  // bytes
 constexpr int kMaxStages = 12;
+constexpr int kBoxes = 4;                      // heights of the copies of B, multiples of one
 constexpr int kEpilogueWarps = 8;               // two for each quarter of the tile's features
 constexpr int kStagingBytes = 4608;            // per epilogue warp: 32 rows of 144 bytes
 constexpr int kFillWarps = 8;                  // producers of operands that TMA cannot take
@@ -44,7 +45,8 @@ constexpr uint64_t kDrainNs = 100000000ull;
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 
 struct ProductArgs {
-    CUtensorMap a_map, b_map;     // not used by the fill producers
+    // not used by the fill producers; rows form: b_maps[i] has boxes of (i + 1) box rows
+    CUtensorMap a_map, b_maps[kBoxes];
     const int32_t *counts, *offsets;
     const uint16_t *a, *b;        // the fill producers' operands and element strides
     int64_t a_expert, a_i, a_k, b_i, b_k;
@@ -53,7 +55,7 @@ struct ProductArgs {
     int32_t feat, cols, red;      // features; weights: columns; rows: length of the sums
     int32_t feat_tiles, col_tiles;
     int32_t tile_n;               // most rows (columns) of a tile
-    int32_t box;                  // rows of one copy of B (rows form)
+    int32_t box;                  // rows form: a copy of B has one to kBoxes times as many rows
     int32_t stages, stage_bytes;
     int32_t acc_stride, tmem_cols;
     int32_t a_slabs, b_slabs;     // operands with i contiguous: 128 i by one copy
@@ -616,7 +618,9 @@ expert_product(const __grid_constant__ ProductArgs a) {
         while (ok && tiles.next(o)) {
             const int half = o.n / CTAS;
             const int slabs = (half + 63) / 64;
+            // rows form: one copy, as high as the tile needs
             const int boxes = WEIGHTS ? slabs : (half + a.box - 1) / a.box;
+            const CUtensorMap *const b_map = &a.b_maps[WEIGHTS ? 0 : boxes - 1];
             const uint32_t bytes = uint32_t(
                 CTAS * (kStageA + (WEIGHTS ? (a.b_slabs ? 2 : slabs) * 64 : boxes * a.box) * 128));
             const int fa = o.f0 + int(rank) * kTileM, cb = o.c0 + int(rank) * half;
@@ -649,14 +653,12 @@ expert_product(const __grid_constant__ ProductArgs a) {
                                                   o.e);
                         }
                     } else if constexpr (!WEIGHTS) {
-                        for (int j = 0; j < boxes; ++j)
-                            copy_2d<CTAS>(db + j * a.box * 128, &a.b_map, bar, k,
-                                          o.row0 + int(rank) * half + j * a.box);
+                        copy_2d<CTAS>(db, b_map, bar, k, o.row0 + int(rank) * half);
                     } else if (a.b_slabs) {
-                        copy_4d<CTAS>(db, &a.b_map, bar, 0, y, z, cb / 64);
+                        copy_4d<CTAS>(db, b_map, bar, 0, y, z, cb / 64);
                     } else {
                         for (int j = 0; j < boxes; ++j)
-                            copy_3d<CTAS>(db + j * 8192, &a.b_map, bar, cb + j * 64, y, z);
+                            copy_3d<CTAS>(db + j * 8192, b_map, bar, cb + j * 64, y, z);
                     }
                     advance();
                 }

@@ -166,7 +166,7 @@ Form rows_form(const vf_product_desc *d, bool maps) {
     if (mean <= 8) return {1, 32, 16};
     if (mean <= 32) return {1, 64, 16};
     if (mean <= 96 || d->N <= 128) return {1, 128, 32};
-    return {2, 256, 128};
+    return {2, 256, 32};
 }
 
 int product(const vf_product_desc *d, cudaStream_t stream) {
@@ -220,7 +220,10 @@ int product(const vf_product_desc *d, cudaStream_t stream) {
     }
     if (rc != VF_OK) return rc;
     const int64_t b_dims[2] = {d->M, d->rows}, b_str[2] = {1, d->M};
-    if ((rc = make_map(&a.b_map, a.bf16, 2, d->packed, b_dims, b_str, f.box)) != VF_OK) return rc;
+    for (int i = 0; i < vfp::kBoxes && rc == VF_OK; ++i)
+        if (i * f.box < f.tile_n / f.ctas)
+            rc = make_map(&a.b_maps[i], a.bf16, 2, d->packed, b_dims, b_str, (i + 1) * f.box);
+    if (rc != VF_OK) return rc;
     const Kernel kernel =
         f.ctas == 2 ? (mn ? vfp::expert_product<2, false, true, false>
                           : vfp::expert_product<2, false, false, false>)
@@ -279,7 +282,7 @@ int weight_grad(const vf_product_desc *d, cudaStream_t stream) {
     a.a_slabs = d->N % 64 == 0;
     a.b_slabs = d->M % 64 == 0;
     if ((rc = make_row_map(&a.a_map, a.bf16, d->grad, d->N, d->rows)) != VF_OK ||
-        (rc = make_row_map(&a.b_map, a.bf16, d->packed, d->M, d->rows)) != VF_OK)
+        (rc = make_row_map(&a.b_maps[0], a.bf16, d->packed, d->M, d->rows)) != VF_OK)
         return rc;
     return launch_product(vfp::expert_product<2, true, true, false>, a, f.ctas, tiles,
                           stream);
