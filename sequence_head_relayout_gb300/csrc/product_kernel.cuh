@@ -104,6 +104,28 @@ __device__ __forceinline__ bool barrier_wait(uint32_t bar, uint32_t parity, vola
     return true;
 }
 
+// The same by a whole warp, `ready`: the result of an earlier try.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *failed,
+                                          bool ready = false, uint64_t more_ns = 0) {
+    if (!ready) ready = barrier_wait(bar, parity, failed, more_ns);
+    return __all_sync(kAll, int(ready));
+}
+
+// True in one lane of the warp, the same one every time.
+__device__ __forceinline__ bool elected() {
+    uint32_t yes;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(yes));
+    return yes != 0;
+}
+
+// A value that all lanes hold, known to be uniform by the compiler: copies and
+// products take their arguments from uniform registers, and a thread that had to move
+// them there one by one issued a block of products in some 400 cycles of the 512 that
+// they run (product of 16,384 rows, 3,584 to 4,096 features: 55% of the tensor pipe).
+template <class T>
+__device__ __forceinline__ T uniform(T v) { return __shfl_sync(kAll, v, 0); }
+
 __device__ __forceinline__ void barrier_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -206,17 +228,31 @@ __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
                      ::"r"(addr), "r"(cols) : "memory");
 }
 
+// Descriptor of an operand in shared memory, 128-byte swizzle.  k contiguous: rows of
+// 128 bytes, groups of 8 rows 1,024 bytes apart.  i contiguous: 64 i to a row of 128
+// bytes, one row for each k, groups of 8 k 1,024 bytes apart and the next 64 i
+// 64 rows on.  The low word holds the address, in units of 16 bytes.
+constexpr uint32_t kDescHigh = (1024 >> 4) | (1u << 14) | (2u << 29);
+
+__device__ __forceinline__ uint32_t operand(uint32_t addr) {
+    return (uint32_t((kBlockK * 128) >> 4) << 16) | ((addr & 0x3FFFF) >> 4);
+}
+
 template <int CTAS>
-__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t instr,
+__device__ __forceinline__ void mma(uint32_t d, uint32_t a, uint32_t b, uint32_t instr,
                                     bool accumulate) {
     if constexpr (CTAS == 1)
-        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                     "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-                     ::"r"(d), "l"(a), "l"(b), "r"(instr), "r"(uint32_t(accumulate)) : "memory");
+        asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                     "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+                     "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}"
+                     ::"r"(d), "r"(a), "r"(b), "r"(instr), "r"(uint32_t(accumulate)),
+                       "n"(kDescHigh) : "memory");
     else
-        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                     "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-                     ::"r"(d), "l"(a), "l"(b), "r"(instr), "r"(uint32_t(accumulate)) : "memory");
+        asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                     "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+                     "tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %3, p;\n\t}"
+                     ::"r"(d), "r"(a), "r"(b), "r"(instr), "r"(uint32_t(accumulate)),
+                       "n"(kDescHigh) : "memory");
 }
 
 // The barrier (of both CTAs of a pair) is arrived at when the products issued so
@@ -255,20 +291,8 @@ __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&v)[32]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
-// Descriptor of an operand in shared memory, 128-byte swizzle.  k contiguous: rows of
-// 128 bytes, groups of 8 rows 1,024 bytes apart.  i contiguous: 64 i to a row of 128
-// bytes, one row for each k, groups of 8 k 1,024 bytes apart and the next 64 i
-// 64 rows on.
-constexpr uint64_t kDescBase = (uint64_t(1) << 46) | (uint64_t(2) << 61) |
-                               (uint64_t(1024 >> 4) << 32) |
-                               (uint64_t((kBlockK * 128) >> 4) << 16);
-
-__device__ __forceinline__ uint64_t operand(uint32_t addr) {
-    return kDescBase | uint64_t((addr & 0x3FFFF) >> 4);
-}
-
-// Bytes from one step of 16 k to the next.
-template <bool MN> constexpr uint32_t kStepBytes = MN ? 16 * 128 : 32;
+// From one step of 16 k to the next, in units of 16 bytes.
+template <bool MN> constexpr uint32_t kStep16 = MN ? 16 * 128 / 16 : 2;
 
 // ---- tiles ---------------------------------------------------------------------
 
@@ -314,7 +338,14 @@ struct Tiles {
     __device__ bool next(Tile &o) {
         const bool there = WEIGHTS ? next_weights(o) : next_rows(o);
         t += step;
-        return there;
+        o.e = uniform(o.e);
+        o.f0 = uniform(o.f0);
+        o.c0 = uniform(o.c0);
+        o.row0 = uniform(o.row0);
+        o.valid = uniform(o.valid);
+        o.n = uniform(o.n);
+        o.kblocks = uniform(o.kblocks);
+        return __all_sync(kAll, int(there));
     }
 
     __device__ bool next_weights(Tile &o) {
@@ -577,7 +608,7 @@ expert_product(const __grid_constant__ ProductArgs a) {
     uint8_t *const staging = smem + a.stages * a.stage_bytes;
     Control &ctl = *reinterpret_cast<Control *>(staging + kEpilogueWarps * kStagingBytes);
     volatile int *const failed = &ctl.failed;
-    const int warp = int(threadIdx.x >> 5), lane = int(threadIdx.x & 31);
+    const int warp = uniform(int(threadIdx.x >> 5)), lane = int(threadIdx.x & 31);
     const uint32_t rank = CTAS == 1 ? 0 : cluster_rank();
 
     if (threadIdx.x == 0) {
@@ -597,11 +628,11 @@ expert_product(const __grid_constant__ ProductArgs a) {
     __syncthreads();
     if constexpr (CTAS > 1) cluster_sync();
     fence_after();
-    const uint32_t tmem = ctl.tmem;
+    const uint32_t tmem = uniform(ctl.tmem);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
-    Tile o;
+    Tile o = {};
     int s = 0;                                       // stage and its phase
     uint32_t phase = 0;
     const auto advance = [&] {
@@ -611,8 +642,12 @@ expert_product(const __grid_constant__ ProductArgs a) {
         }
     };
 
+    const uint32_t ring = smem_addr(smem), full = smem_addr(&ctl.full[0]),
+                   empty = smem_addr(&ctl.empty[0]);
     if (!FILL && (warp == 0 || warp == 3)) {
         // copies: one warp for this CTA's A, one for its share of B
+        const uint32_t bars = first_barrier<CTAS>(full);
+        const bool one = elected();
         Tiles<CTAS, WEIGHTS> tiles(a);
         bool ok = true;
         while (ok && tiles.next(o)) {
@@ -624,79 +659,80 @@ expert_product(const __grid_constant__ ProductArgs a) {
             const uint32_t bytes = uint32_t(
                 CTAS * (kStageA + (WEIGHTS ? (a.b_slabs ? 2 : slabs) * 64 : boxes * a.box) * 128));
             const int fa = o.f0 + int(rank) * kTileM, cb = o.c0 + int(rank) * half;
-            if (lane == 0) {
-                for (int kb = 0; kb < o.kblocks; ++kb) {
-                    ok = barrier_wait(smem_addr(&ctl.empty[s]), phase ^ 1, failed);
-                    if (!ok) break;
-                    const uint32_t bar = first_barrier<CTAS>(smem_addr(&ctl.full[s]));
-                    const uint32_t da = smem_addr(smem + s * a.stage_bytes), db = da + kStageA;
-                    const int k = kb * kBlockK;
-                    // Weights form: the last block's rows lie at its end, behind zeros:
-                    // the maps' second coordinate runs over the same rows as the third,
-                    // so that what lies before it is outside the tensor.
-                    const int y = min(0, o.valid - k - kBlockK), z = o.row0 + k;
-                    if (warp == 0) {
-                        if (rank == 0) barrier_expect(smem_addr(&ctl.full[s]), bytes);
-                        if constexpr (!A_MN) {
-                            copy_3d<CTAS>(da, &a.a_map, bar, k, fa, o.e);
-                        } else if (a.a_slabs) {
-                            if constexpr (WEIGHTS)
-                                copy_4d<CTAS>(da, &a.a_map, bar, 0, y, z, fa / 64);
-                            else
-                                copy_4d<CTAS>(da, &a.a_map, bar, 0, k, fa / 64, o.e);
-                        } else {
-                            for (int j = 0; j < 2; ++j)
-                                if constexpr (WEIGHTS)
-                                    copy_3d<CTAS>(da + j * 8192, &a.a_map, bar, fa + j * 64, y, z);
-                                else
-                                    copy_3d<CTAS>(da + j * 8192, &a.a_map, bar, fa + j * 64, k,
-                                                  o.e);
-                        }
-                    } else if constexpr (!WEIGHTS) {
-                        copy_2d<CTAS>(db, b_map, bar, k, o.row0 + int(rank) * half);
-                    } else if (a.b_slabs) {
-                        copy_4d<CTAS>(db, b_map, bar, 0, y, z, cb / 64);
+            for (int kb = 0; kb < o.kblocks; ++kb) {
+                ok = warp_wait(empty + s * 8, phase ^ 1, failed);
+                if (!ok) break;
+                const uint32_t bar = bars + s * 8;
+                const uint32_t da = ring + s * a.stage_bytes, db = da + kStageA;
+                const int k = kb * kBlockK;
+                // Weights form: the last block's rows lie at its end, behind zeros: the
+                // maps' second coordinate runs over the same rows as the third, so that
+                // what lies before it is outside the tensor.
+                const int y = min(0, o.valid - k - kBlockK), z = o.row0 + k;
+                if (!one) {
+                } else if (warp == 0) {
+                    if (rank == 0) barrier_expect(full + s * 8, bytes);
+                    if constexpr (!A_MN) {
+                        copy_3d<CTAS>(da, &a.a_map, bar, k, fa, o.e);
+                    } else if (a.a_slabs) {
+                        if constexpr (WEIGHTS)
+                            copy_4d<CTAS>(da, &a.a_map, bar, 0, y, z, fa / 64);
+                        else
+                            copy_4d<CTAS>(da, &a.a_map, bar, 0, k, fa / 64, o.e);
                     } else {
-                        for (int j = 0; j < boxes; ++j)
-                            copy_3d<CTAS>(db + j * 8192, b_map, bar, cb + j * 64, y, z);
+                        for (int j = 0; j < 2; ++j)
+                            if constexpr (WEIGHTS)
+                                copy_3d<CTAS>(da + j * 8192, &a.a_map, bar, fa + j * 64, y, z);
+                            else
+                                copy_3d<CTAS>(da + j * 8192, &a.a_map, bar, fa + j * 64, k, o.e);
                     }
-                    advance();
+                } else if constexpr (!WEIGHTS) {
+                    copy_2d<CTAS>(db, b_map, bar, k, o.row0 + int(rank) * half);
+                } else if (a.b_slabs) {
+                    copy_4d<CTAS>(db, b_map, bar, 0, y, z, cb / 64);
+                } else {
+                    for (int j = 0; j < boxes; ++j)
+                        copy_3d<CTAS>(db + j * 8192, b_map, bar, cb + j * 64, y, z);
                 }
+                __syncwarp();
+                advance();
             }
-            ok = __shfl_sync(kAll, int(ok), 0);
         }
     } else if (warp == 1 && rank == 0) {
         // products; one thread issues them
         const uint32_t instr = (1u << 4) | (a.bf16 ? (1u << 7) | (1u << 10) : 0u) |
                                (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u) |
                                (uint32_t(kTileM * CTAS / 16) << 24);
+        const uint32_t first = operand(ring), stage16 = uint32_t(a.stage_bytes) >> 4;
+        const bool one = elected();
         Tiles<CTAS, WEIGHTS> tiles(a);
         uint32_t it = 0;
         bool ok = true;
         while (ok && tiles.next(o)) {
             if (o.kblocks == 0) continue;
-            if (lane == 0) {
-                const uint32_t acc = it & 1, acc_phase = it >> 1 & 1;
-                ok = barrier_wait(smem_addr(&ctl.acc_empty[acc]), acc_phase ^ 1, failed);
+            const uint32_t acc = it & 1, acc_phase = it >> 1 & 1;
+            bool ready = barrier_try(full + s * 8, phase);
+            ok = warp_wait(smem_addr(&ctl.acc_empty[acc]), acc_phase ^ 1, failed);
+            fence_after();
+            const uint32_t d = tmem + acc * uint32_t(a.acc_stride);
+            const uint32_t in = instr | (uint32_t(o.n / 8) << 17);
+            for (int kb = 0; ok && kb < o.kblocks; ++kb) {
+                ok = warp_wait(full + s * 8, phase, failed, ready);
+                if (!ok) break;
                 fence_after();
-                const uint32_t d = tmem + acc * uint32_t(a.acc_stride);
-                const uint32_t in = instr | (uint32_t(o.n / 8) << 17);
-                for (int kb = 0; ok && kb < o.kblocks; ++kb) {
-                    ok = barrier_wait(smem_addr(&ctl.full[s]), phase, failed);
-                    if (!ok) break;
-                    fence_after();
-                    const uint32_t at = smem_addr(smem + s * a.stage_bytes);
+                const uint32_t at = first + uint32_t(s) * stage16, bar = empty + s * 8;
+                advance();
+                ready = barrier_try(full + s * 8, phase);        // the next block's
+                if (one) {
 #pragma unroll
                     for (int q = 0; q < kBlockK / 16; ++q)
-                        mma<CTAS>(d, operand(at + q * kStepBytes<A_MN>),
-                                  operand(at + kStageA + q * kStepBytes<B_MN>), in,
-                                  kb > 0 || q > 0);
-                    mma_commit<CTAS>(smem_addr(&ctl.empty[s]));
-                    advance();
+                        mma<CTAS>(d, at + q * kStep16<A_MN>,
+                                  at + (kStageA >> 4) + q * kStep16<B_MN>, in, kb > 0 || q > 0);
+                    mma_commit<CTAS>(bar);
                 }
-                if (ok) mma_commit<CTAS>(smem_addr(&ctl.acc_full[acc]));
+                __syncwarp();
             }
-            ok = __shfl_sync(kAll, int(ok), 0);
+            if (ok && one) mma_commit<CTAS>(smem_addr(&ctl.acc_full[acc]));
             ++it;
         }
     } else if (warp >= 4 && warp < 4 + kEpilogueWarps) {
