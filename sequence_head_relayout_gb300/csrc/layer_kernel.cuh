@@ -66,7 +66,70 @@ struct View {
     __device__ __forceinline__ S *at(int64_t r, int64_t c) const {
         return static_cast<S *>(p) + r * row + c * col;
     }
+
+    // The same where units of VW > 1 elements are taken: their column stride is 1.
+    template <class S, int VW>
+    __device__ __forceinline__ S *unit(int64_t r, int u) const {
+        if constexpr (VW > 1) return static_cast<S *>(p) + r * row + int64_t(u) * VW;
+        return at<S>(r, u);
+    }
 };
+
+// VW float32 operations, two to an instruction where there are two: a * b, and
+// a * b + c rounded once.  b may be one value for all.
+template <int VW>
+__device__ __forceinline__ void mul_n(const float (&a)[VW], const float (&b)[VW],
+                                      float (&o)[VW]) {
+    if constexpr (VW == 1) {
+        o[0] = a[0] * b[0];
+    } else {
+#pragma unroll
+        for (int i = 0; i < VW; i += 2) {
+            const float2 p = mul2_rn(make_float2(a[i], a[i + 1]), make_float2(b[i], b[i + 1]));
+            o[i] = p.x, o[i + 1] = p.y;
+        }
+    }
+}
+template <int VW>
+__device__ __forceinline__ void mul_n(const float (&a)[VW], float b, float (&o)[VW]) {
+    float all[VW];
+#pragma unroll
+    for (int i = 0; i < VW; ++i) all[i] = b;
+    mul_n<VW>(a, all, o);
+}
+template <int VW>
+__device__ __forceinline__ void fma_n(const float (&a)[VW], const float (&b)[VW],
+                                      const float (&c)[VW], float (&o)[VW]) {
+    if constexpr (VW == 1) {
+        o[0] = fmaf(a[0], b[0], c[0]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < VW; i += 2) {
+            const float2 p = fma2_rn(make_float2(a[i], a[i + 1]), make_float2(b[i], b[i + 1]),
+                                     make_float2(c[i], c[i + 1]));
+            o[i] = p.x, o[i + 1] = p.y;
+        }
+    }
+}
+template <int VW>
+__device__ __forceinline__ void fma_n(const float (&a)[VW], float b, const float (&c)[VW],
+                                      float (&o)[VW]) {
+    float all[VW];
+#pragma unroll
+    for (int i = 0; i < VW; ++i) all[i] = b;
+    fma_n<VW>(a, all, c, o);
+}
+// The sum of a * b added to two running sums.
+template <int VW>
+__device__ __forceinline__ void dot_n(const float (&a)[VW], const float (&b)[VW], float2 &sum) {
+    if constexpr (VW == 1) {
+        sum.x = fmaf(a[0], b[0], sum.x);
+    } else {
+#pragma unroll
+        for (int i = 0; i < VW; i += 2)
+            sum = fma2_rn(make_float2(a[i], a[i + 1]), make_float2(b[i], b[i + 1]), sum);
+    }
+}
 
 // ---- gated activation ------------------------------------------------------------
 
@@ -96,7 +159,6 @@ expert_glu_rows(const __grid_constant__ GluArgs a) {
     const int used = min(max(a.offsets[a.E], 0), a.rows);
     const int unit = int(blockIdx.x % uint32_t(a.col_blocks) * blockDim.x + threadIdx.x);
     if (unit >= a.units) return;
-    const int64_t c = int64_t(unit) * VW;
     const int64_t step = int64_t(gridDim.x / uint32_t(a.col_blocks)) * blockDim.y * U;
     for (int64_t r0 = (int64_t(blockIdx.x / uint32_t(a.col_blocks)) * blockDim.y + threadIdx.y) * U;
          r0 < used; r0 += step) {
@@ -110,9 +172,9 @@ expert_glu_rows(const __grid_constant__ GluArgs a) {
 #pragma unroll
         for (int i = 0; i < U; ++i)
             if (there[i]) {
-                gate[i].load(a.gate.at<const S>(r0 + i, c));
-                up[i].load(a.up.at<const S>(r0 + i, c));
-                if constexpr (BACKWARD) grad[i].load(a.grad.at<const S>(r0 + i, c));
+                gate[i].load(a.gate.unit<const S, VW>(r0 + i, unit));
+                up[i].load(a.up.unit<const S, VW>(r0 + i, unit));
+                if constexpr (BACKWARD) grad[i].load(a.grad.unit<const S, VW>(r0 + i, unit));
             }
 #pragma unroll
         for (int i = 0; i < U; ++i) {
@@ -134,8 +196,8 @@ expert_glu_rows(const __grid_constant__ GluArgs a) {
                 if (!there[i]) y[j] = u[j] = 0.0f;         // a gap row
             }
             if (r0 + i >= used) continue;
-            round_unit<E, VW>(y).store(a.out.at<S>(r0 + i, c));
-            if constexpr (BACKWARD) round_unit<E, VW>(u).store(a.out_up.at<S>(r0 + i, c));
+            round_unit<E, VW>(y).store(a.out.unit<S, VW>(r0 + i, unit));
+            if constexpr (BACKWARD) round_unit<E, VW>(u).store(a.out_up.unit<S, VW>(r0 + i, unit));
         }
     }
 }
@@ -156,7 +218,7 @@ struct NormArgs {
     int32_t warps;                // warps of a row
     int32_t group, groups;        // columns to a scale, scales of a row
     float eps, inv_m;             // 1 / M
-    int32_t blocks;
+    int32_t blocks, stages;
 };
 
 template <class E, int VW>
@@ -226,6 +288,39 @@ __device__ __forceinline__ uint8_t encode32(float y, float inv) {
         return uint8_t(__nv_cvt_float_to_fp8(q, __NV_SATFINITE, __NV_E4M3));
 }
 
+// Eight values to eight codes, with the steps of encode8 (|y| is at most the
+// group's amax, so that no INT8 clamp would act).
+template <int FMT>
+__device__ __forceinline__ uint2 encode32x8(const float (&y)[8], float inv) {
+    uint32_t out[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        uint32_t lo, hi;
+        if constexpr (FMT == kFmtInt8) {
+            lo = __byte_perm(rint_bits(__fmul_rn(y[4 * k], inv)),
+                             rint_bits(__fmul_rn(y[4 * k + 1], inv)), 0x0040);
+            hi = __byte_perm(rint_bits(__fmul_rn(y[4 * k + 2], inv)),
+                             rint_bits(__fmul_rn(y[4 * k + 3], inv)), 0x0040);
+        } else {
+            const float2 inv2 = make_float2(inv, inv);
+            lo = __nv_cvt_float2_to_fp8x2(mul2_rn(make_float2(y[4 * k], y[4 * k + 1]), inv2),
+                                          __NV_SATFINITE, __NV_E4M3);
+            hi = __nv_cvt_float2_to_fp8x2(mul2_rn(make_float2(y[4 * k + 2], y[4 * k + 3]), inv2),
+                                          __NV_SATFINITE, __NV_E4M3);
+        }
+        out[k] = __byte_perm(lo, hi, 0x5410);
+    }
+    return make_uint2(out[0], out[1]);
+}
+
+// The larger magnitude of two floats in one instruction, the sign as it falls; NaN
+// where one is NaN.
+__device__ __forceinline__ float max_magnitude32(float a, float b) {
+    float d;
+    asm("max.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
 // The norm with a row held in the registers of a.warps warps, NV units of VW
 // elements to a lane.  FMT: 0 writes out, else codes (VW = 8, a group is 4 to 32
 // lanes).
@@ -245,64 +340,82 @@ norm_rows(const __grid_constant__ NormArgs a) {
         const int unit = (j * a.warps + part) * 32 + lane;
         there[j] = t < a.T && unit < a.units;
         x[j].b = other[j].b = {};
-        if (there[j]) x[j].load(a.x.at<const S>(t, int64_t(unit) * VW));
+        if (there[j]) x[j].load(a.x.unit<const S, VW>(t, unit));
     }
-    float squares = 0.0f;
+    float y[NV][VW];
     if (a.residual.p) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int unit = (j * a.warps + part) * 32 + lane;
-            if (there[j]) other[j].load(a.residual.at<const S>(t, int64_t(unit) * VW));
+            if (there[j]) other[j].load(a.residual.unit<const S, VW>(t, unit));
         }
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int unit = (j * a.warps + part) * 32 + lane;
-            float f[VW], g[VW];
-            widen_unit<E, VW>(x[j], f);
-            widen_unit<E, VW>(other[j], g);
-#pragma unroll
-            for (int i = 0; i < VW; ++i) f[i] += g[i];
+            float f[VW];
+            widen_unit<E, VW>(x[j], y[j]);
+            widen_unit<E, VW>(other[j], f);
+            fma_n<VW>(y[j], 1.0f, f, f);                   // the sum, rounded once
             x[j] = round_unit<E, VW>(f);
-            if (there[j]) x[j].store(a.total.at<S>(t, int64_t(unit) * VW));
+            if (there[j]) x[j].store(a.total.unit<S, VW>(t, unit));
         }
     }
+    float2 squares = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        float f[VW];
-        widen_unit<E, VW>(x[j], f);
-#pragma unroll
-        for (int i = 0; i < VW; ++i) squares = fmaf(f[i], f[i], squares);
+        widen_unit<E, VW>(x[j], y[j]);
+        dot_n<VW>(y[j], y[j], squares);
     }
-    const float r = inverse_rms(a, row_sum(squares, parts, a.warps));
+    const float r = inverse_rms(a, row_sum(squares.x + squares.y, parts, a.warps));
+    // A group's scale takes two divisions and is the same in all of its lanes: lane j of
+    // a group (it has four at least) divides for unit j, and the others get it from
+    // there (at T = 55,414, M = 3,584, E4M3: 296 us with all of them in every lane).
+    static_assert(FMT == 0 || NV <= 4, "a lane of the group for every unit");
+    uint32_t largest[NV] = {};
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         const int unit = (j * a.warps + part) * 32 + lane;
         const int64_t c = int64_t(unit) * VW;
-        float f[VW], w[VW];
-        widen_unit<E, VW>(x[j], f);
+        float w[VW];
 #pragma unroll
         for (int i = 0; i < VW; ++i) w[i] = 0.0f;
         if (there[j]) load_weight<E, VW>(a, c, w);
-#pragma unroll
-        for (int i = 0; i < VW; ++i) f[i] = f[i] * r * w[i];
+        mul_n<VW>(y[j], r, y[j]);
+        mul_n<VW>(y[j], w, y[j]);
         if constexpr (FMT == 0) {
-            if (there[j]) round_unit<E, VW>(f).store(a.out.at<S>(t, c));
+            if (there[j]) round_unit<E, VW>(y[j]).store(a.out.unit<S, VW>(t, unit));
         } else {
-            uint32_t m = 0;
+            float m = 0.0f;
 #pragma unroll
-            for (int i = 0; i < VW; ++i)
-                m = max(m, there[j] ? __float_as_uint(f[i]) & 0x7FFFFFFFu : 0u);
-            const int lanes = a.group / VW;
-            for (int o = 1; o < lanes; o <<= 1) m = max(m, __shfl_xor_sync(kAll, m, o));
-            float inv, scale;
-            const bool live = group_scale32(m, top_code<FMT>(), inv, scale);
-            uint8_t code[VW];
+            for (int i = 0; i < VW; ++i) m = max_magnitude32(m, y[j][i]);
+            // (a zero times a NaN or an infinite root is a NaN: not in the row's columns)
+            largest[j] = there[j] ? __float_as_uint(m) & 0x7FFFFFFFu : 0u;
+        }
+    }
+    if constexpr (FMT != 0) {
+        const int lanes = a.group / VW;
+        for (int o = 1; o < lanes; o <<= 1)
 #pragma unroll
-            for (int i = 0; i < VW; ++i) code[i] = live ? encode32<FMT>(f[i], inv) : uint8_t(0);
-            if (there[j]) {
-                store_unit<uint8_t, VW>(a.codes + t * a.M + c, code);
-                if (lane % lanes == 0) a.scales[t * a.groups + unit / lanes] = scale;
-            }
+            for (int j = 0; j < NV; ++j)
+                largest[j] = max(largest[j], __shfl_xor_sync(kAll, largest[j], o));
+        const int mine = lane % lanes, first = lane - mine;
+        uint32_t m = largest[0];
+#pragma unroll
+        for (int j = 1; j < NV; ++j) m = mine == j ? largest[j] : m;
+        float inv, scale;
+        const bool live = group_scale32(m, top_code<FMT>(), inv, scale);
+        if (!live) inv = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int unit = (j * a.warps + part) * 32 + lane;
+            const float q = __shfl_sync(kAll, inv, first + j);
+            uint2 code = encode32x8<FMT>(y[j], q);
+            if (q == 0.0f) code = make_uint2(0, 0);        // not live: NaN and infinities too
+            if (there[j])
+                *reinterpret_cast<uint2 *>(a.codes + t * a.M + int64_t(unit) * VW) = code;
+            // (lane j of a row's last group may lie behind the row's end)
+            if (mine == j && t < a.T && unit - mine < a.units)
+                a.scales[t * a.groups + unit / lanes] = scale;
         }
     }
 }
@@ -377,68 +490,146 @@ norm_any(const __grid_constant__ NormArgs a) {
     }
 }
 
-// The norm's backward pass: rows in registers as in norm_rows.  A block walks its
-// rows with the weight's gradient in registers and leaves it in a.partial.
+// Two sums over a row's warps by one barrier; `turn` alternates from call to call.
+__device__ __forceinline__ float2 row_sums(float u, float v, float2 (*parts)[32], int turn,
+                                           int warps) {
+    float2 s = make_float2(warp_sum(u), warp_sum(v));
+    if (warps == 1) return s;
+    const int warp = int(threadIdx.x >> 5);
+    if ((threadIdx.x & 31) == 0) parts[turn][warp] = s;
+    __syncthreads();
+    const int first = warp - warp % warps;
+    s = make_float2(0.0f, 0.0f);
+    for (int i = 0; i < warps; ++i) {
+        s.x += parts[turn][first + i].x;
+        s.y += parts[turn][first + i].y;
+    }
+    return s;
+}
+
+// A unit of global memory to shared memory, behind the thread's back; the hardware
+// has such copies from 4 bytes on.
+__host__ __device__ constexpr bool copies_rows(int size, int vw) { return size == 2 && vw > 1; }
+
+template <class S, int VW>
+__device__ __forceinline__ void copy_unit(Unit<S, VW> *to, const S *from) {
+    constexpr int bytes = int(sizeof(Unit<S, VW>));
+    const uint32_t at = uint32_t(__cvta_generic_to_shared(to));
+    if constexpr (bytes == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(from) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;"
+                     ::"r"(at), "l"(from), "n"(bytes >= 4 ? bytes : 4) : "memory");
+}
+__device__ __forceinline__ void commit_copies() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// The norm's backward pass.  A block walks its rows, a.warps warps to each, with the
+// weight's gradient in registers, and leaves it in a.partial.  What bounds the pass
+// is the bytes in flight.  Rows of 16-bit elements are copied to shared memory (a
+// thread's units to places that no other thread touches), a row ahead of the one that
+// is worked on; their values take too many registers for enough of them to be
+// loaded at a time (bf16, T = 55,414, M = 3,584, with grad_total: 280 us, 335 with the
+// rows in registers).  Rows of float32 stay in registers (T = 55,413, M = 2,048: 271
+// us, 314 through shared memory).
 template <class E, int VW, int NV>
 __global__ void __launch_bounds__(512)
 norm_backward_rows(const __grid_constant__ NormArgs a) {
     using S = typename E::S;
-    __shared__ float parts[32];
-    extern __shared__ float sums[];                        // [M], with more than one row
+    using U = Unit<S, VW>;
+    constexpr bool kCopies = copies_rows(int(sizeof(S)), VW);
+    __shared__ float2 parts[2][32];
+    extern __shared__ uint4 dynamic[];     // [stages][h, g, more][NV][threads] units
     wait_for_previous_grid();
     const int lane = int(threadIdx.x & 31), warp = int(threadIdx.x >> 5);
     const int part = warp % a.warps, rows = int(blockDim.x / 32 / a.warps);
+    U *const ring = reinterpret_cast<U *>(dynamic) + threadIdx.x;
+    const int step = int(blockDim.x);
     float dw[NV][VW] = {};
-    for (int64_t t0 = int64_t(blockIdx.x) * rows; t0 < a.T; t0 += int64_t(gridDim.x) * rows) {
-        const int64_t t = t0 + warp / a.warps;
-        Unit<S, VW> h[NV], g[NV];
+    const auto fetch = [&](int64_t t, U *to) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int unit = (j * a.warps + part) * 32 + lane;
-            h[j].b = g[j].b = {};
             if (t < a.T && unit < a.units) {
-                h[j].load(a.x.at<const S>(t, int64_t(unit) * VW));
-                g[j].load(a.grad.at<const S>(t, int64_t(unit) * VW));
+                copy_unit(to + j * step, a.x.unit<const S, VW>(t, unit));
+                copy_unit(to + (NV + j) * step, a.grad.unit<const S, VW>(t, unit));
+                if (a.grad_total.p)
+                    copy_unit(to + (2 * NV + j) * step, a.grad_total.unit<const S, VW>(t, unit));
             }
         }
-        float squares = 0.0f, dot = 0.0f;
+        commit_copies();
+    };
+    const int64_t ahead = int64_t(gridDim.x) * rows;
+    int64_t t = int64_t(blockIdx.x) * rows + warp / a.warps;
+    if constexpr (kCopies) fetch(t, ring);
+    int turn = 0;
+    for (int64_t t0 = int64_t(blockIdx.x) * rows; t0 < a.T; t0 += ahead, t += ahead) {
+        U *const here = ring + turn * 3 * NV * step;
+        U held[3][NV];
+        if constexpr (!kCopies) {
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int unit = (j * a.warps + part) * 32 + lane;
+                held[0][j].b = held[1][j].b = held[2][j].b = {};
+                if (t < a.T && unit < a.units) {
+                    held[0][j].load(a.x.unit<const S, VW>(t, unit));
+                    held[1][j].load(a.grad.unit<const S, VW>(t, unit));
+                    if (a.grad_total.p) held[2][j].load(a.grad_total.unit<const S, VW>(t, unit));
+                }
+            }
+        } else if (a.stages > 1) {
+            fetch(t + ahead, ring + (turn ^ 1) * 3 * NV * step);
+            wait_copies<1>();
+        } else {
+            wait_copies<0>();
+        }
+        const auto row = [&](int which, int j) {
+            if constexpr (kCopies) return here[(which * NV + j) * step];
+            else return held[which][j];
+        };
+        float2 squares = make_float2(0.0f, 0.0f), dot = squares;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int unit = (j * a.warps + part) * 32 + lane;
-            float f[VW], d[VW], w[VW] = {};
-            if (unit < a.units) load_weight<E, VW>(a, int64_t(unit) * VW, w);
-            widen_unit<E, VW>(h[j], f);
-            widen_unit<E, VW>(g[j], d);
-#pragma unroll
-            for (int i = 0; i < VW; ++i) {
-                squares = fmaf(f[i], f[i], squares);
-                dot = fmaf(w[i] * d[i], f[i], dot);
-            }
+            if (t >= a.T || unit >= a.units) continue;
+            float f[VW], d[VW], w[VW];
+            load_weight<E, VW>(a, int64_t(unit) * VW, w);
+            widen_unit<E, VW>(row(0, j), f);
+            widen_unit<E, VW>(row(1, j), d);
+            dot_n<VW>(f, f, squares);
+            mul_n<VW>(d, w, d);
+            dot_n<VW>(d, f, dot);
         }
-        const float r = inverse_rms(a, row_sum(squares, parts, a.warps));
-        const float q = r * r * (row_sum(dot, parts, a.warps) * a.inv_m);
+        const float2 both =
+            row_sums(squares.x + squares.y, dot.x + dot.y, parts, turn, a.warps);
+        const float r = inverse_rms(a, both.x);
+        const float q = r * r * (both.y * a.inv_m);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int unit = (j * a.warps + part) * 32 + lane;
-            const int64_t c = int64_t(unit) * VW;
-            const bool there = t < a.T && unit < a.units;
-            float f[VW], d[VW], w[VW] = {}, more[VW] = {};
-            if (unit < a.units) load_weight<E, VW>(a, c, w);
-            if (there && a.grad_total.p) {
-                Unit<S, VW> u;
-                u.load(a.grad_total.at<const S>(t, c));
-                widen_unit<E, VW>(u, more);
-            }
-            widen_unit<E, VW>(h[j], f);
-            widen_unit<E, VW>(g[j], d);
-#pragma unroll
-            for (int i = 0; i < VW; ++i) {
-                if (there) dw[j][i] = fmaf(d[i], f[i] * r, dw[j][i]);
-                d[i] = r * (w[i] * d[i] - f[i] * q) + more[i];
-            }
-            if (there) round_unit<E, VW>(d).store(a.grad_x.at<S>(t, c));
+            if (t >= a.T || unit >= a.units) continue;
+            float f[VW], d[VW], w[VW], m[VW] = {};
+            load_weight<E, VW>(a, int64_t(unit) * VW, w);
+            widen_unit<E, VW>(row(0, j), f);
+            widen_unit<E, VW>(row(1, j), d);
+            mul_n<VW>(d, w, w);
+            fma_n<VW>(f, -q, w, w);                        // w g - h q
+            mul_n<VW>(f, r, f);
+            fma_n<VW>(d, f, dw[j], dw[j]);
+            if (a.grad_total.p) widen_unit<E, VW>(row(2, j), m);
+            fma_n<VW>(w, r, m, m);
+            round_unit<E, VW>(m).store(a.grad_x.unit<S, VW>(t, unit));
         }
+        turn ^= 1;
     }
+    if constexpr (kCopies) wait_copies<0>();
+    __syncthreads();                                       // the ring's memory is free
+    float *sums = reinterpret_cast<float *>(dynamic);      // [M], with more than one row
     // the block's rows one after the other, so that the order is fixed
     float *mine = a.partial + int64_t(blockIdx.x) * a.M;
     for (int row = 0; row < rows; ++row) {

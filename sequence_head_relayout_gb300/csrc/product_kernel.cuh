@@ -54,6 +54,7 @@ struct ProductArgs {
     int32_t E, rows;
     int32_t feat, cols, red;      // features; weights: columns; rows: length of the sums
     int32_t feat_tiles, col_tiles;
+    int32_t step_experts, step_tiles;    // weights: the grid's tiles, in experts and the rest
     int32_t tile_n;               // most rows (columns) of a tile
     int32_t box;                  // rows form: a copy of B has one to kBoxes times as many rows
     int32_t stages, stage_bytes;
@@ -296,6 +297,9 @@ template <bool MN> constexpr uint32_t kStep16 = MN ? 16 * 128 / 16 : 2;
 
 // ---- tiles ---------------------------------------------------------------------
 
+// ceil(n / d), for n up to 2^31 - 1
+__device__ __forceinline__ int parts(int n, int d) { return n / d + (n % d != 0); }
+
 struct Tile {
     int e, f0;         // expert, first feature
     int row0, valid;   // rows: first row and rows of the tile; weights: of the expert
@@ -314,16 +318,26 @@ struct Tiles {
     static constexpr int kStep = 16 * CTAS;
     const ProductArgs &a;
     int lane;
-    int64_t t, step;              // this tile, and what is added for the next
     // rows form
+    int64_t t, step;              // this tile, and what is added for the next
     int base = -128;              // first expert of the warp's 128
     int64_t before = 0;           // tiles before it
     int64_t total = 0;            // tiles of the 128
     int64_t first = 0;            // tiles of the 128 before the lane's four experts
     int count[4], begin[4];
+    // weights form: the tile as a number within its expert
+    int e, in, each;
+    int next_row0, next_valid;    // loaded a tile ahead
 
     __device__ __forceinline__ explicit Tiles(const ProductArgs &args)
-        : a(args), lane(int(threadIdx.x & 31)), t(blockIdx.x / CTAS), step(gridDim.x / CTAS) {}
+        : a(args), lane(int(threadIdx.x & 31)), t(blockIdx.x / CTAS), step(gridDim.x / CTAS) {
+        if constexpr (WEIGHTS) {
+            each = a.feat_tiles * a.col_tiles;
+            e = int(t) / each;
+            in = int(t) - e * each;
+            segment(min(e, a.E - 1), next_row0, next_valid);
+        }
+    }
 
     // Rows of an expert that exist, whatever the plan says.
     __device__ __forceinline__ void segment(int e, int &begin_, int &count_) const {
@@ -332,12 +346,11 @@ struct Tiles {
     }
 
     __device__ __forceinline__ int64_t tiles_of(int n) const {
-        return int64_t((n + a.tile_n - 1) / a.tile_n) * a.feat_tiles;
+        return int64_t(parts(n, a.tile_n)) * a.feat_tiles;
     }
 
-    __device__ bool next(Tile &o) {
+    __device__ __forceinline__ bool next(Tile &o) {
         const bool there = WEIGHTS ? next_weights(o) : next_rows(o);
-        t += step;
         o.e = uniform(o.e);
         o.f0 = uniform(o.f0);
         o.c0 = uniform(o.c0);
@@ -348,23 +361,29 @@ struct Tiles {
         return __all_sync(kAll, int(there));
     }
 
-    __device__ bool next_weights(Tile &o) {
-        const int64_t each = int64_t(a.feat_tiles) * a.col_tiles;
-        if (t >= each * a.E) return false;
-        o.e = int(t / each);
-        const int in = int(t - o.e * each);
+    __device__ __forceinline__ bool next_weights(Tile &o) {
+        if (e >= a.E) return false;
+        o.e = e;
         o.f0 = in % a.feat_tiles * (kTileM * CTAS);
         o.c0 = in / a.feat_tiles * a.tile_n;
         // (each CTA's share of B starts at a whole slab)
         const int multiple = a.b_slabs ? 64 * CTAS : kStep;
         o.n = (min(a.tile_n, a.cols - o.c0) + multiple - 1) / multiple * multiple;
-        segment(o.e, o.row0, o.valid);
-        o.kblocks = (o.valid + kBlockK - 1) / kBlockK;
+        o.row0 = next_row0;
+        o.valid = next_valid;
+        o.kblocks = parts(o.valid, kBlockK);
         o.gap = 0;
+        e += a.step_experts;
+        in += a.step_tiles;
+        if (in >= each) {
+            in -= each;
+            ++e;
+        }
+        segment(min(e, a.E - 1), next_row0, next_valid);
         return true;
     }
 
-    __device__ bool next_rows(Tile &o) {
+    __device__ __forceinline__ bool next_rows(Tile &o) {
         while (t >= before + total) {
             base += 128;
             if (base >= a.E) return false;
@@ -404,9 +423,10 @@ struct Tiles {
         b = __shfl_sync(kAll, b, owner);
         rest = __shfl_sync(kAll, rest, owner);
         o.e = base + 4 * owner + __shfl_sync(kAll, i, owner);
-        const int row_tiles = (c + a.tile_n - 1) / a.tile_n;
-        const int part = ((c + row_tiles - 1) / row_tiles + kStep - 1) / kStep * kStep;
-        const int f = int(rest / row_tiles), r = int(rest - int64_t(f) * row_tiles);
+        const int row_tiles = parts(c, a.tile_n);
+        const int part = parts(parts(c, row_tiles), kStep) * kStep;
+        const int f = rest >> 32 ? int(rest / row_tiles) : int(uint32_t(rest) / uint32_t(row_tiles));
+        const int r = int(rest - int64_t(f) * row_tiles);
         o.f0 = f * (kTileM * CTAS);
         o.row0 = b + r * part;
         o.valid = min(part, c - r * part);
@@ -416,6 +436,7 @@ struct Tiles {
         o.gap = 0;
         if (a.gaps && r == row_tiles - 1)
             o.gap = max(0, min(a.offsets[o.e + 1], a.rows) - (b + c));
+        t += step;
         return true;
     }
 };

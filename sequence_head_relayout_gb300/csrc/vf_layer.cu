@@ -136,6 +136,10 @@ int glu(const vf_glu_desc *d, bool backward, cudaStream_t stream) {
 
 constexpr int64_t kNormColumns = int64_t(1) << 24;         // M
 
+// The most that the backward pass takes: two stages of three rows, four units of 16
+// bytes to each of 512 threads.
+constexpr int kNormShared = 2 * 3 * 4 * 16 * 512;
+
 int64_t norm_blocks(int64_t T) { return std::min<int64_t>(T, kSMs * 4); }
 
 using NormKernel = void (*)(vf::NormArgs);
@@ -223,8 +227,8 @@ struct RowShape {
     int64_t nv, warps, rows;       // rows of a block
 };
 
-RowShape row_shape(int64_t units, int64_t T, int64_t most_warps) {
-    RowShape s = {4, 0, 1};
+RowShape row_shape(int64_t units, int64_t T, int64_t most_warps, int64_t nv) {
+    RowShape s = {nv, 0, 1};
     if (T <= kSMs * 4) s.nv = 1;   // few rows: more warps to each
     while (s.nv < 4 && ceil_div(units, 32 * s.nv) > most_warps) s.nv *= 2;
     while (s.nv > 1 && ceil_div(units, 32) <= s.nv / 2) s.nv /= 2;
@@ -281,7 +285,7 @@ int norm(const vf_norm_desc *d, cudaStream_t stream) {
     }
     take_weight(&w, d);
     a.units = int32_t(M / w.vw);
-    const RowShape s = row_shape(a.units, T, 32);
+    const RowShape s = row_shape(a.units, T, 32, 4);
     a.warps = int32_t(s.warps);
     // rows that do not fit the registers of a block, and unaligned ones with codes
     if (s.warps > 32 || (fmt && w.vw < 8)) {
@@ -337,7 +341,7 @@ int norm_backward(const vf_norm_desc *d, cudaStream_t stream) {
         }
         take_weight(&w, d);
         a.units = int32_t(M / w.vw);
-        const RowShape s = row_shape(a.units, T, 16);
+        const RowShape s = row_shape(a.units, T, 16, 2);
         a.warps = int32_t(s.warps);
         if (s.warps > 16) {
             a.blocks = int32_t(norm_blocks(T));
@@ -351,9 +355,21 @@ int norm_backward(const vf_norm_desc *d, cudaStream_t stream) {
                 d->type == VF_TYPE_BF16  ? backward_kernel<vf::Bf16>(w.vw, s.nv)
                 : d->type == VF_TYPE_F16 ? backward_kernel<vf::F16>(w.vw, s.nv)
                                          : backward_kernel<vf::F32>(w.vw, s.nv);
-            // a row of more than one to a block has at most 4 warps: 32 kB of sums
-            rc = launch(kernel, a.blocks, int(s.warps * s.rows * 32),
-                        s.rows > 1 ? size_t(M) * 4 : 0, stream, a);
+            // shared memory: two rows to a group of warps where there are two to walk;
+            // the block's sums (s.rows > 1 has at most 2 units to a lane)
+            a.stages = ceil_div(T, s.rows) > a.blocks ? 2 : 1;
+            const int64_t threads = s.warps * s.rows * 32;
+            const bool copies = vf::copies_rows(int(size), int(w.vw));
+            const size_t smem = size_t(
+                std::max(copies ? a.stages * 3 * s.nv * threads * w.vw * size : 0,
+                         s.rows > 1 ? M * 4 : 0));
+            if (smem > 47 * 1024 &&
+                cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     kNormShared) != cudaSuccess) {
+                cudaGetLastError();
+                return VF_ERR_CUDA;
+            }
+            rc = launch(kernel, a.blocks, int(threads), smem, stream, a);
         }
         if (rc != VF_OK) return rc;
     }

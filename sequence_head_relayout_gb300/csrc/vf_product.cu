@@ -105,9 +105,14 @@ void set_form(vfp::ProductArgs *a, const Form &f, bool fill) {
 
 using Kernel = void (*)(vfp::ProductArgs);
 
-int launch_product(Kernel kernel, const vfp::ProductArgs &a, int64_t ctas, int64_t tiles,
+int launch_product(Kernel kernel, vfp::ProductArgs &a, int64_t ctas, int64_t tiles,
                    cudaStream_t stream, int threads = vfp::kThreads) {
     if (tiles == 0) return VF_OK;
+    const int64_t groups = std::min(kSMs / ctas, tiles);
+    if (a.col_tiles > 0) {
+        a.step_experts = int32_t(groups / (int64_t(a.feat_tiles) * a.col_tiles));
+        a.step_tiles = int32_t(groups % (int64_t(a.feat_tiles) * a.col_tiles));
+    }
     // on every call, so that no state is kept per device, and always the same number
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              int(kSharedMemory)) != cudaSuccess) {
@@ -115,7 +120,7 @@ int launch_product(Kernel kernel, const vfp::ProductArgs &a, int64_t ctas, int64
         return VF_ERR_CUDA;
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(std::min(kSMs / ctas, tiles) * ctas), 1, 1);
+    cfg.gridDim = dim3(unsigned(groups * ctas), 1, 1);
     cfg.blockDim = dim3(unsigned(threads), 1, 1);
     cfg.dynamicSmemBytes = size_t(vfp::shared_bytes(a.stages, a.stage_bytes));
     cfg.stream = stream;
@@ -127,7 +132,7 @@ int launch_product(Kernel kernel, const vfp::ProductArgs &a, int64_t ctas, int64
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = ctas > 1 ? 2 : 1;
     if (cudaLaunchKernelEx(&cfg, kernel, a) != cudaSuccess) {
         cudaGetLastError();
         return VF_ERR_CUDA;
