@@ -45,6 +45,7 @@ and merges refuse a tensor that requires a gradient while grad mode is on.
 """
 import ctypes
 import os
+import struct
 from typing import NamedTuple
 
 import torch
@@ -89,34 +90,11 @@ class _ExpertDesc(ctypes.Structure):
                 ("grad_packed", _P), ("grad_weights", _P)]
 
 
-class _ProductDesc(ctypes.Structure):
-    """vf_product_desc of the C ABI."""
-    _fields_ = [("type", ctypes.c_int32), ("out_type", ctypes.c_int32),
-                ("E", _I64), ("N", _I64), ("M", _I64), ("rows", _I64), ("slots", _I64),
-                ("align", _I64), ("counts", _P), ("offsets", _P), ("packed", _P),
-                ("weights", _P), ("weight_strides", _I64 * 3), ("grad", _P), ("out", _P),
-                ("grad_weights", _P)]
-
-
-class _GluDesc(ctypes.Structure):
-    """vf_glu_desc of the C ABI."""
-    _fields_ = [("type", ctypes.c_int32), ("E", _I64), ("rows", _I64), ("F", _I64),
-                ("slot_of", _P), ("offsets", _P)]
-    for _name in ("gate", "up", "out", "grad", "grad_gate", "grad_up"):
-        _fields_ += [(_name, _P), (_name + "_strides", _I64 * 2)]
-
-
-class _NormDesc(ctypes.Structure):
-    """vf_norm_desc of the C ABI."""
-    _fields_ = [("type", ctypes.c_int32), ("weight_type", ctypes.c_int32),
-                ("format", ctypes.c_int32), ("eps", ctypes.c_float),
-                ("T", _I64), ("M", _I64), ("group", _I64), ("x", _P), ("x_strides", _I64 * 2),
-                ("weight", _P), ("residual", _P), ("residual_strides", _I64 * 2),
-                ("total", _P), ("total_strides", _I64 * 2), ("out", _P),
-                ("out_strides", _I64 * 2), ("codes", _P), ("scales", _P), ("grad", _P),
-                ("grad_strides", _I64 * 2), ("grad_total", _P),
-                ("grad_total_strides", _I64 * 2), ("grad_x", _P), ("grad_x_strides", _I64 * 2),
-                ("grad_weight", _P), ("workspace", _P)]
+# The descriptors of the calls below the expert relayouts are packed by one call each,
+# which takes 1 us where setting the fields of a ctypes structure takes 3 to 4.
+_PRODUCT_DESC = struct.Struct("@ii16q")      # vf_product_desc of the C ABI
+_GLU_DESC = struct.Struct("@iq22q")          # vf_glu_desc
+_NORM_DESC = struct.Struct("@iiif29q")       # vf_norm_desc
 
 
 class VFError(RuntimeError):
@@ -185,14 +163,10 @@ def lib():
             f = getattr(l, name)
             f.argtypes = [ctypes.POINTER(_ExpertDesc), _P]
             f.restype = ctypes.c_int
-        for name in ("vf_expert_product", "vf_expert_weight_grad"):
+        for name in ("vf_expert_product", "vf_expert_weight_grad", "vf_expert_glu",
+                     "vf_expert_glu_backward", "vf_rms_norm", "vf_rms_norm_backward"):
             f = getattr(l, name)
-            f.argtypes = [ctypes.POINTER(_ProductDesc), _P]
-            f.restype = ctypes.c_int
-        for name, desc in (("vf_expert_glu", _GluDesc), ("vf_expert_glu_backward", _GluDesc),
-                           ("vf_rms_norm", _NormDesc), ("vf_rms_norm_backward", _NormDesc)):
-            f = getattr(l, name)
-            f.argtypes = [ctypes.POINTER(desc), _P]
+            f.argtypes = [ctypes.c_char_p, _P]
             f.restype = ctypes.c_int
         l.vf_rms_norm_workspace.argtypes = [_I64, _I64]
         l.vf_rms_norm_workspace.restype = _I64
@@ -963,6 +937,12 @@ def expert_merge_backward_q(grad: torch.Tensor, codes: torch.Tensor, scales: tor
 
 # ---- expert products -------------------------------------------------------------
 
+def _desc_call(fn, desc, stream, like):
+    rc = getattr(_lib or lib(), fn)(desc, _stream(stream, like.device))
+    if rc != 0:
+        raise VFError(fn, rc)
+
+
 def _product_rows(t, what):
     """vf_type of contiguous packed rows that a product takes."""
     if not isinstance(t, torch.Tensor):
@@ -977,12 +957,12 @@ def _product_rows(t, what):
     return f
 
 
-def _product_desc(typ, plan, dims, rows, N, M):
-    if rows != dims[2]:
-        raise ValueError("plan is for %d packed rows, not %d" % (dims[2], rows))
-    d = _ProductDesc(typ, typ, dims[3], N, M, rows, dims[0] * dims[1], plan[4])
-    d.counts, d.offsets = plan[2].data_ptr(), plan[3].data_ptr()
-    return d
+def _packed_plan(plan, n):
+    """(T, K, rows, E) of a plan for n packed rows."""
+    dims = _check_plan(plan)
+    if n != dims[2]:
+        raise ValueError("plan is for %d packed rows, not %d" % (dims[2], n))
+    return dims
 
 
 def expert_product(rows: torch.Tensor, weights: torch.Tensor, plan: ExpertPlan,
@@ -1000,19 +980,19 @@ def expert_product(rows: torch.Tensor, weights: torch.Tensor, plan: ExpertPlan,
     typ = _product_rows(rows, "rows")
     _unrecorded(rows, "rows", "expert_product with the transposed weights")
     n, M = _matrix(rows, "rows")
-    dims = _check_plan(plan)
+    T, K, _, E = _packed_plan(plan, n)
     if not (isinstance(weights, torch.Tensor) and weights.is_cuda):
         _product_rows(weights, "weights")                  # raises
     w = weights.shape
-    if weights.dtype != rows.dtype or len(w) != 3 or w[0] != dims[3] or w[2] != M:
-        raise ValueError("weights must be a %s view of shape [%d,N,%d]"
-                         % (rows.dtype, dims[3], M))
+    if weights.dtype != rows.dtype or len(w) != 3 or w[0] != E or w[2] != M:
+        raise ValueError("weights must be a %s view of shape [%d,N,%d]" % (rows.dtype, E, M))
     _unrecorded(weights, "weights", "expert_weight_grad")
-    d = _product_desc(typ, plan, dims, n, w[1], M)
-    out = _rows_out(out, stream, rows, (n, w[1]), rows.dtype, "out")
-    d.packed, d.weights, d.out = rows.data_ptr(), weights.data_ptr(), out.data_ptr()
-    d.weight_strides = weights.stride()
-    _expert_call("vf_expert_product", d, stream, rows)
+    N = w[1]
+    out = _rows_out(out, stream, rows, (n, N), rows.dtype, "out")
+    _desc_call("vf_expert_product", _PRODUCT_DESC.pack(
+        typ, typ, E, N, M, n, T * K, plan[4], plan[2].data_ptr(), plan[3].data_ptr(),
+        rows.data_ptr(), weights.data_ptr(), *weights.stride(), 0, out.data_ptr(), 0),
+        stream, rows)
     return out
 
 
@@ -1036,19 +1016,25 @@ def expert_weight_grad(grad: torch.Tensor, rows: torch.Tensor, plan: ExpertPlan,
         raise ValueError("grad and rows must have the same number of rows")
     if dtype is None:
         dtype = rows.dtype if out is None else out.dtype
-    if dtype not in (rows.dtype, torch.float32):
+    if dtype != rows.dtype and dtype != torch.float32:
         raise ValueError("dtype must be that of rows or torch.float32")
-    dims = _check_plan(plan)
-    d = _product_desc(typ, plan, dims, n, N, M)
-    out = _rows_out(out, stream, rows, (dims[3], N, M), dtype, "out")
-    if dtype == torch.float32:
-        d.out_type = 2
-    d.packed, d.grad, d.grad_weights = rows.data_ptr(), grad.data_ptr(), out.data_ptr()
-    _expert_call("vf_expert_weight_grad", d, stream, grad)
+    T, K, _, E = _packed_plan(plan, n)
+    out = _rows_out(out, stream, rows, (E, N, M), dtype, "out")
+    _desc_call("vf_expert_weight_grad", _PRODUCT_DESC.pack(
+        typ, _TYPES[dtype], E, N, M, n, T * K, plan[4], plan[2].data_ptr(), plan[3].data_ptr(),
+        rows.data_ptr(), 0, 0, 0, 0, grad.data_ptr(), 0, out.data_ptr()), stream, grad)
     return out
 
 
 # ---- gated activation ------------------------------------------------------------
+
+_NO_VIEW = (0, 0, 0)
+
+
+def _view(t):
+    s = t.stride()
+    return t.data_ptr(), s[0], s[1]
+
 
 def _same_view(t, like, what):
     """Check a view of ``like``'s shape and type."""
@@ -1060,16 +1046,12 @@ def _same_view(t, like, what):
 
 
 def _glu(gate, up, plan):
+    """The descriptor's fields that both calls fill in."""
     typ = _rows_type(gate, "gate")
     n, F = _matrix(gate, "gate")
     _same_view(up, gate, "up")
-    dims = _check_plan(plan)
-    if n != dims[2]:
-        raise ValueError("plan is for %d packed rows, not %d" % (dims[2], n))
-    d = _GluDesc(typ, dims[3], n, F, plan[1].data_ptr(), plan[3].data_ptr())
-    d.gate, d.up = gate.data_ptr(), up.data_ptr()
-    d.gate_strides, d.up_strides = gate.stride(), up.stride()
-    return d
+    E = _packed_plan(plan, n)[3]
+    return (typ, E, n, F, plan[1].data_ptr(), plan[3].data_ptr(), *_view(gate), *_view(up))
 
 
 def expert_glu(gate: torch.Tensor, up: torch.Tensor, plan: ExpertPlan,
@@ -1083,12 +1065,11 @@ def expert_glu(gate: torch.Tensor, up: torch.Tensor, plan: ExpertPlan,
     (the gradient is :func:`expert_glu_backward`): views that require a gradient
     are refused while grad mode is on.
     """
-    d = _glu(gate, up, plan)
+    fields = _glu(gate, up, plan)
     _unrecorded(gate, "gate", "expert_glu_backward")
     _unrecorded(up, "up", "expert_glu_backward")
     out = _tokens_out(out, stream, gate, gate.shape, gate.dtype, "out")
-    d.out, d.out_strides = out.data_ptr(), out.stride()
-    _expert_call("vf_expert_glu", d, stream, gate)
+    _desc_call("vf_expert_glu", _GLU_DESC.pack(*fields, *_view(out), *_NO_VIEW * 3), stream, gate)
     return out
 
 
@@ -1099,49 +1080,49 @@ def expert_glu_backward(grad: torch.Tensor, gate: torch.Tensor, up: torch.Tensor
     result: (grad_gate, grad_up), by default the halves of one [rows,2F] buffer,
     the rows' gradient of the product in front.  Gap rows are written as zeros, rows
     behind the last expert are left as they were."""
-    d = _glu(gate, up, plan)
+    fields = _glu(gate, up, plan)
     _same_view(grad, gate, "grad")
-    n, F = gate.shape
+    shape, dtype = gate.shape, gate.dtype
     if grad_gate is None and grad_up is None:
-        both = _new(stream, gate, (n, 2 * F), gate.dtype)
+        n, F = shape
+        both = _new(stream, gate, (n, 2 * F), dtype)
         grad_gate, grad_up = both[:, :F], both[:, F:]
-    grad_gate = _tokens_out(grad_gate, stream, gate, gate.shape, gate.dtype, "grad_gate")
-    grad_up = _tokens_out(grad_up, stream, gate, gate.shape, gate.dtype, "grad_up")
-    d.grad, d.grad_gate, d.grad_up = grad.data_ptr(), grad_gate.data_ptr(), grad_up.data_ptr()
-    d.grad_strides, d.grad_gate_strides = grad.stride(), grad_gate.stride()
-    d.grad_up_strides = grad_up.stride()
-    _expert_call("vf_expert_glu_backward", d, stream, gate)
+    grad_gate = _tokens_out(grad_gate, stream, gate, shape, dtype, "grad_gate")
+    grad_up = _tokens_out(grad_up, stream, gate, shape, dtype, "grad_up")
+    _desc_call("vf_expert_glu_backward", _GLU_DESC.pack(
+        *fields, *_NO_VIEW, *_view(grad), *_view(grad_gate), *_view(grad_up)), stream, gate)
     return grad_gate, grad_up
 
 
 # ---- root-mean-square norm -------------------------------------------------------
 
-def _norm_desc(x, weight, eps):
+def _norm(x, weight):
+    """(vf_type, the weight's, T, M) of the arguments that all calls take."""
     typ = _rows_type(x, "x")
     T, M = _matrix(x, "x")
     if not (isinstance(weight, torch.Tensor) and weight.is_cuda):
         _gpu_addressable(weight, "weight")
-    if weight.dtype != x.dtype and weight.dtype != torch.float32:
+    w = weight.dtype
+    if w != x.dtype and w != torch.float32:
         raise ValueError("weight must have the type of x or float32")
     if weight.shape != (M,) or not weight.is_contiguous():
         raise ValueError("weight must be contiguous with %d elements" % M)
-    d = _NormDesc(typ, _TYPES[weight.dtype], 0, eps, T, M)
-    d.x, d.x_strides, d.weight = x.data_ptr(), x.stride(), weight.data_ptr()
-    return d
+    return typ, _TYPES[w], T, M
 
 
-def _set_residual(d, x, residual, total, stream):
-    """The total's tensor, None without a residual."""
+def _norm_inputs(x, weight, residual, total, stream):
+    """The total's tensor (None without a residual), and the descriptor's fields of
+    both."""
+    _unrecorded(x, "x", "rms_norm_backward")
+    _unrecorded(weight, "weight", "rms_norm_backward")
     if residual is None:
         if total is not None:
             raise ValueError("total is written only with a residual")
-        return None
+        return None, _NO_VIEW + _NO_VIEW
     _same_view(residual, x, "residual")
     _unrecorded(residual, "residual", "rms_norm_backward")
     total = _tokens_out(total, stream, x, x.shape, x.dtype, "total")
-    d.residual, d.residual_strides = residual.data_ptr(), residual.stride()
-    d.total, d.total_strides = total.data_ptr(), total.stride()
-    return total
+    return total, _view(residual) + _view(total)
 
 
 def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
@@ -1157,13 +1138,12 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
     gradients are :func:`rms_norm_backward`): tensors that require a gradient are
     refused while grad mode is on.
     """
-    d = _norm_desc(x, weight, eps)
-    _unrecorded(x, "x", "rms_norm_backward")
-    _unrecorded(weight, "weight", "rms_norm_backward")
-    total = _set_residual(d, x, residual, total, stream)
+    typ, wtyp, T, M = _norm(x, weight)
+    total, sums = _norm_inputs(x, weight, residual, total, stream)
     out = _tokens_out(out, stream, x, x.shape, x.dtype, "out")
-    d.out, d.out_strides = out.data_ptr(), out.stride()
-    _expert_call("vf_rms_norm", d, stream, x)
+    _desc_call("vf_rms_norm", _NORM_DESC.pack(
+        typ, wtyp, 0, eps, T, M, 0, *_view(x), weight.data_ptr(), *sums, *_view(out), 0, 0,
+        0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0), stream, x)
     return out if total is None else (out, total)
 
 
@@ -1175,15 +1155,14 @@ def rms_norm_q(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, fmt="e4
     [T, ceil(M/group)]), with a residual (codes, scales, total).  Each ``group``
     consecutive columns of the float32 result share a scale, in the format of the
     lossy transport: what :func:`expert_restore_q` packs to expert-major rows."""
-    T, M = _bf16_matrix(x, "x")
+    _bf16_matrix(x, "x")
     f = _fmt(fmt)
-    d = _norm_desc(x, weight, eps)
-    _unrecorded(x, "x", "rms_norm_backward")
-    _unrecorded(weight, "weight", "rms_norm_backward")
-    total = _set_residual(d, x, residual, total, stream)
+    typ, wtyp, T, M = _norm(x, weight)
+    total, sums = _norm_inputs(x, weight, residual, total, stream)
     codes, scales = _kept(codes, scales, stream, x, T, M, f, group)
-    d.format, d.group, d.codes, d.scales = f, group, codes.data_ptr(), scales.data_ptr()
-    _expert_call("vf_rms_norm", d, stream, x)
+    _desc_call("vf_rms_norm", _NORM_DESC.pack(
+        typ, wtyp, f, eps, T, M, group, *_view(x), weight.data_ptr(), *sums, 0, 0, 0,
+        codes.data_ptr(), scales.data_ptr(), 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0), stream, x)
     return (codes, scales) if total is None else (codes, scales, total)
 
 
@@ -1199,20 +1178,20 @@ def rms_norm_backward(grad: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
     paths (the residual stream's) and is added.  With a residual ``grad_x`` is the
     gradient of both summands.
     """
-    d = _norm_desc(x, weight, eps)
+    typ, wtyp, T, M = _norm(x, weight)
     _same_view(grad, x, "grad")
-    T, M = x.shape
+    more = _NO_VIEW
     if grad_total is not None:
         _same_view(grad_total, x, "grad_total")
-        d.grad_total, d.grad_total_strides = grad_total.data_ptr(), grad_total.stride()
+        more = _view(grad_total)
     grad_x = _tokens_out(grad_x, stream, x, x.shape, x.dtype, "grad_x")
     grad_weight = _rows_out(grad_weight, stream, x, (M,), torch.float32, "grad_weight")
     size = lib().vf_rms_norm_workspace(T, M)
     if size < 0:
         raise VFError("vf_rms_norm_workspace", size)
     work = _workspace(stream, x, size // 4)
-    d.grad, d.grad_strides = grad.data_ptr(), grad.stride()
-    d.grad_x, d.grad_x_strides = grad_x.data_ptr(), grad_x.stride()
-    d.grad_weight, d.workspace = grad_weight.data_ptr(), work.data_ptr()
-    _expert_call("vf_rms_norm_backward", d, stream, x)
+    _desc_call("vf_rms_norm_backward", _NORM_DESC.pack(
+        typ, wtyp, 0, eps, T, M, 0, *_view(x), weight.data_ptr(), 0, 0, 0, 0, 0, 0, 0, 0, 0,
+        0, 0, *_view(grad), *more, *_view(grad_x), grad_weight.data_ptr(), work.data_ptr()),
+        stream, x)
     return grad_x, grad_weight

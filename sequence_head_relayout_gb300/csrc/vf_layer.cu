@@ -122,7 +122,7 @@ int glu(const vf_glu_desc *d, bool backward, cudaStream_t stream) {
     const int64_t by = 256 / bx;
     a.col_blocks = int32_t(ceil_div(a.units, bx));
     const int64_t row_blocks =
-        std::min(ceil_div(d->rows, 2 * by), std::max<int64_t>(1, kSMs * 16 / a.col_blocks));
+        std::min(ceil_div(d->rows, 2 * by), std::max<int64_t>(1, kSMs * 32 / a.col_blocks));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(row_blocks * a.col_blocks), 1, 1);
     cfg.blockDim = dim3(unsigned(bx), unsigned(by), 1);

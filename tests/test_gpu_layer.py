@@ -5,7 +5,9 @@ Bounds, with u = 2^-24 (half a unit of float32) and the header's arithmetic:
 
 * s = 1 / (1 + exp(-g)): the exponential is off by at most 2 + 1.173 |g| units of
   2^-23 (CUDA's bound of its fast form; 2 of the full one, which float32 takes),
-  the sum and the reciprocal by u each; below 2^-126 it may be 0;
+  which moves 1 + exp(-g) by no more of itself; the sum rounds by u, half a unit,
+  and the division by u (float32) or 2 units (CUDA's bound of the fast one), 2.5 units
+  together; below 2^-126 it may be 0;
 * a sum of M squares is off by at most M u of itself, its root and reciprocal by
   half of that and 4 u, each product by u;
 * every result is rounded once to its type: half a unit.
@@ -46,7 +48,7 @@ def view_like(x, layout, pad=True):
 
 def sigmoid_units(g, dtype):
     """Units of 2^-23 that s may be off by."""
-    return (2 if dtype == F32 else 2 + 1.173 * g.double().abs()) + 1
+    return 2 + 1 if dtype == F32 else 2 + 1.173 * g.double().abs() + 2.5
 
 
 def limited(y, dtype):
