@@ -54,6 +54,7 @@ struct ProductArgs {
     int32_t E, rows;
     int32_t feat, cols, red;      // features; weights: columns; rows: length of the sums
     int32_t feat_tiles, col_tiles;
+    int32_t part_rows;            // weights: most rows of one accumulation
     int32_t step_experts, step_tiles;    // weights: the grid's tiles, in experts and the rest
     int32_t tile_n;               // most rows (columns) of a tile
     int32_t box;                  // rows form: a copy of B has one to kBoxes times as many rows
@@ -292,6 +293,18 @@ __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&v)[32]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
+// 16 columns likewise.
+__device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+          "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]),
+          "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(addr) : "memory");
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
 // From one step of 16 k to the next, in units of 16 bytes.
 template <bool MN> constexpr uint32_t kStep16 = MN ? 16 * 128 / 16 : 2;
 
@@ -307,6 +320,7 @@ struct Tile {
     int n;             // rows or columns of the product, a multiple of 16 CTAS
     int kblocks;
     int gap;           // rows to be written as zeros behind the tile
+    bool more;         // weights: a later part of the sum, added to what is stored
 };
 
 // The CTA's (pair's) tiles, by all lanes of a warp together.  Rows form: the
@@ -328,6 +342,8 @@ struct Tiles {
     // weights form: the tile as a number within its expert
     int e, in, each;
     int next_row0, next_valid;    // loaded a tile ahead
+    int row0, rest;               // what is left of the expert's rows (sums in parts)
+    bool inside = false;
 
     __device__ __forceinline__ explicit Tiles(const ProductArgs &args)
         : a(args), lane(int(threadIdx.x & 31)), t(blockIdx.x / CTAS), step(gridDim.x / CTAS) {
@@ -362,24 +378,34 @@ struct Tiles {
     }
 
     __device__ __forceinline__ bool next_weights(Tile &o) {
-        if (e >= a.E) return false;
-        o.e = e;
-        o.f0 = in % a.feat_tiles * (kTileM * CTAS);
-        o.c0 = in / a.feat_tiles * a.tile_n;
-        // (each CTA's share of B starts at a whole slab)
-        const int multiple = a.b_slabs ? 64 * CTAS : kStep;
-        o.n = (min(a.tile_n, a.cols - o.c0) + multiple - 1) / multiple * multiple;
-        o.row0 = next_row0;
-        o.valid = next_valid;
-        o.kblocks = parts(o.valid, kBlockK);
-        o.gap = 0;
-        e += a.step_experts;
-        in += a.step_tiles;
-        if (in >= each) {
-            in -= each;
-            ++e;
+        if (inside) {                                      // the same tile's next part
+            o.more = true;
+        } else {
+            if (e >= a.E) return false;
+            o.e = e;
+            o.f0 = in % a.feat_tiles * (kTileM * CTAS);
+            o.c0 = in / a.feat_tiles * a.tile_n;
+            // (each CTA's share of B starts at a whole slab)
+            const int multiple = a.b_slabs ? 64 * CTAS : kStep;
+            o.n = (min(a.tile_n, a.cols - o.c0) + multiple - 1) / multiple * multiple;
+            o.gap = 0;
+            o.more = false;
+            row0 = next_row0;
+            rest = next_valid;
+            e += a.step_experts;
+            in += a.step_tiles;
+            if (in >= each) {
+                in -= each;
+                ++e;
+            }
+            segment(min(e, a.E - 1), next_row0, next_valid);
         }
-        segment(min(e, a.E - 1), next_row0, next_valid);
+        o.row0 = row0;
+        o.valid = min(rest, a.part_rows);
+        o.kblocks = parts(o.valid, kBlockK);
+        row0 += o.valid;
+        rest -= o.valid;
+        inside = rest > 0;
         return true;
     }
 
@@ -544,9 +570,10 @@ __device__ __forceinline__ void zero_rows(const ProductArgs &a, int64_t row, int
             *reinterpret_cast<uint4 *>(out + (row + j) * a.feat + c) = make_uint4(0, 0, 0, 0);
 }
 
-// Weights form: v[c] is column c0 + c of feature f + lane of expert e.
+// Weights form: v[c] is column c0 + c of feature f + lane of expert e.  `more`: it is
+// added to what this thread has stored there before.
 __device__ __forceinline__ void store_weights(const ProductArgs &a, const uint32_t (&v)[32],
-                                              int e, int f, int c0, int lane,
+                                              int e, int f, int c0, int lane, bool more,
                                               uint8_t *staging) {
     const int64_t first = (int64_t(e) * a.feat + f) * a.cols + c0;
     const int rows = min(32, a.feat - f), cols = min(32, a.cols - c0);
@@ -559,18 +586,31 @@ __device__ __forceinline__ void store_weights(const ProductArgs &a, const uint32
                 make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
         __syncwarp();
         if (a.vec) {
+            const int c = lane % 8 * 4;
+            float4 old[8];
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
-                const int r = q * 4 + lane / 8, c = lane % 8 * 4;
+                const int r = q * 4 + lane / 8;
+                old[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (more && r < rows && c < cols)
+                    old[q] = __ldcg(reinterpret_cast<const float4 *>(out + int64_t(r) * a.cols + c));
+            }
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const int r = q * 4 + lane / 8;
+                float4 x = *reinterpret_cast<const float4 *>(staging + r * 144 + c * 4);
+                if (more) x = make_float4(old[q].x + x.x, old[q].y + x.y, old[q].z + x.z,
+                                          old[q].w + x.w);
                 if (r < rows && c < cols)
-                    *reinterpret_cast<uint4 *>(out + int64_t(r) * a.cols + c) =
-                        *reinterpret_cast<const uint4 *>(staging + r * 144 + c * 4);
+                    *reinterpret_cast<float4 *>(out + int64_t(r) * a.cols + c) = x;
             }
         } else if (lane < cols) {
 #pragma unroll 8
-            for (int r = 0; r < rows; ++r)
-                out[int64_t(r) * a.cols + lane] =
-                    *reinterpret_cast<const float *>(staging + r * 144 + lane * 4);
+            for (int r = 0; r < rows; ++r) {
+                const float x = *reinterpret_cast<const float *>(staging + r * 144 + lane * 4);
+                float *p = out + int64_t(r) * a.cols + lane;
+                *p = more ? __ldcg(p) + x : x;
+            }
         }
     } else {
         uint16_t *out = static_cast<uint16_t *>(a.out) + first;
@@ -619,7 +659,8 @@ __host__ __device__ constexpr int64_t shared_bytes(int stages, int stage_bytes) 
 // WEIGHTS  the weights' gradient, else the rows' product
 // A_MN     the first operand is stored with i contiguous
 // FILL     operands come by plain loads, k contiguous in shared memory
-template <int CTAS, bool WEIGHTS, bool A_MN, bool FILL>
+// PARTS    sums are taken in parts of a.part_rows rows, which are added in registers
+template <int CTAS, bool WEIGHTS, bool A_MN, bool FILL, bool PARTS = false>
 __global__ void __launch_bounds__(FILL ? kFillThreads : kThreads, 1)
 expert_product(const __grid_constant__ ProductArgs a) {
     static_assert(!FILL || (CTAS == 1 && !A_MN), "fill producers: single CTAs, k contiguous");
@@ -756,6 +797,58 @@ expert_product(const __grid_constant__ ProductArgs a) {
             if (ok && one) mma_commit<CTAS>(smem_addr(&ctl.acc_full[acc]));
             ++it;
         }
+    } else if (PARTS && warp >= 4 && warp < 4 + kEpilogueWarps) {
+        Tiles<CTAS, WEIGHTS> tiles(a);
+        const int quarter = warp % 4, turn = (warp - 4) / 4;
+        uint8_t *const mine = staging + (warp - 4) * kStagingBytes;
+        uint32_t it = 0;
+        bool ok = true;
+        float sum[4][32];                            // half of the columns, by 32
+        while (tiles.next(o)) {
+            const uint32_t acc = it & 1, acc_phase = it >> 1 & 1;
+            const int n = min(o.n, a.cols - o.c0);
+            if (!o.more) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) sum[i][j] = 0.0f;
+            }
+            if (o.kblocks > 0) {
+                ok = ok && warp_wait(smem_addr(&ctl.acc_full[acc]), acc_phase, failed);
+                fence_after();
+                ++it;
+                const uint32_t d =
+                    tmem + acc * uint32_t(a.acc_stride) + (uint32_t(quarter * 32) << 16);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int c = 32 * turn + 64 * (i / 2) + 16 * (i % 2);
+                    uint32_t v[16];
+                    if (!ok || c >= n) continue;
+                    tmem_load(d + uint32_t(c), v);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        sum[i / 2][16 * (i % 2) + j] += __uint_as_float(v[j]);
+                }
+                fence_before();
+                __syncwarp();
+                if (ok && lane == 0) {
+                    if constexpr (CTAS == 1) barrier_arrive(smem_addr(&ctl.acc_empty[acc]));
+                    else barrier_arrive_first(smem_addr(&ctl.acc_empty[acc]));
+                }
+            }
+            const int f = o.f0 + int(rank) * kTileM + quarter * 32;
+            if (tiles.inside || f >= a.feat) continue;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int c = 32 * turn + 64 * i;
+                if (c >= n) continue;
+                uint32_t v[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    v[j] = ok ? __float_as_uint(sum[i][j]) : 0x7FC00000u;
+                store_weights(a, v, o.e, f, o.c0 + c, lane, false, mine);
+            }
+        }
     } else if (warp >= 4 && warp < 4 + kEpilogueWarps) {
         Tiles<CTAS, WEIGHTS> tiles(a);
         const int quarter = warp % 4, turn = (warp - 4) / 4;
@@ -786,7 +879,7 @@ expert_product(const __grid_constant__ ProductArgs a) {
                 }
                 if (f >= a.feat) continue;           // all lanes alike
                 if constexpr (WEIGHTS)
-                    store_weights(a, v, o.e, f, o.c0 + c, lane, mine);
+                    store_weights(a, v, o.e, f, o.c0 + c, lane, o.more, mine);
                 else
                     store_rows(a, v, int64_t(o.row0) + c, n - c, f, lane, mine);
             }

@@ -270,6 +270,11 @@ int weight_grad(const vf_product_desc *d, cudaStream_t stream) {
     a.cols = int32_t(d->M);
     a.out = d->grad_weights;
     a.out32 = d->out_type == VF_TYPE_F32;
+    // The tensor cores cut off what lies below an accumulator's last bit, always towards
+    // the same side, so that a sum's error grows with its length: 1.2e-6 of the result
+    // at 1,024 rows.  Sums in float32 are therefore taken in parts, which are added with
+    // rounding.  (The 16-bit types round a thousand times as coarsely.)
+    a.part_rows = a.out32 ? 256 : INT32_MAX;
     a.vec = d->M % (16 / size) == 0 && aligned16(d->grad_weights);
     a.a = static_cast<const uint16_t *>(d->grad);
     a.b = static_cast<const uint16_t *>(d->packed);
@@ -289,8 +294,9 @@ int weight_grad(const vf_product_desc *d, cudaStream_t stream) {
     if ((rc = make_row_map(&a.a_map, a.bf16, d->grad, d->N, d->rows)) != VF_OK ||
         (rc = make_row_map(&a.b_maps[0], a.bf16, d->packed, d->M, d->rows)) != VF_OK)
         return rc;
-    return launch_product(vfp::expert_product<2, true, true, false>, a, f.ctas, tiles,
-                          stream);
+    const Kernel kernel = a.out32 ? vfp::expert_product<2, true, true, false, true>
+                                  : vfp::expert_product<2, true, true, false>;
+    return launch_product(kernel, a, f.ctas, tiles, stream);
 }
 
 }  // namespace
