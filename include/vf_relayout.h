@@ -502,11 +502,15 @@ int vf_expert_merge_backward(const vf_expert_desc *desc, vf_stream_t stream);
  *
  * All buffers are device memory of the current device (page-locked host memory is
  * refused).  Ownership, streams and errors as above; a written range that overlaps
- * another range of the call is VF_ERR_ALIAS.  No workspace.  Limits (VF_ERR_ARG):
- * as for the expert relayouts, N and M at most 2^20.
- * Operands go through tensor maps when packed (and grad) start at a multiple of 16
- * bytes with M (and N) multiples of 8, and the weights have unit stride along n or m
- * with the other strides multiples of 8; others are loaded element by element.
+ * another range of the call is VF_ERR_ALIAS.  Limits (VF_ERR_ARG): as for the expert
+ * relayouts, N and M at most 2^20.
+ * Operands are read in place when packed (and grad) start at a multiple of 16 bytes
+ * with M (and N) multiples of 8, and the weights do so with unit stride along n or m and
+ * the other strides positive multiples of 8; no workspace is needed then.  Any other
+ * operand is first copied into the workspace in that form (of the weights what experts
+ * with rows have, of the rows those below offsets[E]): vf_expert_*_workspace() bytes,
+ * 16-byte aligned device memory, one for each of the calls that may run at the same time.
+ * A call that needs it and is given NULL returns VF_ERR_CAPACITY.
  * A kernel whose internal wait lasts for seconds, which only a failing device can
  * bring about, writes NaN to what it has not stored yet.
  */
@@ -525,7 +529,13 @@ typedef struct vf_product_desc {
     const void *grad;           /* [rows][N] */
     void *out;                  /* [rows][N] */
     void *grad_weights;         /* [E][N][M] */
+    void *workspace;            /* or NULL, where none is needed */
 } vf_product_desc;
+
+/* Bytes of workspace of the two calls (0: none), by the sizes, strides and addresses of
+ * their operands; or a negative vf_status.  Pure host functions. */
+int64_t vf_expert_product_workspace(const vf_product_desc *desc);
+int64_t vf_expert_weight_grad_workspace(const vf_product_desc *desc);
 
 int vf_expert_product(const vf_product_desc *desc, vf_stream_t stream);
 int vf_expert_weight_grad(const vf_product_desc *desc, vf_stream_t stream);

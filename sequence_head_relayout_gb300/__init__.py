@@ -92,7 +92,8 @@ class _ExpertDesc(ctypes.Structure):
 
 # The descriptors of the calls below the expert relayouts are packed by one call each,
 # which takes 1 us where setting the fields of a ctypes structure takes 3 to 4.
-_PRODUCT_DESC = struct.Struct("@ii16q")      # vf_product_desc of the C ABI
+_PRODUCT_DESC = struct.Struct("@ii16q")      # vf_product_desc of the C ABI, but for the
+_POINTER = struct.Struct("@q")               # workspace at its end
 _GLU_DESC = struct.Struct("@iq22q")          # vf_glu_desc
 _NORM_DESC = struct.Struct("@iiif29q")       # vf_norm_desc
 
@@ -168,6 +169,10 @@ def lib():
             f = getattr(l, name)
             f.argtypes = [ctypes.c_char_p, _P]
             f.restype = ctypes.c_int
+        for name in ("vf_expert_product_workspace", "vf_expert_weight_grad_workspace"):
+            f = getattr(l, name)
+            f.argtypes = [ctypes.c_char_p]
+            f.restype = _I64
         l.vf_rms_norm_workspace.argtypes = [_I64, _I64]
         l.vf_rms_norm_workspace.restype = _I64
         l.vf_status_string.argtypes = [ctypes.c_int]
@@ -943,6 +948,21 @@ def _desc_call(fn, desc, stream, like):
         raise VFError(fn, rc)
 
 
+def _product_call(fn, desc, stream, like):
+    """A product; with a workspace where the library asks for one."""
+    f = getattr(_lib or lib(), fn)
+    handle = _stream(stream, like.device)
+    rc = f(desc + b"\0" * 8, handle)
+    if rc == -5:                                           # operands that need a copy
+        size = getattr(_lib, fn + "_workspace")(desc + b"\0" * 8)
+        if size < 0:
+            raise VFError(fn + "_workspace", size)
+        work = _workspace(stream, like, -(-size // 4))
+        rc = f(desc + _POINTER.pack(work.data_ptr()), handle)
+    if rc != 0:
+        raise VFError(fn, rc)
+
+
 def _product_rows(t, what):
     """vf_type of contiguous packed rows that a product takes."""
     if not isinstance(t, torch.Tensor):
@@ -976,6 +996,10 @@ def expert_product(rows: torch.Tensor, weights: torch.Tensor, plan: ExpertPlan,
     gradient of ``rows`` is ``expert_product(grad, weights.transpose(1, 2), plan)``,
     that of ``weights`` :func:`expert_weight_grad`.  No graph is recorded: rows
     or weights that require a gradient are refused while grad mode is on.
+
+    M that is no multiple of 8, or operands that do not start at multiples of 16
+    bytes, cost a copy of what is read of them (for weights without unit stride along
+    N or M too).
     """
     typ = _product_rows(rows, "rows")
     _unrecorded(rows, "rows", "expert_product with the transposed weights")
@@ -989,7 +1013,7 @@ def expert_product(rows: torch.Tensor, weights: torch.Tensor, plan: ExpertPlan,
     _unrecorded(weights, "weights", "expert_weight_grad")
     N = w[1]
     out = _rows_out(out, stream, rows, (n, N), rows.dtype, "out")
-    _desc_call("vf_expert_product", _PRODUCT_DESC.pack(
+    _product_call("vf_expert_product", _PRODUCT_DESC.pack(
         typ, typ, E, N, M, n, T * K, plan[4], plan[2].data_ptr(), plan[3].data_ptr(),
         rows.data_ptr(), weights.data_ptr(), *weights.stride(), 0, out.data_ptr(), 0),
         stream, rows)
@@ -1020,7 +1044,7 @@ def expert_weight_grad(grad: torch.Tensor, rows: torch.Tensor, plan: ExpertPlan,
         raise ValueError("dtype must be that of rows or torch.float32")
     T, K, _, E = _packed_plan(plan, n)
     out = _rows_out(out, stream, rows, (E, N, M), dtype, "out")
-    _desc_call("vf_expert_weight_grad", _PRODUCT_DESC.pack(
+    _product_call("vf_expert_weight_grad", _PRODUCT_DESC.pack(
         typ, _TYPES[dtype], E, N, M, n, T * K, plan[4], plan[2].data_ptr(), plan[3].data_ptr(),
         rows.data_ptr(), 0, 0, 0, 0, grad.data_ptr(), 0, out.data_ptr()), stream, grad)
     return out

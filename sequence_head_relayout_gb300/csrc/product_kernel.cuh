@@ -37,19 +37,15 @@ constexpr int kMaxStages = 12;
 constexpr int kBoxes = 4;                      // heights of the copies of B, multiples of one
 constexpr int kEpilogueWarps = 8;               // two for each quarter of the tile's features
 constexpr int kStagingBytes = 4608;            // per epilogue warp: 32 rows of 144 bytes
-constexpr int kFillWarps = 8;                  // producers of operands that TMA cannot take
 constexpr int kThreads = 32 * (4 + kEpilogueWarps);
-constexpr int kFillThreads = kThreads + 32 * kFillWarps;
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr uint64_t kDrainNs = 100000000ull;
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 
 struct ProductArgs {
-    // not used by the fill producers; rows form: b_maps[i] has boxes of (i + 1) box rows
+    // rows form: b_maps[i] has boxes of (i + 1) box rows
     CUtensorMap a_map, b_maps[kBoxes];
     const int32_t *counts, *offsets;
-    const uint16_t *a, *b;        // the fill producers' operands and element strides
-    int64_t a_expert, a_i, a_k, b_i, b_k;
     void *out;                    // rows: [rows][feat]; weights: [E][feat][cols]
     int32_t E, rows;
     int32_t feat, cols, red;      // features; weights: columns; rows: length of the sums
@@ -467,51 +463,6 @@ struct Tiles {
     }
 };
 
-// ---- producers -----------------------------------------------------------------
-
-// Fills 128 rows of 64 k of an operand, k contiguous, from any element strides;
-// zeros past i_end and k_end.  By the kFillWarps warps; `warp` is the number among
-// them.  The lanes lie along the dimension with the smaller stride.
-__device__ __forceinline__ void fill(uint8_t *dst, const uint16_t *src, int64_t s_i, int64_t s_k,
-                                     int i_end, int k_end, int warp, int lane) {
-    if (s_k <= s_i) {
-        constexpr int kRows = kTileM / kFillWarps;
-        uint16_t lo[kRows], hi[kRows];
-        const int k = 2 * lane;
-#pragma unroll
-        for (int j = 0; j < kRows; ++j) {
-            const int i = j * kFillWarps + warp;
-            const uint16_t *p = src + i * s_i + k * s_k;
-            lo[j] = i < i_end && k < k_end ? p[0] : uint16_t(0);
-            hi[j] = i < i_end && k + 1 < k_end ? p[s_k] : uint16_t(0);
-        }
-#pragma unroll
-        for (int j = 0; j < kRows; ++j) {
-            const int i = j * kFillWarps + warp;
-            *reinterpret_cast<uint32_t *>(dst + i * 128 + (((k >> 3) ^ (i & 7)) << 4) +
-                                          (k & 7) * 2) = uint32_t(lo[j]) | uint32_t(hi[j]) << 16;
-        }
-    } else {
-        static_assert(kFillWarps == kBlockK / 8, "a warp for every 8 k");
-#pragma unroll
-        for (int j = 0; j < kTileM / 32; ++j) {
-            const int i = j * 32 + lane;
-            uint16_t v[8];
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                const int k = warp * 8 + q;
-                v[q] = i < i_end && k < k_end ? src[i * s_i + k * s_k] : uint16_t(0);
-            }
-            uint4 w;
-            w.x = uint32_t(v[0]) | uint32_t(v[1]) << 16;
-            w.y = uint32_t(v[2]) | uint32_t(v[3]) << 16;
-            w.z = uint32_t(v[4]) | uint32_t(v[5]) << 16;
-            w.w = uint32_t(v[6]) | uint32_t(v[7]) << 16;
-            *reinterpret_cast<uint4 *>(dst + i * 128 + ((warp ^ (i & 7)) << 4)) = w;
-        }
-    }
-}
-
 // ---- epilogue ------------------------------------------------------------------
 
 __device__ __forceinline__ uint32_t round2(float lo, float hi, bool bf16) {
@@ -658,13 +609,11 @@ __host__ __device__ constexpr int64_t shared_bytes(int stages, int stage_bytes) 
 // CTAS     CTAs that share a tile (2: a pair, 256 features, each CTA holds half of B)
 // WEIGHTS  the weights' gradient, else the rows' product
 // A_MN     the first operand is stored with i contiguous
-// FILL     operands come by plain loads, k contiguous in shared memory
 // PARTS    sums are taken in parts of a.part_rows rows, which are added in registers
-template <int CTAS, bool WEIGHTS, bool A_MN, bool FILL, bool PARTS = false>
-__global__ void __launch_bounds__(FILL ? kFillThreads : kThreads, 1)
+template <int CTAS, bool WEIGHTS, bool A_MN, bool PARTS = false>
+__global__ void __launch_bounds__(kThreads, 1)
 expert_product(const __grid_constant__ ProductArgs a) {
-    static_assert(!FILL || (CTAS == 1 && !A_MN), "fill producers: single CTAs, k contiguous");
-    constexpr bool B_MN = WEIGHTS && !FILL;
+    constexpr bool B_MN = WEIGHTS;
     extern __shared__ uint8_t raw[];
     uint8_t *const smem = raw + (1024 - (smem_addr(raw) & 1023)) % 1024;
     uint8_t *const staging = smem + a.stages * a.stage_bytes;
@@ -675,7 +624,7 @@ expert_product(const __grid_constant__ ProductArgs a) {
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < a.stages; ++s) {
-            barrier_init(smem_addr(&ctl.full[s]), FILL ? kFillWarps : 1);
+            barrier_init(smem_addr(&ctl.full[s]), 1);
             barrier_init(smem_addr(&ctl.empty[s]), 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -706,7 +655,7 @@ expert_product(const __grid_constant__ ProductArgs a) {
 
     const uint32_t ring = smem_addr(smem), full = smem_addr(&ctl.full[0]),
                    empty = smem_addr(&ctl.empty[0]);
-    if (!FILL && (warp == 0 || warp == 3)) {
+    if (warp == 0 || warp == 3) {
         // copies: one warp for this CTA's A, one for its share of B
         const uint32_t bars = first_barrier<CTAS>(full);
         const bool one = elected();
@@ -894,37 +843,6 @@ expert_product(const __grid_constant__ ProductArgs a) {
             if (!WEIGHTS && o.gap > 0 && f < a.feat && turn == 0)
                 zero_rows(a, int64_t(o.row0) + o.valid, o.gap, f, lane);
         }
-    } else if (FILL && warp >= 12) {
-        Tiles<CTAS, WEIGHTS> tiles(a);
-        const int w = warp - 12;
-        bool ok = true;
-        while (ok && tiles.next(o)) {
-            const uint16_t *pa, *pb;
-            int k_end;
-            if constexpr (WEIGHTS) {
-                pa = a.a + o.row0 * a.a_k + o.f0 * a.a_i;
-                pb = a.b + o.row0 * a.b_k + o.c0 * a.b_i;
-                k_end = o.valid;
-            } else {
-                pa = a.a + o.e * a.a_expert + o.f0 * a.a_i;
-                pb = a.b + o.row0 * a.b_i;
-                k_end = a.red;
-            }
-            const int b_end = WEIGHTS ? min(o.n, a.cols - o.c0) : o.valid;
-            for (int kb = 0; ok && kb < o.kblocks; ++kb) {
-                ok = barrier_wait(smem_addr(&ctl.empty[s]), phase ^ 1, failed);
-                ok = __all_sync(kAll, int(ok));
-                if (!ok) break;
-                uint8_t *da = smem + s * a.stage_bytes;
-                const int k = kb * kBlockK;
-                fill(da, pa + k * a.a_k, a.a_i, a.a_k, a.feat - o.f0, k_end - k, w, lane);
-                fill(da + kStageA, pb + k * a.b_k, a.b_i, a.b_k, b_end, k_end - k, w, lane);
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) barrier_arrive(smem_addr(&ctl.full[s]));
-                advance();
-            }
-        }
     }
 
     __syncthreads();
@@ -938,6 +856,86 @@ expert_product(const __grid_constant__ ProductArgs a) {
     if constexpr (CTAS > 1) cluster_sync();
     fence_after();
     if (warp == 2) tmem_free<CTAS>(tmem, uint32_t(a.tmem_cols));
+}
+
+// ---- operands at any address -----------------------------------------------------
+
+// Lines of `len` 16-bit elements, at any address and any element stride, to lines that
+// start at multiples of 16 bytes, as tensor maps need them: [outer][lines][pitch].
+// Only what the product reads: the outer items whose count is above 0, or the lines
+// below *limit.  Bound by HBM: each line is read and written once.
+struct PadArgs {
+    const uint16_t *src, *end;    // the operand, and behind its last element
+    int64_t s_outer, s_line, s_el;
+    uint16_t *dst;
+    int64_t outer, lines, len, pitch;
+    const int32_t *counts;        // [outer], or null
+    const int32_t *limit;         // null: all lines
+};
+
+// The 16 bytes at `at`, a multiple of 16; zeros outside the operand.
+__device__ __forceinline__ uint4 piece(const PadArgs &a, uint64_t at) {
+    const uint64_t lo = reinterpret_cast<uint64_t>(a.src), hi = reinterpret_cast<uint64_t>(a.end);
+    if (at >= lo && at + 16 <= hi) return *reinterpret_cast<const uint4 *>(at);
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const uint64_t q = at + 2 * j;
+        if (q >= lo && q < hi)
+            w[j / 2] |= uint32_t(*reinterpret_cast<const uint16_t *>(q)) << (j % 2 * 16);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__global__ void __launch_bounds__(256)
+pad_lines(const __grid_constant__ PadArgs a) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int lane = int(threadIdx.x & 31);
+    const int64_t warps = int64_t(gridDim.x) * (blockDim.x / 32);
+    const int64_t limit = a.limit ? min(int64_t(max(*a.limit, 0)), a.lines) : a.lines;
+    const int64_t chunks = (a.len + 7) / 8;
+    for (int64_t i = int64_t(blockIdx.x) * (blockDim.x / 32) + (threadIdx.x >> 5);
+         i < a.outer * a.lines; i += warps) {
+        const int64_t e = i / a.lines, l = i - e * a.lines;
+        if (l >= limit || (a.counts && a.counts[e] <= 0)) continue;
+        const uint16_t *const p = a.src + e * a.s_outer + l * a.s_line;
+        uint4 *const to = reinterpret_cast<uint4 *>(a.dst + i * a.pitch);
+        const int shift = int(reinterpret_cast<uint64_t>(p) & 15);
+        const uint64_t at = reinterpret_cast<uint64_t>(p) - shift;
+        for (int64_t c0 = 0; c0 < chunks; c0 += 64) {
+            uint4 v[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int64_t c = c0 + u * 32 + lane;
+                if (c >= chunks) continue;
+                if (a.s_el == 1) {
+                    const uint4 lo = piece(a, at + 16 * c);
+                    const uint4 hi = shift ? piece(a, at + 16 * c + 16) : lo;
+                    uint32_t x[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+                    for (int j = 0; j < 6; ++j) x[j] = shift & 8 ? x[j + 2] : x[j];
+#pragma unroll
+                    for (int j = 0; j < 5; ++j) x[j] = shift & 4 ? x[j + 1] : x[j];
+                    const int bits = shift & 2 ? 16 : 0;
+                    v[u] = make_uint4(__funnelshift_r(x[0], x[1], bits),
+                                      __funnelshift_r(x[1], x[2], bits),
+                                      __funnelshift_r(x[2], x[3], bits),
+                                      __funnelshift_r(x[3], x[4], bits));
+                } else {
+                    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (c * 8 + j < a.len)
+                            w[j / 2] |= uint32_t(p[(c * 8 + j) * a.s_el]) << (j % 2 * 16);
+                    v[u] = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+                if (c0 + u * 32 + lane < chunks) to[c0 + u * 32 + lane] = v[u];
+        }
+    }
 }
 
 }  // namespace vfp

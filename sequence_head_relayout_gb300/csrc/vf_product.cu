@@ -87,11 +87,11 @@ struct Form {
     int64_t ctas, tile_n, box;
 };
 
-void set_form(vfp::ProductArgs *a, const Form &f, bool fill) {
+void set_form(vfp::ProductArgs *a, const Form &f) {
     const int64_t b_rows = f.tile_n / f.ctas;
     a->tile_n = int32_t(f.tile_n);
     a->box = int32_t(f.box);
-    a->stage_bytes = int32_t(vfp::kStageA + (fill ? vfp::kTileM : b_rows) * 128);
+    a->stage_bytes = int32_t(vfp::kStageA + b_rows * 128);
     a->stages = 0;
     while (a->stages < vfp::kMaxStages &&
            vfp::shared_bytes(a->stages + 1, a->stage_bytes) <= kSharedMemory)
@@ -106,7 +106,7 @@ void set_form(vfp::ProductArgs *a, const Form &f, bool fill) {
 using Kernel = void (*)(vfp::ProductArgs);
 
 int launch_product(Kernel kernel, vfp::ProductArgs &a, int64_t ctas, int64_t tiles,
-                   cudaStream_t stream, int threads = vfp::kThreads) {
+                   cudaStream_t stream) {
     if (tiles == 0) return VF_OK;
     const int64_t groups = std::min(kSMs / ctas, tiles);
     if (a.col_tiles > 0) {
@@ -121,7 +121,7 @@ int launch_product(Kernel kernel, vfp::ProductArgs &a, int64_t ctas, int64_t til
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(groups * ctas), 1, 1);
-    cfg.blockDim = dim3(unsigned(threads), 1, 1);
+    cfg.blockDim = dim3(vfp::kThreads, 1, 1);
     cfg.dynamicSmemBytes = size_t(vfp::shared_bytes(a.stages, a.stage_bytes));
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
@@ -140,6 +140,16 @@ int launch_product(Kernel kernel, vfp::ProductArgs &a, int64_t ctas, int64_t til
     return VF_OK;
 }
 
+// Adds the workspace of `need` bytes (or a status) to the call's ranges.
+int add_workspace(Ranges *rs, const vf_product_desc *d, int64_t need) {
+    if (need < 0) return int(need);
+    if (need == 0) return VF_OK;
+    if (d->workspace == nullptr) return VF_ERR_CAPACITY;
+    if (!aligned16(d->workspace)) return VF_ERR_ARG;
+    rs->add(d->workspace, need, 1, true);
+    return rs->rc;
+}
+
 vfp::ProductArgs make_args(const vf_product_desc *d) {
     vfp::ProductArgs a;
     std::memset(&a, 0, sizeof(a));
@@ -153,20 +163,86 @@ vfp::ProductArgs make_args(const vf_product_desc *d) {
     return a;
 }
 
-// How tensor maps take the operands of a product: 0 not at all, 1 the weights with
-// unit stride along m, 2 along n.
-int weight_maps(const vf_product_desc *d) {
-    if (d->M == 0 || d->M % 8 || !aligned16(d->packed) || !aligned16(d->weights)) return 0;
-    int64_t e = d->weight_strides[0], n = d->weight_strides[1], m = d->weight_strides[2];
-    if (!map_stride(d->E, &e, 8)) return 0;
-    if ((m == 1 || d->M == 1) && map_stride(d->N, &n, 8)) return 1;
-    if ((n == 1 || d->N == 1) && map_stride(d->M, &m, 8)) return 2;
-    return 0;
+int64_t pad8(int64_t n) { return ceil_div(n, 8) * 8; }
+
+// An operand as a tensor map takes it, [outer][lines][len] with strides in elements, or
+// as the workspace gets a copy of it that one does.
+struct Operand {
+    const void *p;
+    int64_t outer, lines, len;
+    int64_t s_outer, s_line, s_el;
+    bool copied = false;
+
+    Operand(const void *p_, int64_t outer_, int64_t lines_, int64_t len_, int64_t s_outer_,
+            int64_t s_line_, int64_t s_el_)
+        : p(p_), outer(outer_), lines(lines_), len(len_), s_outer(s_outer_), s_line(s_line_),
+          s_el(s_el_) {
+        int64_t so = s_outer, sl = s_line;
+        copied = len > 0 && !((s_el == 1 || len == 1) && aligned16(p) &&
+                              map_stride(outer, &so, 8) && map_stride(lines, &sl, 8));
+        if (!copied) {
+            map_stride(lines, &s_line, len);
+            map_stride(outer, &s_outer, len);
+        }
+    }
+
+    // Bytes of the workspace; the extents are at most 2^31, 2^20 and 2^12.
+    int64_t bytes() const {
+        int64_t n;
+        if (!copied) return 0;
+        return mul_ok(outer * lines, pad8(len) * 2, &n) ? n : -1;
+    }
+
+    // Copies it to `at`; `span`: elements from p to behind the last.
+    int copy(void *at, int64_t span, const int32_t *counts, const int32_t *limit,
+             cudaStream_t stream) {
+        vfp::PadArgs a;
+        std::memset(&a, 0, sizeof(a));
+        a.src = static_cast<const uint16_t *>(p);
+        a.end = a.src + span;
+        a.s_outer = s_outer;
+        a.s_line = s_line;
+        a.s_el = len == 1 ? 1 : s_el;
+        a.dst = static_cast<uint16_t *>(at);
+        a.outer = outer;
+        a.lines = lines;
+        a.len = len;
+        a.pitch = pad8(len);
+        a.counts = counts;
+        a.limit = limit;
+        p = at;
+        s_line = a.pitch;
+        s_outer = lines * a.pitch;
+        s_el = 1;
+        return launch(vfp::pad_lines, std::min(ceil_div(outer * lines, 8), kSMs * 8), 256, 0,
+                      stream, a);
+    }
+};
+
+// The weights along m, or along n where their unit stride is.
+bool along_n(const vf_product_desc *d) {
+    return d->weight_strides[2] != 1 && d->M != 1 && (d->weight_strides[1] == 1 || d->N == 1);
+}
+
+Operand weights_of(const vf_product_desc *d) {
+    const int64_t *s = d->weight_strides;
+    return along_n(d) ? Operand(d->weights, d->E, d->M, d->N, s[0], s[2], s[1])
+                      : Operand(d->weights, d->E, d->N, d->M, s[0], s[1], s[2]);
+}
+
+Operand rows_of(const void *p, int64_t rows, int64_t len) {
+    return Operand(p, 1, rows, len, 0, len, 1);
+}
+
+// Bytes of workspace for two operands, or a status.
+int64_t workspace_of(const Operand &a, const Operand &b) {
+    const int64_t n = a.bytes(), m = b.bytes();
+    int64_t sum;
+    return n < 0 || m < 0 || !add_ok(n, m, &sum) ? VF_ERR_OVERFLOW : sum;
 }
 
 // Rows of a tile, by the rows that an expert has on average.
-Form rows_form(const vf_product_desc *d, bool maps) {
-    if (!maps) return {1, 128, 0};
+Form rows_form(const vf_product_desc *d) {
     const int64_t mean = ceil_div(d->slots, d->E);
     if (mean <= 8) return {1, 32, 16};
     if (mean <= 32) return {1, 64, 16};
@@ -177,75 +253,69 @@ Form rows_form(const vf_product_desc *d, bool maps) {
 int product(const vf_product_desc *d, cudaStream_t stream) {
     int rc = check_desc(d);
     if (rc != VF_OK) return rc;
-    int64_t n_packed, n_out, w_span;
+    int64_t n_packed, n_out, span;
     const int64_t ext[3] = {d->E, d->N, d->M};
     if (!mul_ok(d->rows, d->M, &n_packed) || !mul_ok(d->rows, d->N, &n_out))
         return VF_ERR_OVERFLOW;
-    if ((rc = max_offset(ext, d->weight_strides, 3, &w_span)) != VF_OK) return rc;
+    if ((rc = max_offset(ext, d->weight_strides, 3, &span)) != VF_OK) return rc;
+    if (!add_ok(span, 1, &span)) return VF_ERR_OVERFLOW;
     if (n_out == 0) return VF_OK;                          // nothing to write
     Ranges rs;
     rs.add(d->counts, d->E, 4, false);
     rs.add(d->offsets, d->E + 1, 4, false);
     rs.add(d->packed, n_packed, 2, false);
-    if (!add_ok(w_span, 1, &w_span)) return VF_ERR_OVERFLOW;
-    if (d->M > 0) rs.add(d->weights, w_span, 2, false);
+    if (d->M > 0) rs.add(d->weights, span, 2, false);
     rs.add(d->out, n_out, 2, true);
+    if (rs.rc != VF_OK) return rs.rc;
+    Operand w = weights_of(d), x = rows_of(d->packed, d->rows, d->M);
+    if ((rc = add_workspace(&rs, d, d->M > 0 ? workspace_of(w, x) : 0)) != VF_OK) return rc;
     if ((rc = rs.check(true)) != VF_OK) return rc;
 
     vfp::ProductArgs a = make_args(d);
     a.red = int32_t(d->M);
     a.out = d->out;
     a.vec = d->N % 8 == 0 && aligned16(d->out);
-    const int64_t most = std::min(d->E, d->rows);          // experts that have rows
-    a.a = static_cast<const uint16_t *>(d->weights);
-    a.b = static_cast<const uint16_t *>(d->packed);
-    a.a_expert = d->weight_strides[0];
-    a.a_i = d->weight_strides[1];
-    a.a_k = d->weight_strides[2];
-    a.b_i = d->M;
-    a.b_k = 1;
-    const int maps = weight_maps(d);
-    const Form f = rows_form(d, maps != 0);
-    set_form(&a, f, maps == 0);
-    const int64_t tiles = a.feat_tiles * (most + d->rows / f.tile_n);
-    if (maps == 0)
-        return launch_product(vfp::expert_product<1, false, false, true>, a, f.ctas, tiles,
-                              stream, vfp::kFillThreads);
-    const bool mn = maps == 2;
-    const int64_t dims[3] = {mn ? d->N : d->M, mn ? d->M : d->N, d->E};
-    int64_t str[3] = {1, d->weight_strides[mn ? 2 : 1], d->weight_strides[0]};
-    map_stride(dims[1], &str[1], dims[0]);
-    map_stride(dims[2], &str[2], dims[0]);
-    a.a_slabs = mn && d->N % 64 == 0;
-    if (a.a_slabs) {
-        const int64_t dims4[4] = {64, dims[1], d->N / 64, d->E}, str4[4] = {1, str[1], 64, str[2]};
-        rc = make_map(&a.a_map, a.bf16, 4, d->weights, dims4, str4, 64, 2);
-    } else {
-        rc = make_map(&a.a_map, a.bf16, 3, d->weights, dims, str, mn ? 64 : 128);
+    const Form f = rows_form(d);
+    set_form(&a, f);
+    const bool mn = along_n(d);
+    if (d->M > 0) {                                        // else sums of nothing: zeros
+        char *const space = static_cast<char *>(d->workspace);
+        if (w.copied && (rc = w.copy(space, span, d->counts, nullptr, stream)) != VF_OK) return rc;
+        if (x.copied && (rc = x.copy(space + w.bytes(), n_packed, nullptr, d->offsets + d->E,
+                                     stream)) != VF_OK)
+            return rc;
+        a.a_slabs = mn && d->N % 64 == 0;
+        if (a.a_slabs) {
+            const int64_t dims[4] = {64, w.lines, d->N / 64, d->E};
+            const int64_t str[4] = {1, w.s_line, 64, w.s_outer};
+            rc = make_map(&a.a_map, a.bf16, 4, w.p, dims, str, 64, 2);
+        } else {
+            const int64_t dims[3] = {w.len, w.lines, d->E}, str[3] = {1, w.s_line, w.s_outer};
+            rc = make_map(&a.a_map, a.bf16, 3, w.p, dims, str, mn ? 64 : 128);
+        }
+        const int64_t dims[2] = {d->M, d->rows}, str[2] = {1, x.s_line};
+        for (int i = 0; i < vfp::kBoxes && rc == VF_OK; ++i)
+            if (i * f.box < f.tile_n / f.ctas)
+                rc = make_map(&a.b_maps[i], a.bf16, 2, x.p, dims, str, (i + 1) * f.box);
+        if (rc != VF_OK) return rc;
     }
-    if (rc != VF_OK) return rc;
-    const int64_t b_dims[2] = {d->M, d->rows}, b_str[2] = {1, d->M};
-    for (int i = 0; i < vfp::kBoxes && rc == VF_OK; ++i)
-        if (i * f.box < f.tile_n / f.ctas)
-            rc = make_map(&a.b_maps[i], a.bf16, 2, d->packed, b_dims, b_str, (i + 1) * f.box);
-    if (rc != VF_OK) return rc;
     const Kernel kernel =
-        f.ctas == 2 ? (mn ? vfp::expert_product<2, false, true, false>
-                          : vfp::expert_product<2, false, false, false>)
-                    : (mn ? vfp::expert_product<1, false, true, false>
-                          : vfp::expert_product<1, false, false, false>);
-    return launch_product(kernel, a, f.ctas, tiles, stream);
+        f.ctas == 2
+            ? (mn ? vfp::expert_product<2, false, true> : vfp::expert_product<2, false, false>)
+            : (mn ? vfp::expert_product<1, false, true> : vfp::expert_product<1, false, false>);
+    const int64_t most = std::min(d->E, d->rows);          // experts that have rows
+    return launch_product(kernel, a, f.ctas, a.feat_tiles * (most + d->rows / f.tile_n), stream);
 }
 
 // The map of packed rows for the weights' gradient: the second dimension steps over
 // the rows as the third does (see the kernel); columns by 64 where they are whole.
-int make_row_map(CUtensorMap *map, bool bf16, const void *p, int64_t cols, int64_t rows) {
-    if (cols % 64) {
-        const int64_t dims[3] = {cols, 64, rows}, str[3] = {1, cols, cols};
-        return make_map(map, bf16, 3, p, dims, str, 64);
+int make_row_map(CUtensorMap *map, bool bf16, const Operand &x) {
+    if (x.len % 64) {
+        const int64_t dims[3] = {x.len, 64, x.lines}, str[3] = {1, x.s_line, x.s_line};
+        return make_map(map, bf16, 3, x.p, dims, str, 64);
     }
-    const int64_t dims[4] = {64, 64, rows, cols / 64}, str[4] = {1, cols, cols, 64};
-    return make_map(map, bf16, 4, p, dims, str, 64, 3);
+    const int64_t dims[4] = {64, 64, x.lines, x.len / 64}, str[4] = {1, x.s_line, x.s_line, 64};
+    return make_map(map, bf16, 4, x.p, dims, str, 64, 3);
 }
 
 int weight_grad(const vf_product_desc *d, cudaStream_t stream) {
@@ -264,6 +334,9 @@ int weight_grad(const vf_product_desc *d, cudaStream_t stream) {
     rs.add(d->packed, n_packed, 2, false);
     rs.add(d->grad, n_grad, 2, false);
     rs.add(d->grad_weights, n_out, size, true);
+    if (rs.rc != VF_OK) return rs.rc;
+    Operand g = rows_of(d->grad, d->rows, d->N), x = rows_of(d->packed, d->rows, d->M);
+    if ((rc = add_workspace(&rs, d, d->rows > 0 ? workspace_of(g, x) : 0)) != VF_OK) return rc;
     if ((rc = rs.check(true)) != VF_OK) return rc;
 
     vfp::ProductArgs a = make_args(d);
@@ -273,35 +346,47 @@ int weight_grad(const vf_product_desc *d, cudaStream_t stream) {
     // The tensor cores cut off what lies below an accumulator's last bit, always towards
     // the same side, so that a sum's error grows with its length: 1.2e-6 of the result
     // at 1,024 rows.  Sums in float32 are therefore taken in parts, which are added with
-    // rounding.  (The 16-bit types round a thousand times as coarsely.)
-    a.part_rows = a.out32 ? 256 : INT32_MAX;
+    // rounding: 4.7e-7 whatever the length.  T = 4,096, K = 8, E = 32, N = 4,096,
+    // M = 2,048 takes 404 us in one part, 425 in parts of 512 rows, 533 in parts of 256.
+    // (The 16-bit types round a thousand times as coarsely.)
+    a.part_rows = a.out32 ? 512 : INT32_MAX;
     a.vec = d->M % (16 / size) == 0 && aligned16(d->grad_weights);
-    a.a = static_cast<const uint16_t *>(d->grad);
-    a.b = static_cast<const uint16_t *>(d->packed);
-    a.a_i = a.b_i = 1;
-    a.a_k = d->N;
-    a.b_k = d->M;
-    const bool maps = d->rows > 0 && d->N % 8 == 0 && d->M % 8 == 0 && aligned16(d->grad) &&
-                      aligned16(d->packed);
-    const Form f = maps ? Form{2, 256, 0} : Form{1, 128, 0};
-    set_form(&a, f, !maps);
-    const int64_t tiles = int64_t(a.feat_tiles) * a.col_tiles * a.E;
-    if (!maps)
-        return launch_product(vfp::expert_product<1, true, false, true>, a, f.ctas, tiles,
-                              stream, vfp::kFillThreads);
+    const Form f = {2, 256, 0};
+    set_form(&a, f);
     a.a_slabs = d->N % 64 == 0;
     a.b_slabs = d->M % 64 == 0;
-    if ((rc = make_row_map(&a.a_map, a.bf16, d->grad, d->N, d->rows)) != VF_OK ||
-        (rc = make_row_map(&a.b_maps[0], a.bf16, d->packed, d->M, d->rows)) != VF_OK)
-        return rc;
-    const Kernel kernel = a.out32 ? vfp::expert_product<2, true, true, false, true>
-                                  : vfp::expert_product<2, true, true, false>;
-    return launch_product(kernel, a, f.ctas, tiles, stream);
+    if (d->rows > 0) {                                     // else sums of nothing: zeros
+        char *const space = static_cast<char *>(d->workspace);
+        const int32_t *const used = d->offsets + d->E;
+        if (g.copied && (rc = g.copy(space, n_grad, nullptr, used, stream)) != VF_OK) return rc;
+        if (x.copied && (rc = x.copy(space + g.bytes(), n_packed, nullptr, used, stream)) != VF_OK)
+            return rc;
+        if ((rc = make_row_map(&a.a_map, a.bf16, g)) != VF_OK ||
+            (rc = make_row_map(&a.b_maps[0], a.bf16, x)) != VF_OK)
+            return rc;
+    }
+    const Kernel kernel = a.out32 ? vfp::expert_product<2, true, true, true>
+                                  : vfp::expert_product<2, true, true>;
+    return launch_product(kernel, a, f.ctas, int64_t(a.feat_tiles) * a.col_tiles * a.E, stream);
 }
 
 }  // namespace
 
 extern "C" {
+
+int64_t vf_expert_product_workspace(const vf_product_desc *d) {
+    const int rc = check_desc(d);
+    if (rc != VF_OK) return rc;
+    for (int i = 0; i < 3; ++i)
+        if (d->weight_strides[i] < 0) return VF_ERR_ARG;
+    return d->M > 0 ? workspace_of(weights_of(d), rows_of(d->packed, d->rows, d->M)) : 0;
+}
+
+int64_t vf_expert_weight_grad_workspace(const vf_product_desc *d) {
+    const int rc = check_desc(d);
+    if (rc != VF_OK) return rc;
+    return workspace_of(rows_of(d->grad, d->rows, d->N), rows_of(d->packed, d->rows, d->M));
+}
 
 int vf_expert_product(const vf_product_desc *d, vf_stream_t stream) {
     return product(d, as_stream(stream));
