@@ -36,7 +36,8 @@ constexpr int kStageA = kTileM * kBlockK * 2;  // bytes
 constexpr int kMaxStages = 12;
 constexpr int kBoxes = 4;                      // heights of the copies of B, multiples of one
 constexpr int kEpilogueWarps = 8;               // two for each quarter of the tile's features
-constexpr int kStagingBytes = 4608;            // per epilogue warp: 32 rows of 144 bytes
+// Staging of an epilogue warp: 32 rows of 64 bytes, or of up to 144.
+constexpr int kStagingRows = 2048, kStagingWeights = 4608;
 constexpr int kThreads = 32 * (4 + kEpilogueWarps);
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr uint64_t kDrainNs = 100000000ull;
@@ -85,6 +86,18 @@ __device__ __forceinline__ bool barrier_try(uint32_t bar, uint32_t parity) {
     return done != 0;
 }
 
+// Whether it has, without a wait: a try may hold its thread for some 4 us (every
+// product took as much longer when the last block of its last tile was issued behind a
+// try for a block that would not come).
+__device__ __forceinline__ bool barrier_test(uint32_t bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(done) : "r"(bar), "r"(parity) : "memory");
+    return done != 0;
+}
+
 // Waits for the phase of the given parity to end, for kWaitNs at most (and more_ns
 // for what may be due in between); false when it gave up, or another role did.
 __device__ __forceinline__ bool barrier_wait(uint32_t bar, uint32_t parity, volatile int *failed,
@@ -102,7 +115,7 @@ __device__ __forceinline__ bool barrier_wait(uint32_t bar, uint32_t parity, vola
     return true;
 }
 
-// The same by a whole warp, `ready`: the result of an earlier try.
+// The same by a whole warp, `ready`: the result of an earlier test.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *failed,
                                           bool ready = false, uint64_t more_ns = 0) {
     if (!ready) ready = barrier_wait(bar, parity, failed, more_ns);
@@ -601,8 +614,9 @@ struct Control {
 };
 
 // Shared memory: stages, staging, Control; 1,024 more for the alignment.
-__host__ __device__ constexpr int64_t shared_bytes(int stages, int stage_bytes) {
-    return int64_t(stages) * stage_bytes + kEpilogueWarps * kStagingBytes +
+__host__ __device__ constexpr int64_t shared_bytes(bool weights, int stages, int stage_bytes) {
+    return int64_t(stages) * stage_bytes +
+           kEpilogueWarps * (weights ? kStagingWeights : kStagingRows) +
            int64_t(sizeof(Control)) + 1024;
 }
 
@@ -614,6 +628,7 @@ template <int CTAS, bool WEIGHTS, bool A_MN, bool PARTS = false>
 __global__ void __launch_bounds__(kThreads, 1)
 expert_product(const __grid_constant__ ProductArgs a) {
     constexpr bool B_MN = WEIGHTS;
+    constexpr int kStagingBytes = WEIGHTS ? kStagingWeights : kStagingRows;
     extern __shared__ uint8_t raw[];
     uint8_t *const smem = raw + (1024 - (smem_addr(raw) & 1023)) % 1024;
     uint8_t *const staging = smem + a.stages * a.stage_bytes;
@@ -622,7 +637,11 @@ expert_product(const __grid_constant__ ProductArgs a) {
     const int warp = uniform(int(threadIdx.x >> 5)), lane = int(threadIdx.x & 31);
     const uint32_t rank = CTAS == 1 ? 0 : cluster_rank();
 
-    if (threadIdx.x == 0) {
+    // Every role walks the same tiles.  The first one is found while tensor memory is
+    // being allocated.
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (warp == 2) tmem_alloc<CTAS>(smem_addr(&ctl.tmem), uint32_t(a.tmem_cols));
+    if (warp == 3 && lane == 0) {
         for (int s = 0; s < a.stages; ++s) {
             barrier_init(smem_addr(&ctl.full[s]), 1);
             barrier_init(smem_addr(&ctl.empty[s]), 1);
@@ -634,16 +653,16 @@ expert_product(const __grid_constant__ ProductArgs a) {
         ctl.failed = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 2) tmem_alloc<CTAS>(smem_addr(&ctl.tmem), uint32_t(a.tmem_cols));
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    Tiles<CTAS, WEIGHTS> tiles(a);
+    Tile o = {};
+    bool more = tiles.next(o);
     fence_before();
     __syncthreads();
     if constexpr (CTAS > 1) cluster_sync();
     fence_after();
     const uint32_t tmem = uniform(ctl.tmem);
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
 
-    Tile o = {};
     int s = 0;                                       // stage and its phase
     uint32_t phase = 0;
     const auto advance = [&] {
@@ -659,9 +678,8 @@ expert_product(const __grid_constant__ ProductArgs a) {
         // copies: one warp for this CTA's A, one for its share of B
         const uint32_t bars = first_barrier<CTAS>(full);
         const bool one = elected();
-        Tiles<CTAS, WEIGHTS> tiles(a);
         bool ok = true;
-        while (ok && tiles.next(o)) {
+        for (; ok && more; more = tiles.next(o)) {
             const int half = o.n / CTAS;
             const int slabs = (half + 63) / 64;
             // rows form: one copy, as high as the tile needs
@@ -716,13 +734,12 @@ expert_product(const __grid_constant__ ProductArgs a) {
                                (uint32_t(kTileM * CTAS / 16) << 24);
         const uint32_t first = operand(ring), stage16 = uint32_t(a.stage_bytes) >> 4;
         const bool one = elected();
-        Tiles<CTAS, WEIGHTS> tiles(a);
         uint32_t it = 0;
         bool ok = true;
-        while (ok && tiles.next(o)) {
+        for (; ok && more; more = tiles.next(o)) {
             if (o.kblocks == 0) continue;
             const uint32_t acc = it & 1, acc_phase = it >> 1 & 1;
-            bool ready = barrier_try(full + s * 8, phase);
+            bool ready = barrier_test(full + s * 8, phase);
             ok = warp_wait(smem_addr(&ctl.acc_empty[acc]), acc_phase ^ 1, failed);
             fence_after();
             const uint32_t d = tmem + acc * uint32_t(a.acc_stride);
@@ -733,7 +750,7 @@ expert_product(const __grid_constant__ ProductArgs a) {
                 fence_after();
                 const uint32_t at = first + uint32_t(s) * stage16, bar = empty + s * 8;
                 advance();
-                ready = barrier_try(full + s * 8, phase);        // the next block's
+                ready = barrier_test(full + s * 8, phase);       // the next block's
                 if (one) {
 #pragma unroll
                     for (int q = 0; q < kBlockK / 16; ++q)
@@ -747,13 +764,12 @@ expert_product(const __grid_constant__ ProductArgs a) {
             ++it;
         }
     } else if (PARTS && warp >= 4 && warp < 4 + kEpilogueWarps) {
-        Tiles<CTAS, WEIGHTS> tiles(a);
         const int quarter = warp % 4, turn = (warp - 4) / 4;
         uint8_t *const mine = staging + (warp - 4) * kStagingBytes;
         uint32_t it = 0;
         bool ok = true;
         float sum[4][32];                            // half of the columns, by 32
-        while (tiles.next(o)) {
+        for (; more; more = tiles.next(o)) {
             const uint32_t acc = it & 1, acc_phase = it >> 1 & 1;
             const int n = min(o.n, a.cols - o.c0);
             if (!o.more) {
@@ -799,11 +815,10 @@ expert_product(const __grid_constant__ ProductArgs a) {
             }
         }
     } else if (warp >= 4 && warp < 4 + kEpilogueWarps) {
-        Tiles<CTAS, WEIGHTS> tiles(a);
         const int quarter = warp % 4, turn = (warp - 4) / 4;
         uint8_t *const mine = staging + (warp - 4) * kStagingBytes;
         uint32_t it = 0;
-        while (tiles.next(o)) {
+        for (; more; more = tiles.next(o)) {
             const uint32_t acc = it & 1, acc_phase = it >> 1 & 1;
             bool ok = true;
             if (o.kblocks > 0) {

@@ -85,6 +85,10 @@ int check_desc(const vf_product_desc *d) {
 // The dimensions of one of the kernel's forms.
 struct Form {
     int64_t ctas, tile_n, box;
+    int64_t resident = 1;         // on an SM
+    bool weights = false;
+
+    int64_t shared() const { return kSharedMemory / resident - (resident > 1 ? 1024 : 0); }
 };
 
 void set_form(vfp::ProductArgs *a, const Form &f) {
@@ -94,7 +98,7 @@ void set_form(vfp::ProductArgs *a, const Form &f) {
     a->stage_bytes = int32_t(vfp::kStageA + b_rows * 128);
     a->stages = 0;
     while (a->stages < vfp::kMaxStages &&
-           vfp::shared_bytes(a->stages + 1, a->stage_bytes) <= kSharedMemory)
+           vfp::shared_bytes(f.weights, a->stages + 1, a->stage_bytes) <= f.shared())
         ++a->stages;
     a->acc_stride = int32_t(std::max<int64_t>(32, f.tile_n));
     a->tmem_cols = 64;
@@ -105,10 +109,11 @@ void set_form(vfp::ProductArgs *a, const Form &f) {
 
 using Kernel = void (*)(vfp::ProductArgs);
 
-int launch_product(Kernel kernel, vfp::ProductArgs &a, int64_t ctas, int64_t tiles,
+int launch_product(Kernel kernel, vfp::ProductArgs &a, const Form &f, int64_t tiles,
                    cudaStream_t stream) {
     if (tiles == 0) return VF_OK;
-    const int64_t groups = std::min(kSMs / ctas, tiles);
+    const int64_t ctas = f.ctas;
+    const int64_t groups = std::min(kSMs * f.resident / ctas, tiles);
     if (a.col_tiles > 0) {
         a.step_experts = int32_t(groups / (int64_t(a.feat_tiles) * a.col_tiles));
         a.step_tiles = int32_t(groups % (int64_t(a.feat_tiles) * a.col_tiles));
@@ -122,7 +127,7 @@ int launch_product(Kernel kernel, vfp::ProductArgs &a, int64_t ctas, int64_t til
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(groups * ctas), 1, 1);
     cfg.blockDim = dim3(vfp::kThreads, 1, 1);
-    cfg.dynamicSmemBytes = size_t(vfp::shared_bytes(a.stages, a.stage_bytes));
+    cfg.dynamicSmemBytes = size_t(vfp::shared_bytes(f.weights, a.stages, a.stage_bytes));
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -304,7 +309,7 @@ int product(const vf_product_desc *d, cudaStream_t stream) {
             ? (mn ? vfp::expert_product<2, false, true> : vfp::expert_product<2, false, false>)
             : (mn ? vfp::expert_product<1, false, true> : vfp::expert_product<1, false, false>);
     const int64_t most = std::min(d->E, d->rows);          // experts that have rows
-    return launch_product(kernel, a, f.ctas, a.feat_tiles * (most + d->rows / f.tile_n), stream);
+    return launch_product(kernel, a, f, a.feat_tiles * (most + d->rows / f.tile_n), stream);
 }
 
 // The map of packed rows for the weights' gradient: the second dimension steps over
@@ -351,7 +356,7 @@ int weight_grad(const vf_product_desc *d, cudaStream_t stream) {
     // (The 16-bit types round a thousand times as coarsely.)
     a.part_rows = a.out32 ? 512 : INT32_MAX;
     a.vec = d->M % (16 / size) == 0 && aligned16(d->grad_weights);
-    const Form f = {2, 256, 0};
+    const Form f = {2, 256, 0, 1, true};
     set_form(&a, f);
     a.a_slabs = d->N % 64 == 0;
     a.b_slabs = d->M % 64 == 0;
@@ -367,7 +372,7 @@ int weight_grad(const vf_product_desc *d, cudaStream_t stream) {
     }
     const Kernel kernel = a.out32 ? vfp::expert_product<2, true, true, true>
                                   : vfp::expert_product<2, true, true>;
-    return launch_product(kernel, a, f.ctas, int64_t(a.feat_tiles) * a.col_tiles * a.E, stream);
+    return launch_product(kernel, a, f, int64_t(a.feat_tiles) * a.col_tiles * a.E, stream);
 }
 
 }  // namespace
