@@ -290,29 +290,22 @@ __device__ __forceinline__ uint8_t encode32(float y, float inv) {
         return uint8_t(__nv_cvt_float_to_fp8(q, __NV_SATFINITE, __NV_E4M3));
 }
 
-// Eight values to eight codes, with the steps of encode8 (|y| is at most the
-// group's amax, so that no INT8 clamp would act).
+// Four values to four codes, with the steps of encode8 (|y| is at most the group's
+// amax, so that no INT8 clamp would act).
 template <int FMT>
-__device__ __forceinline__ uint2 encode32x8(const float (&y)[8], float inv) {
-    uint32_t out[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        uint32_t lo, hi;
-        if constexpr (FMT == kFmtInt8) {
-            lo = __byte_perm(rint_bits(__fmul_rn(y[4 * k], inv)),
-                             rint_bits(__fmul_rn(y[4 * k + 1], inv)), 0x0040);
-            hi = __byte_perm(rint_bits(__fmul_rn(y[4 * k + 2], inv)),
-                             rint_bits(__fmul_rn(y[4 * k + 3], inv)), 0x0040);
-        } else {
-            const float2 inv2 = make_float2(inv, inv);
-            lo = __nv_cvt_float2_to_fp8x2(mul2_rn(make_float2(y[4 * k], y[4 * k + 1]), inv2),
-                                          __NV_SATFINITE, __NV_E4M3);
-            hi = __nv_cvt_float2_to_fp8x2(mul2_rn(make_float2(y[4 * k + 2], y[4 * k + 3]), inv2),
-                                          __NV_SATFINITE, __NV_E4M3);
-        }
-        out[k] = __byte_perm(lo, hi, 0x5410);
+__device__ __forceinline__ uint32_t encode32x4(const float *y, float inv) {
+    uint32_t lo, hi;
+    if constexpr (FMT == kFmtInt8) {
+        lo = __byte_perm(rint_bits(__fmul_rn(y[0], inv)), rint_bits(__fmul_rn(y[1], inv)), 0x0040);
+        hi = __byte_perm(rint_bits(__fmul_rn(y[2], inv)), rint_bits(__fmul_rn(y[3], inv)), 0x0040);
+    } else {
+        const float2 inv2 = make_float2(inv, inv);
+        lo = __nv_cvt_float2_to_fp8x2(mul2_rn(make_float2(y[0], y[1]), inv2), __NV_SATFINITE,
+                                      __NV_E4M3);
+        hi = __nv_cvt_float2_to_fp8x2(mul2_rn(make_float2(y[2], y[3]), inv2), __NV_SATFINITE,
+                                      __NV_E4M3);
     }
-    return make_uint2(out[0], out[1]);
+    return __byte_perm(lo, hi, 0x5410);
 }
 
 // The larger magnitude of two floats in one instruction, the sign as it falls; NaN
@@ -324,7 +317,7 @@ __device__ __forceinline__ float max_magnitude32(float a, float b) {
 }
 
 // The norm with a row held in the registers of a.warps warps, NV units of VW
-// elements to a lane.  FMT: 0 writes out, else codes (VW = 8, a group is 4 to 32
+// elements to a lane.  FMT: 0 writes out, else codes (VW = 8 or 4, a group is 4 to 32
 // lanes).
 template <class E, int VW, int NV, int FMT>
 __global__ void __launch_bounds__(1024)
@@ -411,10 +404,13 @@ norm_rows(const __grid_constant__ NormArgs a) {
         for (int j = 0; j < NV; ++j) {
             const int unit = (j * a.warps + part) * 32 + lane;
             const float q = __shfl_sync(kAll, inv, first + j);
-            uint2 code = encode32x8<FMT>(y[j], q);
-            if (q == 0.0f) code = make_uint2(0, 0);        // not live: NaN and infinities too
+            uint32_t code[VW / 4];
+#pragma unroll
+            for (int i = 0; i < VW / 4; ++i)               // not live: NaN and infinities too
+                code[i] = q == 0.0f ? 0u : encode32x4<FMT>(y[j] + 4 * i, q);
             if (there[j])
-                *reinterpret_cast<uint2 *>(a.codes + t * a.M + int64_t(unit) * VW) = code;
+                store_unit<uint32_t, VW / 4>(
+                    reinterpret_cast<uint32_t *>(a.codes + t * a.M + int64_t(unit) * VW), code);
             // (lane j of a row's last group may lie behind the row's end)
             if (mine == j && t < a.T && unit - mine < a.units)
                 a.scales[t * a.groups + unit / lanes] = scale;

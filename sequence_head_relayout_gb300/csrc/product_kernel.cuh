@@ -57,7 +57,7 @@ struct ProductArgs {
     int32_t box;                  // rows form: a copy of B has one to kBoxes times as many rows
     int32_t stages, stage_bytes;
     int32_t acc_stride, tmem_cols;
-    int32_t a_slabs, b_slabs;     // operands with i contiguous: 128 i by one copy
+    int32_t a_slabs, b_slabs;     // operands with i contiguous: a CTA's share by one copy
     int32_t bf16, gaps, vec, out32;
 };
 
@@ -686,7 +686,7 @@ expert_product(const __grid_constant__ ProductArgs a) {
             const int boxes = WEIGHTS ? slabs : (half + a.box - 1) / a.box;
             const CUtensorMap *const b_map = &a.b_maps[WEIGHTS ? 0 : boxes - 1];
             const uint32_t bytes = uint32_t(
-                CTAS * (kStageA + (WEIGHTS ? (a.b_slabs ? 2 : slabs) * 64 : boxes * a.box) * 128));
+                CTAS * (kStageA + (WEIGHTS ? (a.b_slabs ? 4 / CTAS : slabs) * 64 : boxes * a.box) * 128));
             const int fa = o.f0 + int(rank) * kTileM, cb = o.c0 + int(rank) * half;
             for (int kb = 0; kb < o.kblocks; ++kb) {
                 ok = warp_wait(empty + s * 8, phase ^ 1, failed);

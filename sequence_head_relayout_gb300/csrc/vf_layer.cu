@@ -153,13 +153,18 @@ NormKernel norm_kernel(int64_t nv) {
     }
 }
 
-template <int FMT>
+template <int FMT, int VW>
 NormKernel norm_q_kernel(int64_t nv) {
     switch (nv) {
-        case 1: return vf::norm_rows<vf::Bf16, 8, 1, FMT>;
-        case 2: return vf::norm_rows<vf::Bf16, 8, 2, FMT>;
-        default: return vf::norm_rows<vf::Bf16, 8, 4, FMT>;
+        case 1: return vf::norm_rows<vf::Bf16, VW, 1, FMT>;
+        case 2: return vf::norm_rows<vf::Bf16, VW, 2, FMT>;
+        default: return vf::norm_rows<vf::Bf16, VW, 4, FMT>;
     }
+}
+
+template <int FMT>
+NormKernel norm_q_kernel(int64_t vw, int64_t nv) {
+    return vw == 8 ? norm_q_kernel<FMT, 8>(nv) : norm_q_kernel<FMT, 4>(nv);
 }
 
 template <class E>
@@ -287,8 +292,9 @@ int norm(const vf_norm_desc *d, cudaStream_t stream) {
     a.units = int32_t(M / w.vw);
     const RowShape s = row_shape(a.units, T, 32, 4);
     a.warps = int32_t(s.warps);
-    // rows that do not fit the registers of a block, and unaligned ones with codes
-    if (s.warps > 32 || (fmt && w.vw < 8)) {
+    // rows that do not fit the registers of a block, and those with codes whose groups are
+    // no 4 to 32 lanes
+    if (s.warps > 32 || (fmt && (w.vw < 4 || d->group > 32 * w.vw))) {
         const NormKernel kernel =
             fmt ? (d->format == VF_FORMAT_INT8 ? vf::norm_any<vf::Bf16, vf::kFmtInt8>
                                                : vf::norm_any<vf::Bf16, vf::kFmtE4M3>)
@@ -298,8 +304,8 @@ int norm(const vf_norm_desc *d, cudaStream_t stream) {
         return launch(kernel, std::min<int64_t>(T, kSMs * 8), 256, 0, stream, a);
     }
     const NormKernel kernel =
-        fmt ? (d->format == VF_FORMAT_INT8 ? norm_q_kernel<vf::kFmtInt8>(s.nv)
-                                           : norm_q_kernel<vf::kFmtE4M3>(s.nv))
+        fmt ? (d->format == VF_FORMAT_INT8 ? norm_q_kernel<vf::kFmtInt8>(w.vw, s.nv)
+                                           : norm_q_kernel<vf::kFmtE4M3>(w.vw, s.nv))
         : d->type == VF_TYPE_BF16 ? norm_kernel<vf::Bf16>(w.vw, s.nv)
         : d->type == VF_TYPE_F16  ? norm_kernel<vf::F16>(w.vw, s.nv)
                                   : norm_kernel<vf::F32>(w.vw, s.nv);

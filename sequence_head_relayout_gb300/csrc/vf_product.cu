@@ -40,16 +40,16 @@ EncodeTiled encoder() {
 }
 
 // A map of 16-bit elements, innermost dimension contiguous; strides in elements
-// from the second dimension on; boxes of 64 elements (128 bytes, swizzled), two of
-// them along dimension `slabs`.
+// from the second dimension on; boxes of 64 elements (128 bytes, swizzled), n_slabs of
+// them along dimension `slabs`, where that is not 0.
 int make_map(CUtensorMap *map, bool bf16, int nd, const void *base, const int64_t *ext,
-             const int64_t *str, int64_t box1, int slabs = 0) {
+             const int64_t *str, int64_t box1, int slabs = 0, int64_t n_slabs = 2) {
     const EncodeTiled fn = encoder();
     if (fn == nullptr) return VF_ERR_CUDA;
     cuuint64_t dims[4], strides[3];
     cuuint32_t box[4] = {64, cuuint32_t(box1), 1, 1};
     const cuuint32_t steps[4] = {1, 1, 1, 1};
-    if (slabs) box[slabs] = 2;
+    if (slabs) box[slabs] = cuuint32_t(n_slabs);
     for (int i = 0; i < nd; ++i) {
         dims[i] = cuuint64_t(ext[i]);
         if (i > 0) strides[i - 1] = cuuint64_t(str[i]) * 2;
@@ -314,13 +314,13 @@ int product(const vf_product_desc *d, cudaStream_t stream) {
 
 // The map of packed rows for the weights' gradient: the second dimension steps over
 // the rows as the third does (see the kernel); columns by 64 where they are whole.
-int make_row_map(CUtensorMap *map, bool bf16, const Operand &x) {
+int make_row_map(CUtensorMap *map, bool bf16, const Operand &x, int64_t slabs) {
     if (x.len % 64) {
         const int64_t dims[3] = {x.len, 64, x.lines}, str[3] = {1, x.s_line, x.s_line};
         return make_map(map, bf16, 3, x.p, dims, str, 64);
     }
     const int64_t dims[4] = {64, 64, x.lines, x.len / 64}, str[4] = {1, x.s_line, x.s_line, 64};
-    return make_map(map, bf16, 4, x.p, dims, str, 64, 3);
+    return make_map(map, bf16, 4, x.p, dims, str, 64, 3, slabs);
 }
 
 int weight_grad(const vf_product_desc *d, cudaStream_t stream) {
@@ -351,12 +351,13 @@ int weight_grad(const vf_product_desc *d, cudaStream_t stream) {
     // The tensor cores cut off what lies below an accumulator's last bit, always towards
     // the same side, so that a sum's error grows with its length: 1.2e-6 of the result
     // at 1,024 rows.  Sums in float32 are therefore taken in parts, which are added with
-    // rounding: 4.7e-7 whatever the length.  T = 4,096, K = 8, E = 32, N = 4,096,
-    // M = 2,048 takes 404 us in one part, 425 in parts of 512 rows, 533 in parts of 256.
+    // rounding: some 7e-7 whatever the length.  T = 4,096, K = 8, E = 32, N = 4,096,
+    // M = 2,048 takes 384 us in one part, 397 in parts of 768 rows, 415 in parts of 512.
     // (The 16-bit types round a thousand times as coarsely.)
-    a.part_rows = a.out32 ? 512 : INT32_MAX;
+    a.part_rows = a.out32 ? 768 : INT32_MAX;
     a.vec = d->M % (16 / size) == 0 && aligned16(d->grad_weights);
-    const Form f = {2, 256, 0, 1, true};
+    // (half of a pair would have no feature to store)
+    const Form f = {d->N <= vfp::kTileM ? 1 : 2, 256, 0, 1, true};
     set_form(&a, f);
     a.a_slabs = d->N % 64 == 0;
     a.b_slabs = d->M % 64 == 0;
@@ -366,12 +367,15 @@ int weight_grad(const vf_product_desc *d, cudaStream_t stream) {
         if (g.copied && (rc = g.copy(space, n_grad, nullptr, used, stream)) != VF_OK) return rc;
         if (x.copied && (rc = x.copy(space + g.bytes(), n_packed, nullptr, used, stream)) != VF_OK)
             return rc;
-        if ((rc = make_row_map(&a.a_map, a.bf16, g)) != VF_OK ||
-            (rc = make_row_map(&a.b_maps[0], a.bf16, x)) != VF_OK)
+        if ((rc = make_row_map(&a.a_map, a.bf16, g, 2)) != VF_OK ||
+            (rc = make_row_map(&a.b_maps[0], a.bf16, x, 4 / f.ctas)) != VF_OK)
             return rc;
     }
-    const Kernel kernel = a.out32 ? vfp::expert_product<2, true, true, true>
-                                  : vfp::expert_product<2, true, true>;
+    const Kernel kernel =
+        f.ctas == 2 ? (a.out32 ? vfp::expert_product<2, true, true, true>
+                               : vfp::expert_product<2, true, true>)
+                    : (a.out32 ? vfp::expert_product<1, true, true, true>
+                               : vfp::expert_product<1, true, true>);
     return launch_product(kernel, a, f, int64_t(a.feat_tiles) * a.col_tiles * a.E, stream);
 }
 

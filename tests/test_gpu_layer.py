@@ -245,7 +245,8 @@ def test_norm_special_rows(dtype):
 @pytest.mark.parametrize("fmt", ["int8", "e4m3"])
 @pytest.mark.parametrize("group", [32, 64, 128, 256])
 @pytest.mark.parametrize("T,M", [(1, 1), (2, 33), (3, 256), (5, 264), (1, 4096), (40, 1000),
-                                 (641, 3584), (3, 20000), (2, 40000), (7, 1001)])
+                                 (641, 3584), (3, 20000), (2, 40000), (7, 1001), (700, 1420),
+                                 (9, 36)])
 def test_norm_q(T, M, group, fmt):
     x, r = randn((T, M), BF16, 1) * 3, randn((T, M), BF16, 2)
     w = randn((M,), BF16, 3)
