@@ -227,14 +227,14 @@ void take_weight(Width *w, const vf_norm_desc *d) {
         w->vw /= 2;
 }
 
-// Units of a lane and warps of a row.
+// Units of a lane and warps of a row: by the row alone, so that its result does not
+// depend on how many others there are.
 struct RowShape {
     int64_t nv, warps, rows;       // rows of a block
 };
 
-RowShape row_shape(int64_t units, int64_t T, int64_t most_warps, int64_t nv) {
+RowShape row_shape(int64_t units, int64_t most_warps, int64_t nv) {
     RowShape s = {nv, 0, 1};
-    if (T <= kSMs * 4) s.nv = 1;   // few rows: more warps to each
     while (s.nv < 4 && ceil_div(units, 32 * s.nv) > most_warps) s.nv *= 2;
     while (s.nv > 1 && ceil_div(units, 32) <= s.nv / 2) s.nv /= 2;
     s.warps = ceil_div(units, 32 * s.nv);
@@ -290,7 +290,7 @@ int norm(const vf_norm_desc *d, cudaStream_t stream) {
     }
     take_weight(&w, d);
     a.units = int32_t(M / w.vw);
-    const RowShape s = row_shape(a.units, T, 32, 4);
+    const RowShape s = row_shape(a.units, 32, 4);
     a.warps = int32_t(s.warps);
     // rows that do not fit the registers of a block, and those with codes whose groups are
     // no 4 to 32 lanes
@@ -347,7 +347,7 @@ int norm_backward(const vf_norm_desc *d, cudaStream_t stream) {
         }
         take_weight(&w, d);
         a.units = int32_t(M / w.vw);
-        const RowShape s = row_shape(a.units, T, 16, 2);
+        const RowShape s = row_shape(a.units, 16, 2);
         a.warps = int32_t(s.warps);
         if (s.warps > 16) {
             a.blocks = int32_t(norm_blocks(T));
