@@ -519,7 +519,8 @@ typedef struct vf_product_desc {
     int32_t out_type;           /* vf_expert_weight_grad: type, or VF_TYPE_F32 */
     int64_t E, N, M;
     int64_t rows;               /* rows of packed, grad and out */
-    int64_t slots;              /* T * K of the plan: steers the choice of a form only */
+    int64_t slots;              /* T * K of the plan (0: not known): steers the choice of a
+                                 * form only */
     int64_t align;
     const int32_t *counts;      /* [E] */
     const int32_t *offsets;     /* [E + 1] */

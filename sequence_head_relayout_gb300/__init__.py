@@ -42,6 +42,12 @@ the backward pass: :func:`expert_pack_q`, :func:`expert_restore_q`,
 :func:`expert_merge_q` and :func:`expert_merge_backward_q`.  None of the calls
 records an autograd graph: the gradients are calls of their own, and the packs
 and merges refuse a tensor that requires a gradient while grad mode is on.
+
+An expert layer's arithmetic, in the same manner: :func:`expert_product` (the packed
+rows times their experts' weights) and :func:`expert_weight_grad`,
+:func:`expert_glu` and :func:`expert_glu_backward` (the gated activation between
+two products), :func:`rms_norm`, :func:`rms_norm_q` and :func:`rms_norm_backward` (the
+root-mean-square norm in front, with the residual's addition).
 """
 import ctypes
 import os

@@ -7,7 +7,14 @@
 // norm backward  dx = r (w g - h r^2 mean(w g h)) + dtotal,  dw = sum_t g h r
 //
 // All are bound by HBM: each element is read and written once, with some twenty
-// operations in float32 between.
+// operations in float32 between.  Measured on GB300 (device time; bytes that cannot be
+// avoided over it):
+//   glu            110,828 rows, F = 2,048, bf16                 196 us   7.0 TB/s
+//   glu backward   the same                                      317 us   6.9 TB/s
+//   norm           T = 55,414, M = 3,584, bf16, with a residual  227 us   7.0 TB/s
+//   norm to E4M3   the same                                      227 us   6.1 TB/s
+//   norm backward  T = 55,413, M = 2,048, fp32, with grad_total  268 us   6.8 TB/s
+//                  T = 55,414, M = 3,584, bf16, with grad_total  296 us   5.4 TB/s
 #pragma once
 
 #include <cstdint>

@@ -246,13 +246,20 @@ int64_t workspace_of(const Operand &a, const Operand &b) {
     return n < 0 || m < 0 || !add_ok(n, m, &sum) ? VF_ERR_OVERFLOW : sum;
 }
 
-// Rows of a tile, by the rows that an expert has on average.
+// The form by the rows that an expert has on average.  Measured with E = 64,
+// N = 4,096, M = 2,048 (us; forms by CTAs and rows of a tile):
+//   rows    1 x 32   1 x 64   1 x 128   2 x 128   2 x 256
+//      8       162      159       163       159       166
+//     32       174      164       167       164       171
+//     64       222      179       174       169       174
+//    128       367      239       198       187       185
+//    192       520      305       237       217       201
+// A pair would have no feature to store in its second CTA with N at most 128.
 Form rows_form(const vf_product_desc *d) {
-    const int64_t mean = ceil_div(d->slots, d->E);
-    if (mean <= 8) return {1, 32, 16};
+    const int64_t mean = ceil_div(d->slots > 0 ? d->slots : d->rows, d->E);
     if (mean <= 32) return {1, 64, 16};
-    if (mean <= 96 || d->N <= 128) return {1, 128, 32};
-    return {2, 256, 32};
+    if (d->N <= vfp::kTileM) return {1, 128, 32};
+    return mean <= 112 ? Form{2, 128, 16} : Form{2, 256, 32};
 }
 
 int product(const vf_product_desc *d, cudaStream_t stream) {
