@@ -49,6 +49,7 @@ constexpr int kBoxes = 4;                      // heights of the copies of B, mu
 constexpr int kEpilogueWarps = 8;              // two for each quarter of the tile's features
 // Staging of an epilogue warp: 32 rows of 64 bytes, or of up to 144.
 constexpr int kStagingRows = 2048, kStagingWeights = 4608;
+constexpr int kPartBytes = 2 * 32 * kTileM * 4; // SPLIT: 32 columns of each turn's, in float32
 constexpr int kThreads = 32 * (4 + kEpilogueWarps);
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr uint64_t kDrainNs = 100000000ull;
@@ -65,10 +66,12 @@ struct ProductArgs {
     int32_t part_rows;            // weights: most rows of one accumulation
     int32_t step_experts, step_tiles;    // weights: the grid's tiles, in experts and the rest
     int32_t tile_n;               // most rows (columns) of a tile
+    int32_t split;                // CTAs that share the sums of a tile
     int32_t box;                  // rows form: a copy of B has one to kBoxes times as many rows
     int32_t stages, stage_bytes;
     int32_t acc_stride, tmem_cols;
-    int32_t a_slabs, b_slabs;     // operands with i contiguous: a CTA's share by one copy
+    int32_t a_slabs, b_slabs;     // operands with i contiguous: 64 i to a slab, a CTA's share
+                                  // by one copy of so many; 0: a copy for each
     int32_t bf16, gaps, vec, out32;
 };
 
@@ -152,11 +155,23 @@ __device__ __forceinline__ void barrier_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// Arrival at the barrier of the pair's first CTA.
-__device__ __forceinline__ void barrier_arrive_first(uint32_t bar) {
-    asm volatile("{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %0, 0;\n\t"
-                 "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [r];\n\t}"
-                 ::"r"(bar) : "memory");
+// The address of CTA `to` of the cluster that is `addr` here.
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t to) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(to));
+    return r;
+}
+
+// Arrival at the barrier of CTA `to`.
+__device__ __forceinline__ void barrier_arrive_at(uint32_t bar, uint32_t to) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];"
+                 ::"r"(cluster_addr(bar, to)) : "memory");
+}
+
+__device__ __forceinline__ float cluster_load(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
 }
 
 __device__ __forceinline__ void barrier_expect(uint32_t bar, uint32_t bytes) {
@@ -180,10 +195,7 @@ __device__ __forceinline__ void cluster_sync() {
 // The barrier of a pair's copies is that of its first CTA.
 template <int CTAS>
 __device__ __forceinline__ uint32_t first_barrier(uint32_t bar) {
-    if constexpr (CTAS == 1) return bar;
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(bar));
-    return r;
+    return CTAS == 1 ? bar : cluster_addr(bar, 0);
 }
 
 template <int CTAS>
@@ -347,7 +359,7 @@ struct Tile {
 // experts' tiles in order, an expert's row tiles fastest (they share a tile of
 // weights), each expert's rows cut into equal tiles.  A lane holds four experts, a
 // warp 128 at a time.
-template <int CTAS, bool WEIGHTS>
+template <int CTAS, bool WEIGHTS, bool SPLIT>
 struct Tiles {
     static constexpr int kStep = 16 * CTAS;
     const ProductArgs &a;
@@ -362,11 +374,16 @@ struct Tiles {
     // weights form: the tile as a number within its expert
     int e, in, each;
     int next_row0, next_valid;    // loaded a tile ahead
+    int slice = 0;                // SPLIT: this CTA's of a.split shares of the sums
     int row0, rest;               // what is left of the expert's rows (sums in parts)
     bool inside = false;
 
     __device__ __forceinline__ explicit Tiles(const ProductArgs &args)
-        : a(args), lane(int(threadIdx.x & 31)), t(blockIdx.x / CTAS), step(gridDim.x / CTAS) {
+        : a(args), lane(int(threadIdx.x & 31)) {
+        const uint32_t group = SPLIT ? uint32_t(a.split) : CTAS;
+        t = blockIdx.x / group;
+        step = gridDim.x / group;
+        if constexpr (SPLIT) slice = int(cluster_rank());
         if constexpr (WEIGHTS) {
             each = a.feat_tiles * a.col_tiles;
             e = int(t) / each;
@@ -412,6 +429,14 @@ struct Tiles {
             o.more = false;
             row0 = next_row0;
             rest = next_valid;
+            if constexpr (SPLIT) {
+                // this CTA's share of the blocks
+                const int64_t n = parts(rest, kBlockK);
+                const int from = int(n * slice / a.split) * kBlockK;
+                const int to = int(min(n * (slice + 1) / a.split * kBlockK, int64_t(rest)));
+                row0 += from;
+                rest = to - from;
+            }
             e += a.step_experts;
             in += a.step_tiles;
             if (in >= each) {
@@ -478,7 +503,7 @@ struct Tiles {
         o.valid = min(part, c - r * part);
         o.n = (o.valid + kStep - 1) / kStep * kStep;
         o.c0 = 0;
-        o.kblocks = (a.red + kBlockK - 1) / kBlockK;
+        o.kblocks = parts(a.red, kBlockK);
         o.gap = 0;
         if (a.gaps && r == row_tiles - 1)
             o.gap = max(0, min(a.offsets[o.e + 1], a.rows) - (b + c));
@@ -618,16 +643,64 @@ __device__ __forceinline__ void store_weights(const ProductArgs &a, const uint32
 
 // ---- the kernel ----------------------------------------------------------------
 
+
 struct Control {
     uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2];
+    uint64_t part_full[2], part_empty[2];   // SPLIT, for each turn of the epilogue
     uint32_t tmem;
     int failed;
 };
 
-// Shared memory: stages, staging, Control; 1,024 more for the alignment.
-__host__ __device__ constexpr int64_t shared_bytes(bool weights, int stages, int stage_bytes) {
+// The sum of a tile's 32 columns over the CTAs that share it.  A warp holds 32 features
+// of them; the four warps of its turn leave theirs in `part`, CTA `owner` adds all
+// CTAs' in their order, and its four warps get the result in v (true).  No part is
+// written again before it has been read.
+struct Join {
+    uint32_t chunk = 0, owned = 0;                   // of this turn so far
+
+    __device__ __forceinline__ bool operator()(const ProductArgs &a, Control &ctl, float *part,
+                                               int turn, int quarter, int lane, int slice,
+                                               int owner, volatile int *failed,
+                                               uint64_t more_ns, bool &ok, uint32_t (&v)[32]) {
+        const uint32_t full = smem_addr(&ctl.part_full[turn]);
+        const uint32_t empty = smem_addr(&ctl.part_empty[turn]);
+        if (chunk > 0 && ok) {
+            ok = warp_wait(empty, (chunk - 1) & 1, failed, false, more_ns);
+            asm volatile("fence.acq_rel.cluster;" ::: "memory");
+        }
+        ++chunk;
+        float *const mine = part + turn * 32 * kTileM + quarter * 32 + lane;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) mine[j * kTileM] = __uint_as_float(v[j]);
+        __syncwarp();
+        if (lane == 0) barrier_arrive_at(full, uint32_t(owner));
+        if (slice != owner) return false;
+        if (ok) ok = warp_wait(full, owned & 1, failed, false, more_ns);
+        asm volatile("fence.acq_rel.cluster;" ::: "memory");
+        ++owned;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = 0;
+        for (int q = 0; q < a.split; ++q) {
+            const uint32_t from = cluster_addr(smem_addr(mine), uint32_t(q));
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                v[j] = __float_as_uint(__uint_as_float(v[j]) +
+                                       cluster_load(from + j * kTileM * 4));
+        }
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (!ok) v[j] = 0x7FC00000u;
+        __syncwarp();
+        if (lane < a.split) barrier_arrive_at(empty, uint32_t(lane));
+        return true;
+    }
+};
+
+// Shared memory: stages, staging, parts, Control; 1,024 more for the alignment.
+__host__ __device__ constexpr int64_t shared_bytes(bool weights, bool split, int stages,
+                                                   int stage_bytes) {
     return int64_t(stages) * stage_bytes +
-           kEpilogueWarps * (weights ? kStagingWeights : kStagingRows) +
+           kEpilogueWarps * (weights ? kStagingWeights : kStagingRows) + (split ? kPartBytes : 0) +
            int64_t(sizeof(Control)) + 1024;
 }
 
@@ -635,15 +708,18 @@ __host__ __device__ constexpr int64_t shared_bytes(bool weights, int stages, int
 // WEIGHTS  the weights' gradient, else the rows' product
 // A_MN     the first operand is stored with i contiguous
 // PARTS    sums are taken in parts of a.part_rows rows, which are added in registers
-template <int CTAS, bool WEIGHTS, bool A_MN, bool PARTS = false>
+// SPLIT    the a.split CTAs of a cluster share the sums of a tile (weights)
+template <int CTAS, bool WEIGHTS, bool A_MN, bool PARTS = false, bool SPLIT = false>
 __global__ void __launch_bounds__(kThreads, 1)
 expert_product(const __grid_constant__ ProductArgs a) {
+    static_assert(!SPLIT || (CTAS == 1 && WEIGHTS), "single CTAs share the weights' sums");
     constexpr bool B_MN = WEIGHTS;
     constexpr int kStagingBytes = WEIGHTS ? kStagingWeights : kStagingRows;
     extern __shared__ uint8_t raw[];
     uint8_t *const smem = raw + (1024 - (smem_addr(raw) & 1023)) % 1024;
     uint8_t *const staging = smem + a.stages * a.stage_bytes;
-    Control &ctl = *reinterpret_cast<Control *>(staging + kEpilogueWarps * kStagingBytes);
+    uint8_t *const part = staging + kEpilogueWarps * kStagingBytes;
+    Control &ctl = *reinterpret_cast<Control *>(part + (SPLIT ? kPartBytes : 0));
     volatile int *const failed = &ctl.failed;
     const int warp = uniform(int(threadIdx.x >> 5)), lane = int(threadIdx.x & 31);
     const uint32_t rank = CTAS == 1 ? 0 : cluster_rank();
@@ -660,17 +736,21 @@ expert_product(const __grid_constant__ ProductArgs a) {
         for (int i = 0; i < 2; ++i) {
             barrier_init(smem_addr(&ctl.acc_full[i]), 1);
             barrier_init(smem_addr(&ctl.acc_empty[i]), kEpilogueWarps * CTAS);
+            if constexpr (SPLIT) {
+                barrier_init(smem_addr(&ctl.part_full[i]), kEpilogueWarps / 2 * a.split);
+                barrier_init(smem_addr(&ctl.part_empty[i]), kEpilogueWarps / 2);
+            }
         }
         ctl.failed = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    Tiles<CTAS, WEIGHTS> tiles(a);
+    Tiles<CTAS, WEIGHTS, SPLIT> tiles(a);
     Tile o = {};
     bool more = tiles.next(o);
     fence_before();
     __syncthreads();
-    if constexpr (CTAS > 1) cluster_sync();
+    if constexpr (CTAS > 1 || SPLIT) cluster_sync();
     fence_after();
     const uint32_t tmem = uniform(ctl.tmem);
 
@@ -697,7 +777,7 @@ expert_product(const __grid_constant__ ProductArgs a) {
             const int boxes = WEIGHTS ? slabs : (half + a.box - 1) / a.box;
             const CUtensorMap *const b_map = &a.b_maps[WEIGHTS ? 0 : boxes - 1];
             const uint32_t bytes = uint32_t(
-                CTAS * (kStageA + (WEIGHTS ? (a.b_slabs ? 4 / CTAS : slabs) * 64 : boxes * a.box) * 128));
+                CTAS * (kStageA + (WEIGHTS ? (a.b_slabs ? a.b_slabs : slabs) * 64 : boxes * a.box) * 128));
             const int fa = o.f0 + int(rank) * kTileM, cb = o.c0 + int(rank) * half;
             for (int kb = 0; kb < o.kblocks; ++kb) {
                 ok = warp_wait(empty + s * 8, phase ^ 1, failed);
@@ -780,6 +860,7 @@ expert_product(const __grid_constant__ ProductArgs a) {
         uint32_t it = 0;
         bool ok = true;
         float sum[4][32];                            // half of the columns, by 32
+        Join join;
         for (; more; more = tiles.next(o)) {
             const uint32_t acc = it & 1, acc_phase = it >> 1 & 1;
             const int n = min(o.n, a.cols - o.c0);
@@ -809,11 +890,11 @@ expert_product(const __grid_constant__ ProductArgs a) {
                 __syncwarp();
                 if (ok && lane == 0) {
                     if constexpr (CTAS == 1) barrier_arrive(smem_addr(&ctl.acc_empty[acc]));
-                    else barrier_arrive_first(smem_addr(&ctl.acc_empty[acc]));
+                    else barrier_arrive_at(smem_addr(&ctl.acc_empty[acc]), 0);
                 }
             }
             const int f = o.f0 + int(rank) * kTileM + quarter * 32;
-            if (tiles.inside || f >= a.feat) continue;
+            if (tiles.inside || (!SPLIT && f >= a.feat)) continue;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int c = 32 * turn + 64 * i;
@@ -822,6 +903,11 @@ expert_product(const __grid_constant__ ProductArgs a) {
 #pragma unroll
                 for (int j = 0; j < 32; ++j)
                     v[j] = ok ? __float_as_uint(sum[i][j]) : 0x7FC00000u;
+                if constexpr (SPLIT)
+                    if (!join(a, ctl, reinterpret_cast<float *>(part), turn, quarter, lane,
+                              tiles.slice, i % a.split, failed, uint64_t(o.kblocks) * 8192, ok, v))
+                        continue;
+                if (f >= a.feat) continue;
                 store_weights(a, v, o.e, f, o.c0 + c, lane, false, mine);
             }
         }
@@ -829,6 +915,7 @@ expert_product(const __grid_constant__ ProductArgs a) {
         const int quarter = warp % 4, turn = (warp - 4) / 4;
         uint8_t *const mine = staging + (warp - 4) * kStagingBytes;
         uint32_t it = 0;
+        Join join;
         for (; more; more = tiles.next(o)) {
             const uint32_t acc = it & 1, acc_phase = it >> 1 & 1;
             bool ok = true;
@@ -852,6 +939,10 @@ expert_product(const __grid_constant__ ProductArgs a) {
 #pragma unroll
                     for (int j = 0; j < 32; ++j) v[j] = ok ? 0u : 0x7FC00000u;
                 }
+                if constexpr (SPLIT)
+                    if (!join(a, ctl, reinterpret_cast<float *>(part), turn, quarter, lane,
+                              tiles.slice, c / 64 % a.split, failed, uint64_t(o.kblocks) * 8192, ok, v))
+                        continue;
                 if (f >= a.feat) continue;           // all lanes alike
                 if constexpr (WEIGHTS)
                     store_weights(a, v, o.e, f, o.c0 + c, lane, o.more, mine);
@@ -863,7 +954,7 @@ expert_product(const __grid_constant__ ProductArgs a) {
                 __syncwarp();
                 if (lane == 0) {
                     if constexpr (CTAS == 1) barrier_arrive(smem_addr(&ctl.acc_empty[acc]));
-                    else barrier_arrive_first(smem_addr(&ctl.acc_empty[acc]));
+                    else barrier_arrive_at(smem_addr(&ctl.acc_empty[acc]), 0);
                 }
             }
             if (!WEIGHTS && o.gap > 0 && f < a.feat && turn == 0)
@@ -879,7 +970,7 @@ expert_product(const __grid_constant__ ProductArgs a) {
     }
     fence_before();
     __syncthreads();
-    if constexpr (CTAS > 1) cluster_sync();
+    if constexpr (CTAS > 1 || SPLIT) cluster_sync();
     fence_after();
     if (warp == 2) tmem_free<CTAS>(tmem, uint32_t(a.tmem_cols));
 }

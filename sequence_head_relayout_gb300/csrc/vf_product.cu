@@ -85,20 +85,27 @@ int check_desc(const vf_product_desc *d) {
 // The dimensions of one of the kernel's forms.
 struct Form {
     int64_t ctas, tile_n, box;
-    int64_t resident = 1;         // on an SM
     bool weights = false;
+    int64_t split = 1;            // CTAs that share a tile's sums
 
-    int64_t shared() const { return kSharedMemory / resident - (resident > 1 ? 1024 : 0); }
+    int64_t cluster() const { return ctas * split; }
 };
+
+// Rows that an expert has on average.
+int64_t mean_rows(const vf_product_desc *d) {
+    return ceil_div(d->slots > 0 ? d->slots : d->rows, d->E);
+}
 
 void set_form(vfp::ProductArgs *a, const Form &f) {
     const int64_t b_rows = f.tile_n / f.ctas;
     a->tile_n = int32_t(f.tile_n);
     a->box = int32_t(f.box);
+    a->split = int32_t(f.split);
     a->stage_bytes = int32_t(vfp::kStageA + b_rows * 128);
     a->stages = 0;
     while (a->stages < vfp::kMaxStages &&
-           vfp::shared_bytes(f.weights, a->stages + 1, a->stage_bytes) <= f.shared())
+           vfp::shared_bytes(f.weights, f.split > 1, a->stages + 1, a->stage_bytes) <=
+               kSharedMemory)
         ++a->stages;
     a->acc_stride = int32_t(std::max<int64_t>(32, f.tile_n));
     a->tmem_cols = 64;
@@ -112,8 +119,8 @@ using Kernel = void (*)(vfp::ProductArgs);
 int launch_product(Kernel kernel, vfp::ProductArgs &a, const Form &f, int64_t tiles,
                    cudaStream_t stream) {
     if (tiles == 0) return VF_OK;
-    const int64_t ctas = f.ctas;
-    const int64_t groups = std::min(kSMs * f.resident / ctas, tiles);
+    const int64_t ctas = f.cluster();
+    const int64_t groups = std::min(kSMs / ctas, tiles);
     if (a.col_tiles > 0) {
         a.step_experts = int32_t(groups / (int64_t(a.feat_tiles) * a.col_tiles));
         a.step_tiles = int32_t(groups % (int64_t(a.feat_tiles) * a.col_tiles));
@@ -127,7 +134,7 @@ int launch_product(Kernel kernel, vfp::ProductArgs &a, const Form &f, int64_t ti
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(groups * ctas), 1, 1);
     cfg.blockDim = dim3(vfp::kThreads, 1, 1);
-    cfg.dynamicSmemBytes = size_t(vfp::shared_bytes(f.weights, a.stages, a.stage_bytes));
+    cfg.dynamicSmemBytes = size_t(vfp::shared_bytes(f.weights, f.split > 1, a.stages, a.stage_bytes));
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -256,7 +263,7 @@ int64_t workspace_of(const Operand &a, const Operand &b) {
 //    192       520      305       237       217       201
 // A pair would have no feature to store in its second CTA with N at most 128.
 Form rows_form(const vf_product_desc *d) {
-    const int64_t mean = ceil_div(d->slots > 0 ? d->slots : d->rows, d->E);
+    const int64_t mean = mean_rows(d);
     if (mean <= 32) return {1, 64, 16};
     if (d->N <= vfp::kTileM) return {1, 128, 32};
     return mean <= 112 ? Form{2, 128, 16} : Form{2, 256, 32};
@@ -296,7 +303,7 @@ int product(const vf_product_desc *d, cudaStream_t stream) {
         if (x.copied && (rc = x.copy(space + w.bytes(), n_packed, nullptr, d->offsets + d->E,
                                      stream)) != VF_OK)
             return rc;
-        a.a_slabs = mn && d->N % 64 == 0;
+        a.a_slabs = mn && d->N % 64 == 0 ? 2 : 0;
         if (a.a_slabs) {
             const int64_t dims[4] = {64, w.lines, d->N / 64, d->E};
             const int64_t str[4] = {1, w.s_line, 64, w.s_outer};
@@ -328,6 +335,24 @@ int make_row_map(CUtensorMap *map, bool bf16, const Operand &x, int64_t slabs) {
     }
     const int64_t dims[4] = {64, 64, x.lines, x.len / 64}, str[4] = {1, x.s_line, x.s_line, 64};
     return make_map(map, bf16, 4, x.p, dims, str, 64, 3, slabs);
+}
+
+// Pairs, unless half of a pair would have no feature to store, or they would leave half
+// of the SMs idle.  Tiles that are still few are made smaller, and the CTAs of a cluster
+// share their rows: N = M = 512, E = 2 with 27,707 rows each takes 199 us with
+// 16 tiles of 256 columns, 71 with four CTAs to each (102 with eight, whose clusters do
+// not all find room at once), 47 with 32 tiles of 128 columns and four CTAs to each.
+// Below some 24 blocks to a CTA its sums cost more than they save (1,500 rows: 8.1 us,
+// 11.9 with two CTAs).
+Form weights_form(const vf_product_desc *d) {
+    const int64_t columns = d->E * ceil_div(d->M, 256), features = ceil_div(d->N, vfp::kTileM);
+    if (features > 1 && 4 * columns * ceil_div(features, 2) > kSMs) return {2, 256, 0, true};
+    const bool few = 4 * columns * features < kSMs;
+    Form f = {1, few ? 128 : 256, 0, true};
+    const int64_t tiles = d->E * ceil_div(d->M, f.tile_n) * features;
+    const int64_t blocks = ceil_div(mean_rows(d), vfp::kBlockK);
+    while (f.split < 4 && 2 * f.split * tiles <= kSMs && blocks >= 48 * f.split) f.split *= 2;
+    return f;
 }
 
 int weight_grad(const vf_product_desc *d, cudaStream_t stream) {
@@ -363,11 +388,10 @@ int weight_grad(const vf_product_desc *d, cudaStream_t stream) {
     // (The 16-bit types round a thousand times as coarsely.)
     a.part_rows = a.out32 ? 768 : INT32_MAX;
     a.vec = d->M % (16 / size) == 0 && aligned16(d->grad_weights);
-    // (half of a pair would have no feature to store)
-    const Form f = {d->N <= vfp::kTileM ? 1 : 2, 256, 0, 1, true};
+    const Form f = weights_form(d);
     set_form(&a, f);
-    a.a_slabs = d->N % 64 == 0;
-    a.b_slabs = d->M % 64 == 0;
+    a.a_slabs = d->N % 64 ? 0 : 2;
+    a.b_slabs = d->M % 64 ? 0 : int32_t(f.tile_n / f.ctas / 64);
     if (d->rows > 0) {                                     // else sums of nothing: zeros
         char *const space = static_cast<char *>(d->workspace);
         const int32_t *const used = d->offsets + d->E;
@@ -375,14 +399,16 @@ int weight_grad(const vf_product_desc *d, cudaStream_t stream) {
         if (x.copied && (rc = x.copy(space + g.bytes(), n_packed, nullptr, used, stream)) != VF_OK)
             return rc;
         if ((rc = make_row_map(&a.a_map, a.bf16, g, 2)) != VF_OK ||
-            (rc = make_row_map(&a.b_maps[0], a.bf16, x, 4 / f.ctas)) != VF_OK)
+            (rc = make_row_map(&a.b_maps[0], a.bf16, x, a.b_slabs)) != VF_OK)
             return rc;
     }
     const Kernel kernel =
-        f.ctas == 2 ? (a.out32 ? vfp::expert_product<2, true, true, true>
-                               : vfp::expert_product<2, true, true>)
-                    : (a.out32 ? vfp::expert_product<1, true, true, true>
-                               : vfp::expert_product<1, true, true>);
+        f.ctas == 2    ? (a.out32 ? vfp::expert_product<2, true, true, true>
+                                  : vfp::expert_product<2, true, true>)
+        : f.split == 1 ? (a.out32 ? vfp::expert_product<1, true, true, true>
+                                  : vfp::expert_product<1, true, true>)
+                       : (a.out32 ? vfp::expert_product<1, true, true, true, true>
+                                  : vfp::expert_product<1, true, true, false, true>);
     return launch_product(kernel, a, f, int64_t(a.feat_tiles) * a.col_tiles * a.E, stream);
 }
 
