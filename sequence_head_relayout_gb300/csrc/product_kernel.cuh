@@ -72,7 +72,7 @@ struct ProductArgs {
     int32_t acc_stride, tmem_cols;
     int32_t a_slabs, b_slabs;     // operands with i contiguous: 64 i to a slab, a CTA's share
                                   // by one copy of so many; 0: a copy for each
-    int32_t bf16, gaps, vec, out32;
+    int32_t bf16, gaps, vec;
 };
 
 // ---- synchronisation -----------------------------------------------------------
@@ -352,7 +352,7 @@ struct Tile {
     int n;             // rows or columns of the product, a multiple of 16 CTAS
     int kblocks;
     int gap;           // rows to be written as zeros behind the tile
-    bool more;         // weights: a later part of the sum, added to what is stored
+    bool more;         // weights: a later part of the sum
 };
 
 // The CTA's (pair's) tiles, by all lanes of a warp together.  Rows form: the
@@ -373,7 +373,7 @@ struct Tiles {
     int count[4], begin[4];
     // weights form: the tile as a number within its expert
     int e, in, each;
-    int next_row0, next_valid;    // loaded a tile ahead
+    int next_offset, next_count;  // of the next tile's expert, loaded a tile ahead
     int slice = 0;                // SPLIT: this CTA's of a.split shares of the sums
     int row0, rest;               // what is left of the expert's rows (sums in parts)
     bool inside = false;
@@ -388,14 +388,20 @@ struct Tiles {
             each = a.feat_tiles * a.col_tiles;
             e = int(t) / each;
             in = int(t) - e * each;
-            segment(min(e, a.E - 1), next_row0, next_valid);
+            ahead();
         }
     }
 
+    __device__ __forceinline__ void ahead() {
+        const int expert = min(e, a.E - 1);
+        next_offset = a.offsets[expert];
+        next_count = a.counts[expert];
+    }
+
     // Rows of an expert that exist, whatever the plan says.
-    __device__ __forceinline__ void segment(int e, int &begin_, int &count_) const {
-        begin_ = min(max(a.offsets[e], 0), a.rows);
-        count_ = min(max(a.counts[e], 0), a.rows - begin_);
+    __device__ __forceinline__ void segment(int offset, int n, int &begin_, int &count_) const {
+        begin_ = min(max(offset, 0), a.rows);
+        count_ = min(max(n, 0), a.rows - begin_);
     }
 
     __device__ __forceinline__ int64_t tiles_of(int n) const {
@@ -427,8 +433,7 @@ struct Tiles {
             o.n = (min(a.tile_n, a.cols - o.c0) + multiple - 1) / multiple * multiple;
             o.gap = 0;
             o.more = false;
-            row0 = next_row0;
-            rest = next_valid;
+            segment(next_offset, next_count, row0, rest);
             if constexpr (SPLIT) {
                 // this CTA's share of the blocks
                 const int64_t n = parts(rest, kBlockK);
@@ -443,7 +448,7 @@ struct Tiles {
                 in -= each;
                 ++e;
             }
-            segment(min(e, a.E - 1), next_row0, next_valid);
+            ahead();
         }
         o.row0 = row0;
         o.valid = min(rest, a.part_rows);
@@ -464,7 +469,7 @@ struct Tiles {
             for (int i = 0; i < 4; ++i) {
                 const int e = base + 4 * lane + i;
                 count[i] = begin[i] = 0;
-                if (e < a.E) segment(e, begin[i], count[i]);
+                if (e < a.E) segment(a.offsets[e], a.counts[e], begin[i], count[i]);
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) sum += tiles_of(count[i]);
@@ -513,6 +518,18 @@ struct Tiles {
 };
 
 // ---- epilogue ------------------------------------------------------------------
+
+// The 16 bytes from byte `shift` (even) of lo and hi on.
+__device__ __forceinline__ uint4 shifted(const uint4 &lo, const uint4 &hi, int shift) {
+    uint32_t x[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+    for (int j = 0; j < 6; ++j) x[j] = shift & 8 ? x[j + 2] : x[j];
+#pragma unroll
+    for (int j = 0; j < 5; ++j) x[j] = shift & 4 ? x[j + 1] : x[j];
+    const int bits = shift & 2 ? 16 : 0;
+    return make_uint4(__funnelshift_r(x[0], x[1], bits), __funnelshift_r(x[1], x[2], bits),
+                      __funnelshift_r(x[2], x[3], bits), __funnelshift_r(x[3], x[4], bits));
+}
 
 __device__ __forceinline__ uint32_t round2(float lo, float hi, bool bf16) {
     if (bf16) {
@@ -570,72 +587,91 @@ __device__ __forceinline__ void zero_rows(const ProductArgs &a, int64_t row, int
             *reinterpret_cast<uint4 *>(out + (row + j) * a.feat + c) = make_uint4(0, 0, 0, 0);
 }
 
-// Weights form: v[c] is column c0 + c of feature f + lane of expert e.  `more`: it is
-// added to what this thread has stored there before.
-__device__ __forceinline__ void store_weights(const ProductArgs &a, const uint32_t (&v)[32],
-                                              int e, int f, int c0, int lane, bool more,
-                                              uint8_t *staging) {
-    const int64_t first = (int64_t(e) * a.feat + f) * a.cols + c0;
+// Weights form, float32: v[c] is column c0 + c of feature f + lane of expert e.  Through
+// rows of 144 bytes in shared memory (both sides without bank conflicts), so that 32
+// columns leave as 128 bytes.
+__device__ __forceinline__ void store_weights32(const ProductArgs &a, const uint32_t (&v)[32],
+                                                int e, int f, int c0, int lane,
+                                                uint8_t *staging) {
+    float *out = static_cast<float *>(a.out) + (int64_t(e) * a.feat + f) * a.cols + c0;
     const int rows = min(32, a.feat - f), cols = min(32, a.cols - c0);
-    if (a.out32) {
-        // rows of 144 bytes: both sides of the exchange without bank conflicts
-        float *out = static_cast<float *>(a.out) + first;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            *reinterpret_cast<uint4 *>(staging + lane * 144 + j * 16) =
-                make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-        __syncwarp();
-        if (a.vec) {
-            const int c = lane % 8 * 4;
-            float4 old[8];
+    for (int j = 0; j < 8; ++j)
+        *reinterpret_cast<uint4 *>(staging + lane * 144 + j * 16) =
+            make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+    __syncwarp();
+    if (a.vec) {
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                const int r = q * 4 + lane / 8;
-                old[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                if (more && r < rows && c < cols)
-                    old[q] = __ldcg(reinterpret_cast<const float4 *>(out + int64_t(r) * a.cols + c));
-            }
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                const int r = q * 4 + lane / 8;
-                float4 x = *reinterpret_cast<const float4 *>(staging + r * 144 + c * 4);
-                if (more) x = make_float4(old[q].x + x.x, old[q].y + x.y, old[q].z + x.z,
-                                          old[q].w + x.w);
-                if (r < rows && c < cols)
-                    *reinterpret_cast<float4 *>(out + int64_t(r) * a.cols + c) = x;
-            }
-        } else if (lane < cols) {
+        for (int q = 0; q < 8; ++q) {
+            const int r = q * 4 + lane / 8, c = lane % 8 * 4;
+            if (r < rows && c < cols)
+                *reinterpret_cast<uint4 *>(out + int64_t(r) * a.cols + c) =
+                    *reinterpret_cast<const uint4 *>(staging + r * 144 + c * 4);
+        }
+    } else if (lane < cols) {
 #pragma unroll 8
-            for (int r = 0; r < rows; ++r) {
-                const float x = *reinterpret_cast<const float *>(staging + r * 144 + lane * 4);
-                float *p = out + int64_t(r) * a.cols + lane;
-                *p = more ? __ldcg(p) + x : x;
+        for (int r = 0; r < rows; ++r)
+            out[int64_t(r) * a.cols + lane] =
+                *reinterpret_cast<const float *>(staging + r * 144 + lane * 4);
+    }
+    __syncwarp();
+}
+
+// The same for 16-bit results, 64 columns to 128 bytes, in two steps: half `h` of the
+// columns to shared memory, and both to the result.
+__device__ __forceinline__ void stage_weights16(const ProductArgs &a, const uint32_t (&v)[32],
+                                                int h, int lane, uint8_t *staging) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            w[i] = round2(__uint_as_float(v[8 * j + 2 * i]), __uint_as_float(v[8 * j + 2 * i + 1]),
+                          a.bf16);
+        *reinterpret_cast<uint4 *>(staging + lane * 144 + h * 64 + j * 16) =
+            make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+__device__ __forceinline__ void store_weights16(const ProductArgs &a, int e, int f, int c0,
+                                                int lane, uint8_t *staging) {
+    uint16_t *out = static_cast<uint16_t *>(a.out) + (int64_t(e) * a.feat + f) * a.cols + c0;
+    const int rows = min(32, a.feat - f), cols = min(64, a.cols - c0);
+    __syncwarp();
+    if (a.vec) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const int r = q * 4 + lane / 8, c = lane % 8 * 8;
+            if (r < rows && c < cols)
+                *reinterpret_cast<uint4 *>(out + int64_t(r) * a.cols + c) =
+                    *reinterpret_cast<const uint4 *>(staging + r * 144 + c * 2);
+        }
+    } else if (cols == 64) {
+        // each row in the 16-byte pieces that lie in it, and eight elements at its ends
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const int r = q * 4 + lane / 8, i = lane % 8;
+            uint16_t *const row = out + int64_t(r) * a.cols;
+            const int head = int(-(reinterpret_cast<uint64_t>(row) >> 1) & 7);
+            if (r >= rows) continue;
+            const uint4 lo = *reinterpret_cast<const uint4 *>(staging + r * 144 + i * 16);
+            if (head == 0) {
+                *reinterpret_cast<uint4 *>(row + i * 8) = lo;
+                continue;
             }
+            if (i < 7) {
+                const uint4 hi = *reinterpret_cast<const uint4 *>(staging + r * 144 + i * 16 + 16);
+                *reinterpret_cast<uint4 *>(row + head + i * 8) = shifted(lo, hi, head * 2);
+            }
+            const int c = i < head ? i : 56 + i;
+            row[c] = *reinterpret_cast<const uint16_t *>(staging + r * 144 + c * 2);
         }
     } else {
-        uint16_t *out = static_cast<uint16_t *>(a.out) + first;
-        uint32_t w[16];
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-            w[j] = round2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]), a.bf16);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<uint4 *>(staging + lane * 80 + j * 16) =
-                make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-        __syncwarp();
-        if (a.vec) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int r = q * 8 + lane / 4, c = lane % 4 * 8;
-                if (r < rows && c < cols)
-                    *reinterpret_cast<uint4 *>(out + int64_t(r) * a.cols + c) =
-                        *reinterpret_cast<const uint4 *>(staging + r * 80 + c * 2);
-            }
-        } else if (lane < cols) {
+        const uint16_t *const s = reinterpret_cast<const uint16_t *>(staging) + lane;
+        out += lane;
 #pragma unroll 8
-            for (int r = 0; r < rows; ++r)
-                out[int64_t(r) * a.cols + lane] =
-                    *reinterpret_cast<const uint16_t *>(staging + r * 80 + lane * 2);
+        for (int r = 0; r < rows; ++r) {
+            if (lane < cols) out[int64_t(r) * a.cols] = s[r * 72];
+            if (lane + 32 < cols) out[int64_t(r) * a.cols + 32] = s[r * 72 + 32];
         }
     }
     __syncwarp();
@@ -908,7 +944,7 @@ expert_product(const __grid_constant__ ProductArgs a) {
                               tiles.slice, i % a.split, failed, uint64_t(o.kblocks) * 8192, ok, v))
                         continue;
                 if (f >= a.feat) continue;
-                store_weights(a, v, o.e, f, o.c0 + c, lane, false, mine);
+                store_weights32(a, v, o.e, f, o.c0 + c, lane, mine);
             }
         }
     } else if (warp >= 4 && warp < 4 + kEpilogueWarps) {
@@ -930,24 +966,34 @@ expert_product(const __grid_constant__ ProductArgs a) {
             const int f = o.f0 + int(rank) * kTileM + quarter * 32;
             const uint32_t d = tmem + acc * uint32_t(a.acc_stride) + (uint32_t(quarter * 32) << 16);
             const int n = WEIGHTS ? min(o.n, a.cols - o.c0) : o.valid;
-            for (int c = 32 * turn; c < n; c += 64) {
-                uint32_t v[32];
-                if (o.kblocks > 0 && ok) {
-                    tmem_load(d + uint32_t(c), v);
-                } else {
-                    // an empty sum, or one that was given up: NaN
+            // 32 columns at a time; of the weights 64, which leave together
+            constexpr int kHalves = WEIGHTS ? 2 : 1, kCols = 32 * kHalves;
+            for (int c0 = kCols * turn; c0 < n; c0 += 2 * kCols) {
+                bool store = f < a.feat;             // all lanes alike
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = ok ? 0u : 0x7FC00000u;
+                for (int h = 0; h < kHalves; ++h) {
+                    const int c = c0 + 32 * h;
+                    uint32_t v[32];
+                    if (o.kblocks > 0 && ok && c < n) {
+                        tmem_load(d + uint32_t(c), v);
+                    } else {
+                        // an empty sum, or one that was given up: NaN
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = ok ? 0u : 0x7FC00000u;
+                    }
+                    if constexpr (SPLIT)
+                        if (!join(a, ctl, reinterpret_cast<float *>(part), turn, quarter, lane,
+                                  tiles.slice, c0 / 128 % a.split, failed,
+                                  uint64_t(o.kblocks) * 8192, ok, v))
+                            store = false;
+                    if constexpr (WEIGHTS) {
+                        if (store) stage_weights16(a, v, h, lane, mine);
+                    } else {
+                        if (store) store_rows(a, v, int64_t(o.row0) + c, n - c, f, lane, mine);
+                    }
                 }
-                if constexpr (SPLIT)
-                    if (!join(a, ctl, reinterpret_cast<float *>(part), turn, quarter, lane,
-                              tiles.slice, c / 64 % a.split, failed, uint64_t(o.kblocks) * 8192, ok, v))
-                        continue;
-                if (f >= a.feat) continue;           // all lanes alike
                 if constexpr (WEIGHTS)
-                    store_weights(a, v, o.e, f, o.c0 + c, lane, o.more, mine);
-                else
-                    store_rows(a, v, int64_t(o.row0) + c, n - c, f, lane, mine);
+                    if (store) store_weights16(a, o.e, f, o.c0 + c0, lane, mine);
             }
             if (o.kblocks > 0 && ok) {
                 fence_before();
@@ -1029,16 +1075,7 @@ pad_lines(const __grid_constant__ PadArgs a) {
                 if (a.s_el == 1) {
                     const uint4 lo = piece(a, at + 16 * c);
                     const uint4 hi = shift ? piece(a, at + 16 * c + 16) : lo;
-                    uint32_t x[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-#pragma unroll
-                    for (int j = 0; j < 6; ++j) x[j] = shift & 8 ? x[j + 2] : x[j];
-#pragma unroll
-                    for (int j = 0; j < 5; ++j) x[j] = shift & 4 ? x[j + 1] : x[j];
-                    const int bits = shift & 2 ? 16 : 0;
-                    v[u] = make_uint4(__funnelshift_r(x[0], x[1], bits),
-                                      __funnelshift_r(x[1], x[2], bits),
-                                      __funnelshift_r(x[2], x[3], bits),
-                                      __funnelshift_r(x[3], x[4], bits));
+                    v[u] = shifted(lo, hi, shift);
                 } else {
                     uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll

@@ -337,8 +337,13 @@ int make_row_map(CUtensorMap *map, bool bf16, const Operand &x, int64_t slabs) {
     return make_map(map, bf16, 4, x.p, dims, str, 64, 3, slabs);
 }
 
-// Pairs, unless half of a pair would have no feature to store, or they would leave half
-// of the SMs idle.  Tiles that are still few are made smaller, and the CTAs of a cluster
+// Pairs, unless half of a pair would have no feature to store, they would leave half of
+// the SMs idle, or experts have few rows: then a tile is mostly its stores, for which
+// the CTAs of a pair wait for each other (E = 64, N = 2,048, M = 1,024, bf16, us):
+//   rows             64    128    192    256    384    512   1,024
+//   pairs          76.1   83.9   90.4   97.1  109.8  122.5   198.9
+//   single CTAs    54.1   65.8   77.1   88.5  114.1  140.2   258.3
+// Tiles that are still few are made smaller, and the CTAs of a cluster
 // share their rows: N = M = 512, E = 2 with 27,707 rows each takes 199 us with
 // 16 tiles of 256 columns, 71 with four CTAs to each (102 with eight, whose clusters do
 // not all find room at once), 47 with 32 tiles of 128 columns and four CTAs to each.
@@ -346,7 +351,8 @@ int make_row_map(CUtensorMap *map, bool bf16, const Operand &x, int64_t slabs) {
 // 11.9 with two CTAs).
 Form weights_form(const vf_product_desc *d) {
     const int64_t columns = d->E * ceil_div(d->M, 256), features = ceil_div(d->N, vfp::kTileM);
-    if (features > 1 && 4 * columns * ceil_div(features, 2) > kSMs) return {2, 256, 0, true};
+    if (features > 1 && 4 * columns * ceil_div(features, 2) > kSMs && mean_rows(d) > 352)
+        return {2, 256, 0, true};
     const bool few = 4 * columns * features < kSMs;
     Form f = {1, few ? 128 : 256, 0, true};
     const int64_t tiles = d->E * ceil_div(d->M, f.tile_n) * features;
@@ -379,14 +385,14 @@ int weight_grad(const vf_product_desc *d, cudaStream_t stream) {
     vfp::ProductArgs a = make_args(d);
     a.cols = int32_t(d->M);
     a.out = d->grad_weights;
-    a.out32 = d->out_type == VF_TYPE_F32;
+    const bool out32 = d->out_type == VF_TYPE_F32;
     // The tensor cores cut off what lies below an accumulator's last bit, always towards
     // the same side, so that a sum's error grows with its length: 1.2e-6 of the result
     // at 1,024 rows.  Sums in float32 are therefore taken in parts, which are added with
     // rounding: some 7e-7 whatever the length.  T = 4,096, K = 8, E = 32, N = 4,096,
     // M = 2,048 takes 384 us in one part, 397 in parts of 768 rows, 415 in parts of 512.
     // (The 16-bit types round a thousand times as coarsely.)
-    a.part_rows = a.out32 ? 768 : INT32_MAX;
+    a.part_rows = out32 ? 768 : INT32_MAX;
     a.vec = d->M % (16 / size) == 0 && aligned16(d->grad_weights);
     const Form f = weights_form(d);
     set_form(&a, f);
@@ -403,11 +409,11 @@ int weight_grad(const vf_product_desc *d, cudaStream_t stream) {
             return rc;
     }
     const Kernel kernel =
-        f.ctas == 2    ? (a.out32 ? vfp::expert_product<2, true, true, true>
+        f.ctas == 2    ? (out32 ? vfp::expert_product<2, true, true, true>
                                   : vfp::expert_product<2, true, true>)
-        : f.split == 1 ? (a.out32 ? vfp::expert_product<1, true, true, true>
+        : f.split == 1 ? (out32 ? vfp::expert_product<1, true, true, true>
                                   : vfp::expert_product<1, true, true>)
-                       : (a.out32 ? vfp::expert_product<1, true, true, true, true>
+                       : (out32 ? vfp::expert_product<1, true, true, true, true>
                                   : vfp::expert_product<1, true, true, false, true>);
     return launch_product(kernel, a, f, int64_t(a.feat_tiles) * a.col_tiles * a.E, stream);
 }
