@@ -1032,6 +1032,7 @@ struct PadArgs {
     int64_t s_outer, s_line, s_el;
     uint16_t *dst;
     int64_t outer, lines, len, pitch;
+    int64_t step_outer, step_lines;      // the grid's warps, in outer items and the rest
     const int32_t *counts;        // [outer], or null
     const int32_t *limit;         // null: all lines
 };
@@ -1052,31 +1053,42 @@ __device__ __forceinline__ uint4 piece(const PadArgs &a, uint64_t at) {
 
 __global__ void __launch_bounds__(256)
 pad_lines(const __grid_constant__ PadArgs a) {
+    constexpr int U = 4;                                   // pieces of a lane in flight
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = int(threadIdx.x & 31);
-    const int64_t warps = int64_t(gridDim.x) * (blockDim.x / 32);
     const int64_t limit = a.limit ? min(int64_t(max(*a.limit, 0)), a.lines) : a.lines;
     const int64_t chunks = (a.len + 7) / 8;
-    for (int64_t i = int64_t(blockIdx.x) * (blockDim.x / 32) + (threadIdx.x >> 5);
-         i < a.outer * a.lines; i += warps) {
-        const int64_t e = i / a.lines, l = i - e * a.lines;
+    const int64_t first = int64_t(blockIdx.x) * (blockDim.x / 32) + (threadIdx.x >> 5);
+    int64_t e = first / a.lines, l = first - e * a.lines;
+    for (; e < a.outer; e += a.step_outer, l += a.step_lines) {
+        if (l >= a.lines) {
+            l -= a.lines;
+            if (++e >= a.outer) break;
+        }
         if (l >= limit || (a.counts && a.counts[e] <= 0)) continue;
         const uint16_t *const p = a.src + e * a.s_outer + l * a.s_line;
-        uint4 *const to = reinterpret_cast<uint4 *>(a.dst + i * a.pitch);
+        uint4 *const to = reinterpret_cast<uint4 *>(a.dst + (e * a.lines + l) * a.pitch);
         const int shift = int(reinterpret_cast<uint64_t>(p) & 15);
         const uint64_t at = reinterpret_cast<uint64_t>(p) - shift;
-        for (int64_t c0 = 0; c0 < chunks; c0 += 64) {
-            uint4 v[2];
+        for (int64_t c0 = 0; c0 < chunks; c0 += 32 * U) {
+            uint4 v[U];
+            if (a.s_el == 1) {
+                uint4 hi[U];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int64_t c = c0 + u * 32 + lane;
-                if (c >= chunks) continue;
-                if (a.s_el == 1) {
-                    const uint4 lo = piece(a, at + 16 * c);
-                    const uint4 hi = shift ? piece(a, at + 16 * c + 16) : lo;
-                    v[u] = shifted(lo, hi, shift);
-                } else {
+                for (int u = 0; u < U; ++u) {
+                    const int64_t c = c0 + u * 32 + lane;
+                    v[u] = hi[u] = make_uint4(0, 0, 0, 0);
+                    if (c >= chunks) continue;
+                    v[u] = piece(a, at + 16 * c);
+                    if (shift) hi[u] = piece(a, at + 16 * c + 16);
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) v[u] = shifted(v[u], hi[u], shift);
+            } else {
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int64_t c = c0 + u * 32 + lane;
                     uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
@@ -1086,7 +1098,7 @@ pad_lines(const __grid_constant__ PadArgs a) {
                 }
             }
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+            for (int u = 0; u < U; ++u)
                 if (c0 + u * 32 + lane < chunks) to[c0 + u * 32 + lane] = v[u];
         }
     }

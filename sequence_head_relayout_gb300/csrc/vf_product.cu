@@ -226,8 +226,10 @@ struct Operand {
         s_line = a.pitch;
         s_outer = lines * a.pitch;
         s_el = 1;
-        return launch(vfp::pad_lines, std::min(ceil_div(outer * lines, 8), kSMs * 8), 256, 0,
-                      stream, a);
+        const int64_t blocks = std::min(ceil_div(outer * lines, 8), kSMs * 8);
+        a.step_outer = blocks * 8 / lines;
+        a.step_lines = blocks * 8 % lines;
+        return launch(vfp::pad_lines, blocks, 256, 0, stream, a);
     }
 };
 
