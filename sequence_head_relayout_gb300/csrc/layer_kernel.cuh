@@ -14,7 +14,7 @@
 //   norm           T = 55,414, M = 3,584, bf16, with a residual  227 us   7.0 TB/s
 //   norm to E4M3   the same                                      227 us   6.1 TB/s
 //   norm backward  T = 55,413, M = 2,048, fp32, with grad_total  268 us   6.8 TB/s
-//                  T = 55,414, M = 3,584, bf16, with grad_total  296 us   5.4 TB/s
+//                  T = 55,414, M = 3,584, bf16, with grad_total  288 us   5.5 TB/s
 #pragma once
 
 #include <cstdint>
@@ -227,7 +227,7 @@ struct NormArgs {
     int32_t warps;                // warps of a row
     int32_t group, groups;        // columns to a scale, scales of a row
     float eps, inv_m;             // 1 / M
-    int32_t blocks, stages;
+    int32_t blocks;
 };
 
 template <class E, int VW>
@@ -512,10 +512,16 @@ __device__ __forceinline__ float2 row_sums(float u, float v, float2 (*parts)[32]
     return s;
 }
 
+// Rows of a group of warps in shared memory, one of them worked on.  (With three, fewer
+// blocks fit an SM: 318 us for 288 at T = 55,414, M = 3,584.)
+constexpr int kNormStages = 2;
+
+__host__ __device__ constexpr bool copies_rows(int size, int vw, int nv) {
+    return size == 2 && vw > 1 && nv <= 2;  // with four units to a lane they do not fit
+}
+
 // A unit of global memory to shared memory, behind the thread's back; the hardware
 // has such copies from 4 bytes on.
-__host__ __device__ constexpr bool copies_rows(int size, int vw) { return size == 2 && vw > 1; }
-
 template <class S, int VW>
 __device__ __forceinline__ void copy_unit(Unit<S, VW> *to, const S *from) {
     constexpr int bytes = int(sizeof(Unit<S, VW>));
@@ -539,7 +545,7 @@ __device__ __forceinline__ void wait_copies() {
 // is the bytes in flight.  Rows of 16-bit elements are copied to shared memory (a
 // thread's units to places that no other thread touches), a row ahead of the one that
 // is worked on; their values take too many registers for enough of them to be
-// loaded at a time (bf16, T = 55,414, M = 3,584, with grad_total: 280 us, 335 with the
+// loaded at a time (bf16, T = 55,414, M = 3,584, with grad_total: 288 us, 335 with the
 // rows in registers).  Rows of float32 stay in registers (T = 55,413, M = 2,048: 271
 // us, 314 through shared memory).
 template <class E, int VW, int NV>
@@ -547,9 +553,9 @@ __global__ void __launch_bounds__(512, NV <= 2 ? 2 : 1)
 norm_backward_rows(const __grid_constant__ NormArgs a) {
     using S = typename E::S;
     using U = Unit<S, VW>;
-    constexpr bool kCopies = copies_rows(int(sizeof(S)), VW);
+    constexpr bool kCopies = copies_rows(int(sizeof(S)), VW, NV);
     __shared__ float2 parts[2][32];
-    extern __shared__ uint4 dynamic[];     // [stages][h, g, more][NV][threads] units
+    extern __shared__ uint4 dynamic[];     // [kNormStages][h, g, more][NV][threads] units
     wait_for_previous_grid();
     const int lane = int(threadIdx.x & 31), warp = int(threadIdx.x >> 5);
     const int part = warp % a.warps, rows = int(blockDim.x / 32 / a.warps);
@@ -571,10 +577,11 @@ norm_backward_rows(const __grid_constant__ NormArgs a) {
     };
     const int64_t ahead = int64_t(gridDim.x) * rows;
     int64_t t = int64_t(blockIdx.x) * rows + warp / a.warps;
-    if constexpr (kCopies) fetch(t, ring);
-    int turn = 0;
+    if constexpr (kCopies)
+        for (int i = 0; i < kNormStages - 1; ++i) fetch(t + i * ahead, ring + i * 3 * NV * step);
+    int turn = 0, stage = 0;
     for (int64_t t0 = int64_t(blockIdx.x) * rows; t0 < a.T; t0 += ahead, t += ahead) {
-        U *const here = ring + turn * 3 * NV * step;
+        U *const here = ring + stage * 3 * NV * step;
         U held[3][NV];
         if constexpr (!kCopies) {
 #pragma unroll
@@ -587,11 +594,11 @@ norm_backward_rows(const __grid_constant__ NormArgs a) {
                     if (a.grad_total.p) held[2][j].load(a.grad_total.unit<const S, VW>(t, unit));
                 }
             }
-        } else if (a.stages > 1) {
-            fetch(t + ahead, ring + (turn ^ 1) * 3 * NV * step);
-            wait_copies<1>();
         } else {
-            wait_copies<0>();
+            // the stage that was read last time takes the row that comes last
+            const int free = stage == 0 ? kNormStages - 1 : stage - 1;
+            fetch(t + (kNormStages - 1) * ahead, ring + free * 3 * NV * step);
+            wait_copies<kNormStages - 1>();
         }
         const auto row = [&](int which, int j) {
             if constexpr (kCopies) return here[(which * NV + j) * step];
@@ -631,6 +638,7 @@ norm_backward_rows(const __grid_constant__ NormArgs a) {
             round_unit<E, VW>(m).store(a.grad_x.unit<S, VW>(t, unit));
         }
         turn ^= 1;
+        if (++stage == kNormStages) stage = 0;
     }
     if constexpr (kCopies) wait_copies<0>();
     __syncthreads();                                       // the ring's memory is free
@@ -701,17 +709,24 @@ norm_backward_any(const __grid_constant__ NormArgs a) {
 }
 
 // The weight's gradient: the blocks' shares, summed in a fixed order.  A block takes
-// 32 columns, its warps every 32nd share.
+// 32 columns, its warps every 32nd share, all of whose loads are issued at once (608
+// shares of 2,048 columns: 8.4 us with four at a time).
+constexpr int kNormBlocks = 608;                           // most blocks of the pass before
+
 __global__ void __launch_bounds__(1024)
 norm_weight_grad(const __grid_constant__ NormArgs a) {
     __shared__ float sums[32][33];
     wait_for_previous_grid();
     const int lane = int(threadIdx.x & 31), warp = int(threadIdx.x >> 5);
     const int64_t c = int64_t(blockIdx.x) * 32 + lane;
-    float v = 0.0f;
-    if (c < a.M)
-#pragma unroll 4
-        for (int b = warp; b < a.blocks; b += 32) v += a.partial[int64_t(b) * a.M + c];
+    float share[kNormBlocks / 32], v = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kNormBlocks / 32; ++i) {
+        const int b = warp + 32 * i;
+        share[i] = c < a.M && b < a.blocks ? a.partial[int64_t(b) * a.M + c] : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < kNormBlocks / 32; ++i) v += share[i];
     sums[warp][lane] = v;
     __syncthreads();
     if (warp > 0 || c >= a.M) return;

@@ -136,11 +136,12 @@ int glu(const vf_glu_desc *d, bool backward, cudaStream_t stream) {
 
 constexpr int64_t kNormColumns = int64_t(1) << 24;         // M
 
-// The most that the backward pass takes: two stages of three rows, four units of 16
-// bytes to each of 512 threads.
-constexpr int kNormShared = 2 * 3 * 4 * 16 * 512;
+// The most that the backward pass takes: stages of three rows, two units of 16 bytes to
+// each of 512 threads.
+constexpr int kNormShared = vf::kNormStages * 3 * 2 * 16 * 512;
 
-int64_t norm_blocks(int64_t T) { return std::min<int64_t>(T, kSMs * 4); }
+int64_t norm_blocks(int64_t T) { return std::min<int64_t>(T, vf::kNormBlocks); }
+static_assert(vf::kNormBlocks == kSMs * 4, "four blocks to an SM");
 
 using NormKernel = void (*)(vf::NormArgs);
 
@@ -361,14 +362,16 @@ int norm_backward(const vf_norm_desc *d, cudaStream_t stream) {
                 d->type == VF_TYPE_BF16  ? backward_kernel<vf::Bf16>(w.vw, s.nv)
                 : d->type == VF_TYPE_F16 ? backward_kernel<vf::F16>(w.vw, s.nv)
                                          : backward_kernel<vf::F32>(w.vw, s.nv);
-            // shared memory: two rows to a group of warps where there are two to walk;
-            // the block's sums (s.rows > 1 has at most 2 units to a lane)
-            a.stages = ceil_div(T, s.rows) > a.blocks ? 2 : 1;
+            // shared memory: the rows to come, and the block's sums (s.rows > 1 has at
+            // most 2 units to a lane); as many blocks as fit an SM
             const int64_t threads = s.warps * s.rows * 32;
-            const bool copies = vf::copies_rows(int(size), int(w.vw));
+            const bool copies = vf::copies_rows(int(size), int(w.vw), int(s.nv));
             const size_t smem = size_t(
-                std::max(copies ? a.stages * 3 * s.nv * threads * w.vw * size : 0,
+                std::max(copies ? vf::kNormStages * 3 * s.nv * threads * w.vw * size : 0,
                          s.rows > 1 ? M * 4 : 0));
+            const int64_t resident =
+                std::max<int64_t>(1, std::min<int64_t>(4, 220 * 1024 / std::max<int64_t>(1, smem)));
+            a.blocks = int32_t(std::min<int64_t>(a.blocks, kSMs * resident));
             if (smem > 47 * 1024 &&
                 cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      kNormShared) != cudaSuccess) {
