@@ -347,7 +347,7 @@ __device__ __forceinline__ int parts(int n, int d) { return n / d + (n % d != 0)
 
 struct Tile {
     int e, f0;         // expert, first feature
-    int row0, valid;   // rows: first row and rows of the tile; weights: of the expert
+    int row0, valid;   // first row and rows of the tile; weights: of this part of the sum
     int c0;            // weights: first column
     int n;             // rows or columns of the product, a multiple of 16 CTAS
     int kblocks;
@@ -679,7 +679,6 @@ __device__ __forceinline__ void store_weights16(const ProductArgs &a, int e, int
 
 // ---- the kernel ----------------------------------------------------------------
 
-
 struct Control {
     uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2];
     uint64_t part_full[2], part_empty[2];   // SPLIT, for each turn of the epilogue
@@ -812,8 +811,8 @@ expert_product(const __grid_constant__ ProductArgs a) {
             // rows form: one copy, as high as the tile needs
             const int boxes = WEIGHTS ? slabs : (half + a.box - 1) / a.box;
             const CUtensorMap *const b_map = &a.b_maps[WEIGHTS ? 0 : boxes - 1];
-            const uint32_t bytes = uint32_t(
-                CTAS * (kStageA + (WEIGHTS ? (a.b_slabs ? a.b_slabs : slabs) * 64 : boxes * a.box) * 128));
+            const int copied = WEIGHTS ? (a.b_slabs ? a.b_slabs : slabs) * 64 : boxes * a.box;
+            const uint32_t bytes = uint32_t(CTAS * (kStageA + copied * 128));
             const int fa = o.f0 + int(rank) * kTileM, cb = o.c0 + int(rank) * half;
             for (int kb = 0; kb < o.kblocks; ++kb) {
                 ok = warp_wait(empty + s * 8, phase ^ 1, failed);
@@ -890,7 +889,7 @@ expert_product(const __grid_constant__ ProductArgs a) {
             if (ok && one) mma_commit<CTAS>(smem_addr(&ctl.acc_full[acc]));
             ++it;
         }
-    } else if (PARTS && warp >= 4 && warp < 4 + kEpilogueWarps) {
+    } else if (PARTS && warp >= 4) {
         const int quarter = warp % 4, turn = (warp - 4) / 4;
         uint8_t *const mine = staging + (warp - 4) * kStagingBytes;
         uint32_t it = 0;
@@ -947,7 +946,7 @@ expert_product(const __grid_constant__ ProductArgs a) {
                 store_weights32(a, v, o.e, f, o.c0 + c, lane, mine);
             }
         }
-    } else if (warp >= 4 && warp < 4 + kEpilogueWarps) {
+    } else if (warp >= 4) {
         const int quarter = warp % 4, turn = (warp - 4) / 4;
         uint8_t *const mine = staging + (warp - 4) * kStagingBytes;
         uint32_t it = 0;

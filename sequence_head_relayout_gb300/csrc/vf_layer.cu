@@ -123,13 +123,11 @@ int glu(const vf_glu_desc *d, bool backward, cudaStream_t stream) {
     a.col_blocks = int32_t(ceil_div(a.units, bx));
     const int64_t row_blocks =
         std::min(ceil_div(d->rows, 2 * by), std::max<int64_t>(1, kSMs * 32 / a.col_blocks));
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(row_blocks * a.col_blocks), 1, 1);
-    cfg.blockDim = dim3(unsigned(bx), unsigned(by), 1);
     auto *kernel = d->type == VF_TYPE_BF16  ? glu_kernel<vf::Bf16>(backward, w.vw)
                    : d->type == VF_TYPE_F16 ? glu_kernel<vf::F16>(backward, w.vw)
                                             : glu_kernel<vf::F32>(backward, w.vw);
-    return launch(kernel, cfg.gridDim, cfg.blockDim, 0, stream, a);
+    return launch(kernel, dim3(unsigned(row_blocks * a.col_blocks)),
+                  dim3(unsigned(bx), unsigned(by)), 0, stream, a);
 }
 
 // ---------------------------------------------------------------- norm

@@ -134,7 +134,8 @@ int launch_product(Kernel kernel, vfp::ProductArgs &a, const Form &f, int64_t ti
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(groups * ctas), 1, 1);
     cfg.blockDim = dim3(vfp::kThreads, 1, 1);
-    cfg.dynamicSmemBytes = size_t(vfp::shared_bytes(f.weights, f.split > 1, a.stages, a.stage_bytes));
+    cfg.dynamicSmemBytes =
+        size_t(vfp::shared_bytes(f.weights, f.split > 1, a.stages, a.stage_bytes));
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

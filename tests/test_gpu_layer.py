@@ -154,7 +154,8 @@ def test_glu_differences():
     g, u, d = (rows_of(plan, 40, F32, i) for i in range(3))
     dg, du = vf.expert_glu_backward(d.to(DEV), g.to(DEV), u.to(DEV), plan)
     h = 1e-5
-    for got, f in ((dg, lambda e: L.glu(g.double() + e, u)), (du, lambda e: L.glu(g, u.double() + e))):
+    for got, f in ((dg, lambda e: L.glu(g.double() + e, u)),
+                   (du, lambda e: L.glu(g, u.double() + e))):
         want = d.double() * (f(h) - f(-h)) / (2 * h)
         # h^2 / 6 times the third derivative, at most 1 here, and float64's 2^-52 / h
         assert (got.cpu().double() - want).abs().max() < 1e-5

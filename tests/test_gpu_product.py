@@ -94,13 +94,15 @@ def make(T, K, E, align, how="mixed", seed=0):
 SHAPES = [
     # T, K, E, align, N, M
     (1, 1, 1, 1, 1, 1), (1, 8, 16, 1, 128, 64), (1, 8, 16, 128, 256, 128), (3, 2, 4, 1, 8, 8),
-    (16, 4, 8, 16, 136, 72), (33, 3, 7, 5, 65, 63), (40, 2, 3, 1, 127, 200), (64, 8, 5, 8, 264, 264),
-    (100, 4, 130, 1, 72, 136), (257, 2, 3, 128, 384, 320), (300, 1, 2, 1, 129, 65),
-    (700, 2, 3, 1, 256, 512), (1000, 2, 300, 4, 40, 96), (1500, 1, 1, 1, 520, 88),
-    (5, 1, 4096, 1, 16, 24), (90, 2, 3, 1, 64, 320), (1600, 1, 2, 1, 128, 192), (2000, 1, 1, 8, 192, 328),
-    (1, 2, 4, 1, 200, 4096), (20, 1, 2, 16, 130, 2500), (2, 1, 3, 1, 4096, 72), (60, 1, 2, 1, 513, 1030),
-    (5000, 1, 1, 1, 72, 200), (6000, 1, 2, 8, 300, 130), (3000, 1, 3, 1, 256, 264), (14000, 1, 1, 1, 40, 100),
-    (30000, 1, 2, 1, 130, 64), (9, 1, 2, 1, 1, 512), (9, 1, 2, 1, 512, 1), (50, 2, 4, 1, 24, 1000),
+    (16, 4, 8, 16, 136, 72), (33, 3, 7, 5, 65, 63), (40, 2, 3, 1, 127, 200),
+    (64, 8, 5, 8, 264, 264), (100, 4, 130, 1, 72, 136), (257, 2, 3, 128, 384, 320),
+    (300, 1, 2, 1, 129, 65), (700, 2, 3, 1, 256, 512), (1000, 2, 300, 4, 40, 96),
+    (1500, 1, 1, 1, 520, 88), (5, 1, 4096, 1, 16, 24), (90, 2, 3, 1, 64, 320),
+    (1600, 1, 2, 1, 128, 192), (2000, 1, 1, 8, 192, 328), (1, 2, 4, 1, 200, 4096),
+    (20, 1, 2, 16, 130, 2500), (2, 1, 3, 1, 4096, 72), (60, 1, 2, 1, 513, 1030),
+    (5000, 1, 1, 1, 72, 200), (6000, 1, 2, 8, 300, 130), (3000, 1, 3, 1, 256, 264),
+    (14000, 1, 1, 1, 40, 100), (30000, 1, 2, 1, 130, 64), (9, 1, 2, 1, 1, 512),
+    (9, 1, 2, 1, 512, 1), (50, 2, 4, 1, 24, 1000),
 ]
 
 
