@@ -23,11 +23,11 @@
 // which the weights are read once.  Measured on GB300 (bf16, device time after a pause;
 // under the power cap long products take a fifth longer, as cuBLAS's do):
 //   rows     T = 55,414, K = 2, E = 16, 3,584 to 4,096   1,630 us   1.92 PFLOP/s
-//   rows     T = 4,096, K = 8, E = 64, 4,096 to 2,048      355 us   1.49 PFLOP/s
+//   rows     T = 4,096, K = 8, E = 64, 4,096 to 2,048      339 us   1.56 PFLOP/s
 //   rows     T = 64, K = 4, E = 64, 2,048 to 3,584         135 us   7.0 TB/s
 //   rows     T = 1, K = 8, E = 128, 4,096 to 2,048          24 us   5.6 TB/s
-//   weights  T = 4,096, K = 8, E = 32, 4,096 x 2,048       325 us   1.69 PFLOP/s
-//                                    in float32            397 us   1.38 PFLOP/s
+//   weights  T = 4,096, K = 8, E = 32, 4,096 x 2,048       321 us   1.71 PFLOP/s
+//                                    in float32            391 us   1.41 PFLOP/s
 //
 // No wait is without an end: a role that waits for kWaitNs gives up, sets the
 // CTA's flag, and what is still to be stored is stored as NaN.
