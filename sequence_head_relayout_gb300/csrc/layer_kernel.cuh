@@ -20,6 +20,7 @@
 #include <cstdint>
 
 #include "expert_kernel.cuh"
+#include "shift.cuh"
 
 namespace vf {
 
@@ -81,6 +82,168 @@ struct View {
         return at<S>(r, u);
     }
 };
+
+// ---- rows at any address -----------------------------------------------------------
+//
+// Rows of odd lengths start at any multiple of their elements' size.  They are read in the
+// 16-byte pieces that they lie in.  Where a row's first or last piece reaches out of the view
+// (in its first and last row at most, but for views that repeat a row) elements are
+// read one by one.  There are two ways to take them:
+// * A lane's unit is a piece, with head = the elements in front of the row in its first
+//   one: unit u has columns u VW - head and on.  All views of a call have to lie alike; the
+//   weight is shifted to them.  This costs next to nothing.
+// * A lane's unit is columns u VW and on (the codes' groups are columns): it shifts together
+//   the two pieces that its unit lies in, the second of which is the next lane's first, and
+//   stores the piece that its unit and the one of the lane before it fill.
+
+// Bytes from .. to - 1 (both even) at p, zeros for the others of the 16.
+__device__ __noinline__ uint4 load_some(uint64_t p, int from, int to) {
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (2 * j >= from && 2 * j < to)
+            w[j / 2] |= uint32_t(*reinterpret_cast<const uint16_t *>(p + 2 * j)) << (j % 2 * 16);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// A row in its pieces: piece u is at start + 16 u, its bytes of the row end at span.
+struct PieceRow {
+    uint64_t start;
+    int head, span;               // bytes in front of the row; behind its end, from the start on
+    bool inside;                  // all pieces lie in the view
+
+    __device__ __forceinline__ PieceRow() {}
+    template <class S>
+    __device__ __forceinline__ PieceRow(const View &v, int64_t r, int64_t rows, int m, S) {
+        const uint64_t at = reinterpret_cast<uint64_t>(v.at<S>(r, 0));
+        head = int(at & 15);
+        start = at - uint64_t(head);
+        span = head + m * int(sizeof(S));
+        inside = start >= reinterpret_cast<uint64_t>(v.p) &&
+                 start + uint64_t((span + 15) & ~15) <=
+                     reinterpret_cast<uint64_t>(v.at<S>(rows - 1, 0)) + uint64_t(span - head);
+    }
+
+    // The row's bytes of piece u are from .. to - 1; whether those of the 32 pieces from u on
+    // are whole.
+    __device__ __forceinline__ int from(int u) const { return u == 0 ? head : 0; }
+    __device__ __forceinline__ int to(int u) const { return min(max(span - 16 * u, 0), 16); }
+    __device__ __forceinline__ bool whole(int u) const {
+        return (u > 0 || head == 0) && 16 * (u + 32) <= span;
+    }
+    // Piece u; of a piece outside the row zeros.
+    __device__ __forceinline__ uint4 load(int u) const {
+        if (!inside) return load_slow(u);
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (16 * u < span) v = *reinterpret_cast<const uint4 *>(start + int64_t(16 * u));
+        return v;
+    }
+    __device__ __forceinline__ uint4 load_slow(int u) const {
+        return load_some(start + int64_t(16 * u), from(u), to(u));
+    }
+};
+
+// The two pieces of a unit of columns.
+struct Pieces {
+    uint4 lo, hi;
+
+    __device__ __forceinline__ void load(const PieceRow &r, int unit) {
+        lo = r.load(unit);
+        hi = r.load(unit + 1);
+    }
+};
+
+// Bytes from .. to - 1 (both even) of v, zeros for the others.
+__device__ __forceinline__ uint4 some_bytes(const uint4 &v, int from, int to) {
+    const auto word = [&](uint32_t w, int i) {
+        const uint32_t lo = 4 * i >= from && 4 * i < to ? 0xFFFFu : 0u;
+        const uint32_t hi = 4 * i + 2 >= from && 4 * i + 2 < to ? 0xFFFF0000u : 0u;
+        return w & (lo | hi);
+    };
+    return make_uint4(word(v.x, 0), word(v.y, 1), word(v.z, 2), word(v.w, 3));
+}
+
+// The unit; zeros behind the row's end.
+__device__ __forceinline__ uint4 join_pieces(const PieceRow &r, int unit, const uint4 &lo,
+                                             const uint4 &hi) {
+    const uint4 v = shifted(lo, hi, r.head);
+    const int left = r.span - r.head - 16 * unit;
+    return left >= 16 ? v : some_bytes(v, 0, max(left, 0));
+}
+
+// Bytes from .. to - 1 of v (even) to p + from and on.
+__device__ __forceinline__ void store_some(uint64_t p, const uint4 &v, int from, int to) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (2 * j >= from && 2 * j < to)
+            *reinterpret_cast<uint16_t *>(p + 2 * j) = uint16_t(w[j / 2] >> (j % 2 * 16));
+}
+__device__ __forceinline__ void store_some(uint64_t p, uint64_t v, int from, int to) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (j >= from && j < to) *reinterpret_cast<uint8_t *>(p + j) = uint8_t(v >> (8 * j));
+}
+
+// Stores a row's first or last piece (from and to even): what is next to a multiple of 16
+// bytes leaves in 8, 4 and 2 bytes.
+__device__ __noinline__ void store_part(uint64_t p, uint4 v, int from, int to) {
+    const bool back = from > 0;
+    const int n = to - from;
+    if (back && to < 16) {
+        store_some(p, v, from, to);
+        return;
+    }
+    if (n == 16) {
+        *reinterpret_cast<uint4 *>(p) = v;
+        return;
+    }
+    const auto word = [&](int i) { return i & 2 ? (i & 1 ? v.w : v.z) : i & 1 ? v.y : v.x; };
+    const int at4 = back ? 12 - (n & 8) : n & 8, at2 = back ? 14 - (n & 12) : n & 12;
+    if (n & 8)
+        *reinterpret_cast<uint2 *>(p + (back ? 8 : 0)) =
+            back ? make_uint2(v.z, v.w) : make_uint2(v.x, v.y);
+    if (n & 4) *reinterpret_cast<uint32_t *>(p + at4) = word(at4 / 4);
+    if (n & 2)
+        *reinterpret_cast<uint16_t *>(p + at2) = uint16_t(word(at2 / 4) >> (at2 & 2 ? 16 : 0));
+}
+
+// The 8 bytes from byte `shift` (1 to 7) of lo and hi on.
+__device__ __forceinline__ uint64_t shifted(uint64_t lo, uint64_t hi, int shift) {
+    return lo >> (8 * shift) | hi << (64 - 8 * shift);
+}
+// The value of the lane before.
+__device__ __forceinline__ uint4 from_before(const uint4 &v) {
+    return make_uint4(__shfl_up_sync(kAll, v.x, 1), __shfl_up_sync(kAll, v.y, 1),
+                      __shfl_up_sync(kAll, v.z, 1), __shfl_up_sync(kAll, v.w, 1));
+}
+__device__ __forceinline__ uint64_t from_before(uint64_t v) {
+    return __shfl_up_sync(kAll, static_cast<unsigned long long>(v), 1);
+}
+
+// Stores a warp's units of a row of `bytes`, unit + 1 in the next lane; by all lanes of the
+// warp, those with units behind the row's end too.  P: uint4 (16 bytes) or uint64_t.
+template <class P>
+__device__ __forceinline__ void store_shifted(void *row, int unit, int64_t bytes, const P &v,
+                                              int lane) {
+    constexpr int N = int(sizeof(P));
+    const uint64_t p = reinterpret_cast<uint64_t>(row) + uint64_t(unit) * N;
+    const int64_t left = bytes - int64_t(unit) * N;
+    const int n = int(min(max(left, int64_t(0)), int64_t(N)));
+    const int next = lane < 31 ? int(min(max(left - N, int64_t(0)), int64_t(N))) : 0;
+    const int shift = int(p & (N - 1));                    // the same in all lanes
+    if (shift == 0) {
+        if (n == N) *reinterpret_cast<P *>(p) = v;
+        else store_some(p, v, 0, n);
+        return;
+    }
+    const P before = from_before(v);
+    const bool whole = lane > 0 && n + shift >= N, after = next + shift >= N;
+    if (whole) *reinterpret_cast<P *>(p - shift) = shifted(before, v, N - shift);
+    if (!whole || !after) store_some(p, v, whole ? N - shift : 0, after ? N - shift : n);
+}
+
+// ---- arithmetic --------------------------------------------------------------------
 
 // VW float32 operations, two to an instruction where there are two: a * b, and
 // a * b + c rounded once.  b may be one value for all.
@@ -222,7 +385,7 @@ struct NormArgs {
     float *partial;               // backward: [blocks][M]
     float *grad_weight;
     int64_t T;
-    int32_t M, units;             // units: M / VW
+    int32_t M, units;             // units: of VW elements in a row
     int32_t weight32;             // the weight is float32
     int32_t warps;                // warps of a row
     int32_t group, groups;        // columns to a scale, scales of a row
@@ -247,6 +410,54 @@ __device__ __forceinline__ void load_weight(const NormArgs &a, int64_t c, float 
     } else {
         Unit<typename E::S, VW> u;
         u.load(static_cast<const typename E::S *>(a.weight) + c);
+        widen_unit<E, VW>(u, w);
+    }
+}
+
+// The weight from any column c on, zeros outside it, where it starts at a multiple of 16 bytes.
+// All lanes of a warp are here.
+template <class E, int VW>
+__device__ __forceinline__ void load_weight_at(const NormArgs &a, int c, float (&w)[VW]) {
+    using S = typename E::S;
+    const int each = a.weight32 ? 4 : 16 / int(sizeof(S));
+    const int c0 = c & -each, o = c & (each - 1);
+    const uint4 *const p = static_cast<const uint4 *>(a.weight) + (a.weight32 ? c0 >> 2 : c0 / VW);
+    if (a.weight32) {
+        constexpr int N = VW / 4 + 1;
+        float f[4 * N];
+        if (__all_sync(kAll, c >= 0 && c0 + 4 * N <= a.M)) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const uint4 v = p[i];
+                memcpy(f + 4 * i, &v, 16);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4 * N; ++i) {
+                f[i] = 0.0f;
+                if (c0 + i >= 0 && c0 + i < a.M)
+                    f[i] = static_cast<const float *>(a.weight)[c0 + i];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < VW + 2; ++i) f[i] = o & 2 ? f[i + 2] : f[i];
+#pragma unroll
+        for (int i = 0; i < VW; ++i) w[i] = o & 1 ? f[i + 1] : f[i];
+    } else {
+        Unit<S, VW> u;
+        if (__all_sync(kAll, c >= 0 && c0 + 2 * VW <= a.M)) {
+            u.b = shifted(p[0], p[1], o * int(sizeof(S)));
+        } else {
+            uint32_t h[VW];
+#pragma unroll
+            for (int i = 0; i < VW; ++i) {
+                h[i] = 0;
+                if (c + i >= 0 && c + i < a.M) h[i] = static_cast<const S *>(a.weight)[c + i];
+            }
+            if constexpr (VW == 8)
+                u.b = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16,
+                                 h[6] | h[7] << 16);
+        }
         widen_unit<E, VW>(u, w);
     }
 }
@@ -325,41 +536,93 @@ __device__ __forceinline__ float max_magnitude32(float a, float b) {
 
 // The norm with a row held in the registers of a.warps warps, NV units of VW
 // elements to a lane.  FMT: 0 writes out, else codes (VW = 8 or 4, a group is 4 to 32
-// lanes).
-template <class E, int VW, int NV, int FMT>
+// lanes).  ANY: rows at any address, taken in pieces for out and in columns for codes.
+template <class E, int VW, int NV, int FMT, bool ANY>
 __global__ void __launch_bounds__(1024)
 norm_rows(const __grid_constant__ NormArgs a) {
     using S = typename E::S;
+    constexpr bool kPieces = ANY && FMT == 0, kColumns = ANY && FMT != 0;
     __shared__ float parts[32];
     wait_for_previous_grid();
     const int lane = int(threadIdx.x & 31), warp = int(threadIdx.x >> 5);
     const int part = warp % a.warps;
     const int64_t t = int64_t(blockIdx.x) * int(blockDim.x / 32 / a.warps) + warp / a.warps;
+    const auto unit_of = [&](int j) { return (j * a.warps + part) * 32 + lane; };
+    PieceRow row, other_row;
+    if constexpr (ANY) {
+        row = PieceRow(a.x, t, a.T, a.M, S());
+        other_row = a.residual.p ? PieceRow(a.residual, t, a.T, a.M, S()) : row;
+    }
+    const int head = kPieces ? row.head / int(sizeof(S)) : 0;
+    const auto store = [&](const View &view, int j, bool there, const Unit<S, VW> &u) {
+        if constexpr (kPieces) {
+            const uint64_t p = reinterpret_cast<uint64_t>(view.at<S>(t, 0)) - uint64_t(row.head) +
+                               int64_t(16 * unit_of(j));
+            if (t < a.T && row.whole(unit_of(j) - lane)) *reinterpret_cast<uint4 *>(p) = u.b;
+            else if (there) store_part(p, u.b, row.from(unit_of(j)), row.to(unit_of(j)));
+        } else if constexpr (kColumns) {
+            if (t < a.T)
+                store_shifted(view.at<S>(t, 0), unit_of(j), int64_t(a.M) * sizeof(S), u.b, lane);
+        } else if (there) {
+            u.store(view.unit<S, VW>(t, unit_of(j)));
+        }
+    };
     Unit<S, VW> x[NV], other[NV];
     bool there[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        const int unit = (j * a.warps + part) * 32 + lane;
-        there[j] = t < a.T && unit < a.units;
+        there[j] = t < a.T && (kPieces ? 16 * unit_of(j) < row.span : unit_of(j) < a.units);
         x[j].b = other[j].b = {};
-        if (there[j]) x[j].load(a.x.unit<const S, VW>(t, unit));
+    }
+    if constexpr (kPieces) {
+        if (t < a.T) {
+#pragma unroll
+            for (int j = 0; j < NV; ++j) x[j].b = row.load(unit_of(j));
+            if (a.residual.p)
+#pragma unroll
+                for (int j = 0; j < NV; ++j) other[j].b = other_row.load(unit_of(j));
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+                if (!row.whole(unit_of(j) - lane)) {
+                    const int from = row.from(unit_of(j)), to = row.to(unit_of(j));
+                    x[j].b = some_bytes(x[j].b, from, to);
+                    other[j].b = some_bytes(other[j].b, from, to);
+                }
+        }
+    } else if constexpr (kColumns) {
+        if (t < a.T) {
+            Pieces px[NV], pother[NV];
+#pragma unroll
+            for (int j = 0; j < NV; ++j) px[j].load(row, unit_of(j));
+            if (a.residual.p)
+#pragma unroll
+                for (int j = 0; j < NV; ++j) pother[j].load(other_row, unit_of(j));
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                x[j].b = join_pieces(row, unit_of(j), px[j].lo, px[j].hi);
+                if (a.residual.p)
+                    other[j].b = join_pieces(other_row, unit_of(j), pother[j].lo, pother[j].hi);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            if (there[j]) x[j].load(a.x.unit<const S, VW>(t, unit_of(j)));
+        if (a.residual.p)
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+                if (there[j]) other[j].load(a.residual.unit<const S, VW>(t, unit_of(j)));
     }
     float y[NV][VW];
     if (a.residual.p) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int unit = (j * a.warps + part) * 32 + lane;
-            if (there[j]) other[j].load(a.residual.unit<const S, VW>(t, unit));
-        }
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int unit = (j * a.warps + part) * 32 + lane;
             float f[VW];
             widen_unit<E, VW>(x[j], y[j]);
             widen_unit<E, VW>(other[j], f);
             fma_n<VW>(y[j], 1.0f, f, f);                   // the sum, rounded once
             x[j] = round_unit<E, VW>(f);
-            if (there[j]) x[j].store(a.total.unit<S, VW>(t, unit));
+            store(a.total, j, there[j], x[j]);
         }
     }
     float2 squares = make_float2(0.0f, 0.0f);
@@ -376,20 +639,21 @@ norm_rows(const __grid_constant__ NormArgs a) {
     uint32_t largest[NV] = {};
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        const int unit = (j * a.warps + part) * 32 + lane;
-        const int64_t c = int64_t(unit) * VW;
+        const int64_t c = int64_t(unit_of(j)) * VW;
         float w[VW];
 #pragma unroll
         for (int i = 0; i < VW; ++i) w[i] = 0.0f;
-        if (there[j]) load_weight<E, VW>(a, c, w);
+        if constexpr (ANY) load_weight_at<E, VW>(a, int(c) - head, w);
+        else if (there[j]) load_weight<E, VW>(a, c, w);
         mul_n<VW>(y[j], r, y[j]);
         mul_n<VW>(y[j], w, y[j]);
         if constexpr (FMT == 0) {
-            if (there[j]) round_unit<E, VW>(y[j]).store(a.out.unit<S, VW>(t, unit));
+            store(a.out, j, there[j], round_unit<E, VW>(y[j]));
         } else {
             float m = 0.0f;
 #pragma unroll
-            for (int i = 0; i < VW; ++i) m = max_magnitude32(m, y[j][i]);
+            for (int i = 0; i < VW; ++i)
+                m = max_magnitude32(m, kColumns && c + i >= a.M ? 0.0f : y[j][i]);
             // (a zero times a NaN or an infinite root is a NaN: not in the row's columns)
             largest[j] = there[j] ? __float_as_uint(m) & 0x7FFFFFFFu : 0u;
         }
@@ -409,15 +673,21 @@ norm_rows(const __grid_constant__ NormArgs a) {
         if (!live) inv = 0.0f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int unit = (j * a.warps + part) * 32 + lane;
+            const int unit = unit_of(j);
             const float q = __shfl_sync(kAll, inv, first + j);
             uint32_t code[VW / 4];
 #pragma unroll
             for (int i = 0; i < VW / 4; ++i)               // not live: NaN and infinities too
                 code[i] = q == 0.0f ? 0u : encode32x4<FMT>(y[j] + 4 * i, q);
-            if (there[j])
+            if constexpr (kColumns) {
+                static_assert(VW == 8, "units of 8 codes");
+                if (t < a.T)
+                    store_shifted(a.codes + t * a.M, unit, a.M,
+                                  uint64_t(code[1]) << 32 | code[0], lane);
+            } else if (there[j]) {
                 store_unit<uint32_t, VW / 4>(
                     reinterpret_cast<uint32_t *>(a.codes + t * a.M + int64_t(unit) * VW), code);
+            }
             // (lane j of a row's last group may lie behind the row's end)
             if (mine == j && t < a.T && unit - mine < a.units)
                 a.scales[t * a.groups + unit / lanes] = scale;
@@ -516,8 +786,14 @@ __device__ __forceinline__ float2 row_sums(float u, float v, float2 (*parts)[32]
 // blocks fit an SM: 318 us for 288 at T = 55,414, M = 3,584.)
 constexpr int kNormStages = 2;
 
-__host__ __device__ constexpr bool copies_rows(int size, int vw, int nv) {
-    return size == 2 && vw > 1 && nv <= 2;  // with four units to a lane they do not fit
+__host__ __device__ constexpr bool copies_rows(int size, int vw, int nv, bool any) {
+    return any || (size == 2 && vw > 1 && nv <= 2);  // with four units to a lane they do not fit
+}
+
+// The unit's piece, for rows that lie in the view.
+__device__ __forceinline__ void copy_piece(uint4 *to, uint64_t p) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                 ::"r"(uint32_t(__cvta_generic_to_shared(to))), "l"(p) : "memory");
 }
 
 // A unit of global memory to shared memory, behind the thread's back; the hardware
@@ -548,35 +824,88 @@ __device__ __forceinline__ void wait_copies() {
 // loaded at a time (bf16, T = 55,414, M = 3,584, with grad_total: 288 us, 335 with the
 // rows in registers).  Rows of float32 stay in registers (T = 55,413, M = 2,048: 271
 // us, 314 through shared memory).
-template <class E, int VW, int NV>
+//
+// ANY: rows at any address, in pieces, copied whatever their type; the weight's units lie in
+// shared memory too, shifted once.  The rows of a block are a multiple of 8 apart where
+// there is more than one round of them, so that they lie alike: a lane has the same
+// columns of all.
+template <class E, int VW, int NV, bool ANY>
 __global__ void __launch_bounds__(512, NV <= 2 ? 2 : 1)
 norm_backward_rows(const __grid_constant__ NormArgs a) {
     using S = typename E::S;
     using U = Unit<S, VW>;
-    constexpr bool kCopies = copies_rows(int(sizeof(S)), VW, NV);
+    constexpr bool kCopies = copies_rows(int(sizeof(S)), VW, NV, ANY);
     __shared__ float2 parts[2][32];
-    extern __shared__ uint4 dynamic[];     // [kNormStages][h, g, more][NV][threads] units
+    // [kNormStages][h, g, more][NV][threads] units; ANY: the weight's, [VW / 4][NV][threads]
+    // in float32 or [NV][threads]
+    extern __shared__ uint4 dynamic[];
     wait_for_previous_grid();
     const int lane = int(threadIdx.x & 31), warp = int(threadIdx.x >> 5);
     const int part = warp % a.warps, rows = int(blockDim.x / 32 / a.warps);
     U *const ring = reinterpret_cast<U *>(dynamic) + threadIdx.x;
     const int step = int(blockDim.x);
     float dw[NV][VW] = {};
+    const int64_t ahead = int64_t(gridDim.x) * rows;
+    int64_t t = int64_t(blockIdx.x) * rows + warp / a.warps;
+    const auto unit_of = [&](int j) { return (j * a.warps + part) * 32 + lane; };
+    PieceRow first = {};                   // all of the lane's rows lie as it does
+    if constexpr (ANY) first = PieceRow(a.x, t, a.T, a.M, S());
+    const auto there = [&](int j) {
+        return ANY ? 16 * unit_of(j) < first.span : unit_of(j) < a.units;
+    };
+    const auto whole = [&](int j) { return !ANY || first.whole(unit_of(j) - lane); };
+    const int head = first.head / int(sizeof(S));
+    const auto copy = [&](const View &view, int64_t r, int j, U *to) {
+        if constexpr (ANY) {
+            const PieceRow row(view, r, a.T, a.M, S());
+            if (row.inside) copy_piece(&to->b, row.start + int64_t(16 * unit_of(j)));
+            else to->b = row.load_slow(unit_of(j));
+        } else {
+            copy_unit(to, view.unit<const S, VW>(r, unit_of(j)));
+        }
+    };
+    const auto load = [&](const View &view, int j) {
+        U u;
+        if constexpr (ANY) u.b = PieceRow(view, t, a.T, a.M, S()).load(unit_of(j));
+        else u.load(view.unit<const S, VW>(t, unit_of(j)));
+        return u;
+    };
+    uint4 *const weights = dynamic + (kCopies ? kNormStages * 3 * NV * step : 0) + threadIdx.x;
+    if constexpr (ANY) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            float w[VW];
+            load_weight_at<E, VW>(a, unit_of(j) * VW - head, w);
+            if (a.weight32) {
+#pragma unroll
+                for (int i = 0; i < VW / 4; ++i)
+                    memcpy(&weights[(i * NV + j) * step], w + 4 * i, 16);
+            } else {
+                weights[j * step] = round_unit<E, VW>(w).b;
+            }
+        }
+    }
+    const auto weight = [&](int j, float (&w)[VW]) {
+        if constexpr (!ANY) {
+            load_weight<E, VW>(a, int64_t(unit_of(j)) * VW, w);
+        } else if (a.weight32) {
+#pragma unroll
+            for (int i = 0; i < VW / 4; ++i) memcpy(w + 4 * i, &weights[(i * NV + j) * step], 16);
+        } else {
+            widen_unit<E, VW>(U{weights[j * step]}, w);
+        }
+    };
     const auto fetch = [&](int64_t t, U *to) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int unit = (j * a.warps + part) * 32 + lane;
-            if (t < a.T && unit < a.units) {
-                copy_unit(to + j * step, a.x.unit<const S, VW>(t, unit));
-                copy_unit(to + (NV + j) * step, a.grad.unit<const S, VW>(t, unit));
-                if (a.grad_total.p)
-                    copy_unit(to + (2 * NV + j) * step, a.grad_total.unit<const S, VW>(t, unit));
+            if (t < a.T && there(j)) {
+                copy(a.x, t, j, to + j * step);
+                copy(a.grad, t, j, to + (NV + j) * step);
+                if (a.grad_total.p) copy(a.grad_total, t, j, to + (2 * NV + j) * step);
             }
         }
         commit_copies();
     };
-    const int64_t ahead = int64_t(gridDim.x) * rows;
-    int64_t t = int64_t(blockIdx.x) * rows + warp / a.warps;
     if constexpr (kCopies)
         for (int i = 0; i < kNormStages - 1; ++i) fetch(t + i * ahead, ring + i * 3 * NV * step);
     int turn = 0, stage = 0;
@@ -586,12 +915,11 @@ norm_backward_rows(const __grid_constant__ NormArgs a) {
         if constexpr (!kCopies) {
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                const int unit = (j * a.warps + part) * 32 + lane;
                 held[0][j].b = held[1][j].b = held[2][j].b = {};
-                if (t < a.T && unit < a.units) {
-                    held[0][j].load(a.x.unit<const S, VW>(t, unit));
-                    held[1][j].load(a.grad.unit<const S, VW>(t, unit));
-                    if (a.grad_total.p) held[2][j].load(a.grad_total.unit<const S, VW>(t, unit));
+                if (t < a.T && there(j)) {
+                    held[0][j] = load(a.x, j);
+                    held[1][j] = load(a.grad, j);
+                    if (a.grad_total.p) held[2][j] = load(a.grad_total, j);
                 }
             }
         } else {
@@ -601,16 +929,20 @@ norm_backward_rows(const __grid_constant__ NormArgs a) {
             wait_copies<kNormStages - 1>();
         }
         const auto row = [&](int which, int j) {
-            if constexpr (kCopies) return here[(which * NV + j) * step];
-            else return held[which][j];
+            U u;
+            if constexpr (kCopies) u = here[(which * NV + j) * step];
+            else u = held[which][j];
+            if constexpr (ANY)
+                if (!whole(j))
+                    u.b = some_bytes(u.b, first.from(unit_of(j)), first.to(unit_of(j)));
+            return u;
         };
         float2 squares = make_float2(0.0f, 0.0f), dot = squares;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int unit = (j * a.warps + part) * 32 + lane;
-            if (t >= a.T || unit >= a.units) continue;
+            if (t >= a.T || !there(j)) continue;
             float f[VW], d[VW], w[VW];
-            load_weight<E, VW>(a, int64_t(unit) * VW, w);
+            weight(j, w);
             widen_unit<E, VW>(row(0, j), f);
             widen_unit<E, VW>(row(1, j), d);
             dot_n<VW>(f, f, squares);
@@ -623,10 +955,9 @@ norm_backward_rows(const __grid_constant__ NormArgs a) {
         const float q = r * r * (both.y * a.inv_m);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int unit = (j * a.warps + part) * 32 + lane;
-            if (t >= a.T || unit >= a.units) continue;
+            if (t >= a.T || !there(j)) continue;
             float f[VW], d[VW], w[VW], m[VW] = {};
-            load_weight<E, VW>(a, int64_t(unit) * VW, w);
+            weight(j, w);
             widen_unit<E, VW>(row(0, j), f);
             widen_unit<E, VW>(row(1, j), d);
             mul_n<VW>(d, w, w);
@@ -635,7 +966,15 @@ norm_backward_rows(const __grid_constant__ NormArgs a) {
             fma_n<VW>(d, f, dw[j], dw[j]);
             if (a.grad_total.p) widen_unit<E, VW>(row(2, j), m);
             fma_n<VW>(w, r, m, m);
-            round_unit<E, VW>(m).store(a.grad_x.unit<S, VW>(t, unit));
+            const U result = round_unit<E, VW>(m);
+            if constexpr (ANY) {
+                const uint64_t p = reinterpret_cast<uint64_t>(a.grad_x.at<S>(t, 0)) -
+                                   uint64_t(first.head) + int64_t(16 * unit_of(j));
+                if (whole(j)) *reinterpret_cast<uint4 *>(p) = result.b;
+                else store_part(p, result.b, first.from(unit_of(j)), first.to(unit_of(j)));
+            } else {
+                result.store(a.grad_x.unit<S, VW>(t, unit_of(j)));
+            }
         }
         turn ^= 1;
         if (++stage == kNormStages) stage = 0;
@@ -650,11 +989,10 @@ norm_backward_rows(const __grid_constant__ NormArgs a) {
         if (warp / a.warps != row) continue;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int unit = (j * a.warps + part) * 32 + lane;
-            if (unit >= a.units) continue;
 #pragma unroll
             for (int i = 0; i < VW; ++i) {
-                const int c = unit * VW + i;
+                const int c = unit_of(j) * VW - head + i;
+                if (c < 0 || c >= a.M) continue;
                 const float v = row > 0 ? sums[c] + dw[j][i] : dw[j][i];
                 if (row < rows - 1) sums[c] = v;
                 else mine[c] = v;

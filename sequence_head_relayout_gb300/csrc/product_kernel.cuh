@@ -39,6 +39,8 @@
 
 #include <cstdint>
 
+#include "shift.cuh"
+
 namespace vfp {
 
 constexpr int kBlockK = 64;                    // k of a stage: 128 bytes of 16-bit elements
@@ -519,18 +521,6 @@ struct Tiles {
 
 // ---- epilogue ------------------------------------------------------------------
 
-// The 16 bytes from byte `shift` (even) of lo and hi on.
-__device__ __forceinline__ uint4 shifted(const uint4 &lo, const uint4 &hi, int shift) {
-    uint32_t x[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-#pragma unroll
-    for (int j = 0; j < 6; ++j) x[j] = shift & 8 ? x[j + 2] : x[j];
-#pragma unroll
-    for (int j = 0; j < 5; ++j) x[j] = shift & 4 ? x[j + 1] : x[j];
-    const int bits = shift & 2 ? 16 : 0;
-    return make_uint4(__funnelshift_r(x[0], x[1], bits), __funnelshift_r(x[1], x[2], bits),
-                      __funnelshift_r(x[2], x[3], bits), __funnelshift_r(x[3], x[4], bits));
-}
-
 __device__ __forceinline__ uint32_t round2(float lo, float hi, bool bf16) {
     if (bf16) {
         const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
@@ -660,7 +650,7 @@ __device__ __forceinline__ void store_weights16(const ProductArgs &a, int e, int
             }
             if (i < 7) {
                 const uint4 hi = *reinterpret_cast<const uint4 *>(staging + r * 144 + i * 16 + 16);
-                *reinterpret_cast<uint4 *>(row + head + i * 8) = shifted(lo, hi, head * 2);
+                *reinterpret_cast<uint4 *>(row + head + i * 8) = vf::shifted(lo, hi, head * 2);
             }
             const int c = i < head ? i : 56 + i;
             row[c] = *reinterpret_cast<const uint16_t *>(staging + r * 144 + c * 2);
@@ -1083,7 +1073,7 @@ pad_lines(const __grid_constant__ PadArgs a) {
                     if (shift) hi[u] = piece(a, at + 16 * c + 16);
                 }
 #pragma unroll
-                for (int u = 0; u < U; ++u) v[u] = shifted(v[u], hi[u], shift);
+                for (int u = 0; u < U; ++u) v[u] = vf::shifted(v[u], hi[u], shift);
             } else {
 #pragma unroll
                 for (int u = 0; u < U; ++u) {

@@ -21,22 +21,48 @@ vf::View view(const void *p, const int64_t str[2]) {
     return {const_cast<void *>(p), str[0], str[1]};
 }
 
-// Widest unit (elements) that keeps every access of the views aligned.
+// Widest unit (elements) that keeps every access of the views aligned; and whether their
+// rows can be taken at any address, in pieces of 16 bytes, and lie in them alike.
 struct Width {
     int64_t size, n, m, vw;
+    bool any = true, alike = true;
+    int64_t first = -1, stride = 0;            // of the first view, in a piece
 
     Width(int64_t size_, int64_t n_, int64_t m_) : size(size_), n(n_), m(m_), vw(16 / size_) {
         while (vw > 1 && m % vw) vw /= 2;
     }
     void take(const void *p, const int64_t str[2]) {
         if (p == nullptr) return;
-        if (str[1] != 1 && m > 1) vw = 1;
-        while (vw > 1 && (reinterpret_cast<uintptr_t>(p) % uintptr_t(vw * size) ||
-                          (n > 1 && str[0] % vw)))
-            vw /= 2;
+        const int64_t at = int64_t(reinterpret_cast<uintptr_t>(p) % 16);
+        const int64_t step = n > 1 ? str[0] % (16 / size) : 0;
+        if (first < 0) first = at, stride = step;
+        else if (at != first || step != stride) alike = false;
+        if (str[1] != 1 && m > 1) vw = 1, any = false;
+        while (vw > 1 && (at % (vw * size) || (n > 1 && str[0] % vw))) vw /= 2;
     }
+    // Rows in pieces, where accesses would have at most `narrow` elements and a block holds
+    // the units.  With narrow accesses and in pieces (T = 40,000, with a residual or
+    // grad_total, us):
+    //               norm bf16   norm fp32   backward bf16   backward fp32
+    //   M = 1,421   216   108   209   138     465   174       268   239
+    //   M = 1,422    86   106   132   136     222   173       240   238
+    //   M = 1,420    74   103                 169   171
+    bool any_pieces(int64_t narrow, int64_t most) {
+        if (!any || !alike || vw > narrow || ceil_div(m + 16 / size - 1, 16 / size) > most)
+            return false;
+        vw = 16 / size;
+        return true;
+    }
+    // The same in columns, for codes (M = 1,421, 1,422 and 1,420: 566 and 257, 478 and 227,
+    // 151 and 216).
+    bool any_columns() {
+        if (!any || vw > 2 || m > 32 * 32 * 2 * 8) return false;
+        vw = 16 / size;
+        return true;
+    }
+    // The most units of a row.
+    int64_t units(bool pieces) const { return ceil_div(m + (pieces ? 16 / size - 1 : 0), vw); }
 };
-
 // ---------------------------------------------------------------- gated activation
 
 template <class E, int VW>
@@ -135,39 +161,34 @@ int glu(const vf_glu_desc *d, bool backward, cudaStream_t stream) {
 constexpr int64_t kNormColumns = int64_t(1) << 24;         // M
 
 // The most that the backward pass takes: stages of three rows, two units of 16 bytes to
-// each of 512 threads.
-constexpr int kNormShared = vf::kNormStages * 3 * 2 * 16 * 512;
+// each of 512 threads, and the weight's units in float32.
+constexpr int kNormShared = (vf::kNormStages * 3 + 2) * 2 * 16 * 512;
 
 int64_t norm_blocks(int64_t T) { return std::min<int64_t>(T, vf::kNormBlocks); }
 static_assert(vf::kNormBlocks == kSMs * 4, "four blocks to an SM");
 
 using NormKernel = void (*)(vf::NormArgs);
 
-template <class E, int VW>
+template <class E, int VW, int FMT = 0, bool ANY = false>
 NormKernel norm_kernel(int64_t nv) {
     switch (nv) {
-        case 1: return vf::norm_rows<E, VW, 1, 0>;
-        case 2: return vf::norm_rows<E, VW, 2, 0>;
-        default: return vf::norm_rows<E, VW, 4, 0>;
-    }
-}
-
-template <int FMT, int VW>
-NormKernel norm_q_kernel(int64_t nv) {
-    switch (nv) {
-        case 1: return vf::norm_rows<vf::Bf16, VW, 1, FMT>;
-        case 2: return vf::norm_rows<vf::Bf16, VW, 2, FMT>;
-        default: return vf::norm_rows<vf::Bf16, VW, 4, FMT>;
+        case 1: return vf::norm_rows<E, VW, 1, FMT, ANY>;
+        case 2: return vf::norm_rows<E, VW, 2, FMT, ANY>;
+        default: return vf::norm_rows<E, VW, 4, FMT, ANY>;
     }
 }
 
 template <int FMT>
-NormKernel norm_q_kernel(int64_t vw, int64_t nv) {
-    return vw == 8 ? norm_q_kernel<FMT, 8>(nv) : norm_q_kernel<FMT, 4>(nv);
+NormKernel norm_q_kernel(int64_t vw, int64_t nv, bool any) {
+    if (any)
+        return nv == 1 ? vf::norm_rows<vf::Bf16, 8, 1, FMT, true>
+                       : vf::norm_rows<vf::Bf16, 8, 2, FMT, true>;
+    return vw == 8 ? norm_kernel<vf::Bf16, 8, FMT>(nv) : norm_kernel<vf::Bf16, 4, FMT>(nv);
 }
 
 template <class E>
-NormKernel norm_kernel(int64_t vw, int64_t nv) {
+NormKernel norm_kernel(int64_t vw, int64_t nv, bool any) {
+    if (any) return norm_kernel<E, 16 / int(sizeof(typename E::S)), 0, true>(nv);
     if constexpr (sizeof(typename E::S) == 2)
         if (vw == 8) return norm_kernel<E, 8>(nv);
     switch (vw) {
@@ -179,13 +200,17 @@ NormKernel norm_kernel(int64_t vw, int64_t nv) {
 
 template <class E, int VW>
 NormKernel backward_kernel(int64_t nv) {
-    return nv == 1   ? vf::norm_backward_rows<E, VW, 1>
-           : nv == 2 ? vf::norm_backward_rows<E, VW, 2>
-                     : vf::norm_backward_rows<E, VW, 4>;
+    return nv == 1   ? vf::norm_backward_rows<E, VW, 1, false>
+           : nv == 2 ? vf::norm_backward_rows<E, VW, 2, false>
+                     : vf::norm_backward_rows<E, VW, 4, false>;
 }
 
 template <class E>
-NormKernel backward_kernel(int64_t vw, int64_t nv) {
+NormKernel backward_kernel(int64_t vw, int64_t nv, bool any) {
+    constexpr int kMost = 16 / int(sizeof(typename E::S));
+    if (any)
+        return nv == 1 ? vf::norm_backward_rows<E, kMost, 1, true>
+                       : vf::norm_backward_rows<E, kMost, 2, true>;
     if constexpr (sizeof(typename E::S) == 2)
         if (vw == 8) return backward_kernel<E, 8>(nv);
     switch (vw) {
@@ -220,6 +245,7 @@ vf::NormArgs norm_args(const vf_norm_desc *d) {
 // The weight as a row of the views: its units are aligned like theirs, and 16-byte
 // float32 accesses where they have four elements or more.
 void take_weight(Width *w, const vf_norm_desc *d) {
+    if (reinterpret_cast<uintptr_t>(d->weight) % 16) w->any = false;
     const int64_t size = type_size(d->weight_type);
     while (w->vw > 1 && reinterpret_cast<uintptr_t>(d->weight) %
                             uintptr_t(std::min<int64_t>(16, w->vw * size)))
@@ -239,6 +265,40 @@ RowShape row_shape(int64_t units, int64_t most_warps, int64_t nv) {
     s.warps = ceil_div(units, 32 * s.nv);
     s.rows = std::max<int64_t>(1, 8 / s.warps);
     return s;
+}
+
+// Blocks of the backward pass: their rows, shared memory and how many are to be on an SM.
+struct Backward {
+    int64_t resident = 0, smem = 0;
+};
+
+// The rows of a block that bring most warps onto an SM (32 have registers; at most four
+// blocks, whose shares of the weight's gradient are kept).  Blocks walk their rows, so that
+// each SM has to get as many: those that copy rows ask for so much shared memory that one
+// more does not fit (T = 40,000, bf16, M = 1,424: 117 us with two rows to a block, of which
+// an SM had three to five, 98 so; M = 2,304: 208 and 143).  The others leave it to the L1
+// cache, which holds the weight (float32, M = 3,584: 375 us without, 361).
+Backward backward_shape(RowShape *s, const Width &w, bool any, int64_t M, int64_t weight_size) {
+    constexpr int64_t kShared = 228 * 1024, kReserved = 1024 + 512;   // (512: static)
+    const bool copies = vf::copies_rows(int(w.size), int(w.vw), int(s->nv), any);
+    Backward best;
+    int64_t most = 0;
+    for (int64_t rows = 1; rows * s->warps <= 16; ++rows) {
+        const int64_t warps = rows * s->warps, units = s->nv * warps * 32;
+        // the rows to come, the weight's units, and the block's sums (rows > 1: at most two
+        // units to a lane)
+        const int64_t smem = std::max((copies ? vf::kNormStages * 3 * units * w.vw * w.size : 0) +
+                                          (any ? units * w.vw * weight_size : 0),
+                                      rows > 1 ? M * 4 : 0);
+        const int64_t resident =
+            std::min<int64_t>({4, 32 / warps, kShared / (smem + kReserved)});
+        if (smem > kNormShared || resident * warps <= most) continue;
+        most = resident * warps;
+        s->rows = rows;
+        best.resident = resident;
+        best.smem = copies ? std::max(smem, kShared / (resident + 1) - kReserved + 16) : smem;
+    }
+    return best;
 }
 
 int norm(const vf_norm_desc *d, cudaStream_t stream) {
@@ -288,8 +348,9 @@ int norm(const vf_norm_desc *d, cudaStream_t stream) {
         w.take(d->out, d->out_strides);
     }
     take_weight(&w, d);
-    a.units = int32_t(M / w.vw);
-    const RowShape s = row_shape(a.units, 32, 4);
+    const bool any = fmt ? w.any_columns() : w.any_pieces(1, 32 * 32 * 4);
+    a.units = int32_t(w.units(any && !fmt));
+    const RowShape s = row_shape(a.units, 32, any && fmt ? 2 : 4);
     a.warps = int32_t(s.warps);
     // rows that do not fit the registers of a block, and those with codes whose groups are
     // no 4 to 32 lanes
@@ -303,11 +364,11 @@ int norm(const vf_norm_desc *d, cudaStream_t stream) {
         return launch(kernel, std::min<int64_t>(T, kSMs * 8), 256, 0, stream, a);
     }
     const NormKernel kernel =
-        fmt ? (d->format == VF_FORMAT_INT8 ? norm_q_kernel<vf::kFmtInt8>(w.vw, s.nv)
-                                           : norm_q_kernel<vf::kFmtE4M3>(w.vw, s.nv))
-        : d->type == VF_TYPE_BF16 ? norm_kernel<vf::Bf16>(w.vw, s.nv)
-        : d->type == VF_TYPE_F16  ? norm_kernel<vf::F16>(w.vw, s.nv)
-                                  : norm_kernel<vf::F32>(w.vw, s.nv);
+        fmt ? (d->format == VF_FORMAT_INT8 ? norm_q_kernel<vf::kFmtInt8>(w.vw, s.nv, any)
+                                           : norm_q_kernel<vf::kFmtE4M3>(w.vw, s.nv, any))
+        : d->type == VF_TYPE_BF16 ? norm_kernel<vf::Bf16>(w.vw, s.nv, any)
+        : d->type == VF_TYPE_F16  ? norm_kernel<vf::F16>(w.vw, s.nv, any)
+                                  : norm_kernel<vf::F32>(w.vw, s.nv, any);
     return launch(kernel, ceil_div(T, s.rows), int(s.warps * s.rows * 32), 0, stream, a);
 }
 
@@ -345,8 +406,9 @@ int norm_backward(const vf_norm_desc *d, cudaStream_t stream) {
             w.take(d->grad_total, d->grad_total_strides);
         }
         take_weight(&w, d);
-        a.units = int32_t(M / w.vw);
-        const RowShape s = row_shape(a.units, 16, 2);
+        const bool any = w.any_pieces(2, 16 * 32 * 2);
+        a.units = int32_t(w.units(any));
+        RowShape s = row_shape(a.units, 16, 2);
         a.warps = int32_t(s.warps);
         if (s.warps > 16) {
             a.blocks = int32_t(norm_blocks(T));
@@ -355,28 +417,21 @@ int norm_backward(const vf_norm_desc *d, cudaStream_t stream) {
                                                                : vf::norm_backward_any<vf::F32>;
             rc = launch(kernel, a.blocks, 256, 0, stream, a);
         } else {
-            a.blocks = int32_t(std::min(norm_blocks(T), ceil_div(T, s.rows)));
             const NormKernel kernel =
-                d->type == VF_TYPE_BF16  ? backward_kernel<vf::Bf16>(w.vw, s.nv)
-                : d->type == VF_TYPE_F16 ? backward_kernel<vf::F16>(w.vw, s.nv)
-                                         : backward_kernel<vf::F32>(w.vw, s.nv);
-            // shared memory: the rows to come, and the block's sums (s.rows > 1 has at
-            // most 2 units to a lane); as many blocks as fit an SM
-            const int64_t threads = s.warps * s.rows * 32;
-            const bool copies = vf::copies_rows(int(size), int(w.vw), int(s.nv));
-            const size_t smem = size_t(
-                std::max(copies ? vf::kNormStages * 3 * s.nv * threads * w.vw * size : 0,
-                         s.rows > 1 ? M * 4 : 0));
-            const int64_t resident =
-                std::max<int64_t>(1, std::min<int64_t>(4, 220 * 1024 / std::max<int64_t>(1, smem)));
-            a.blocks = int32_t(std::min<int64_t>(a.blocks, kSMs * resident));
-            if (smem > 47 * 1024 &&
+                d->type == VF_TYPE_BF16  ? backward_kernel<vf::Bf16>(w.vw, s.nv, any)
+                : d->type == VF_TYPE_F16 ? backward_kernel<vf::F16>(w.vw, s.nv, any)
+                                         : backward_kernel<vf::F32>(w.vw, s.nv, any);
+            const Backward b = backward_shape(&s, w, any, M, type_size(d->weight_type));
+            const int64_t blocks =
+                std::min(norm_blocks(T), std::min(ceil_div(T, s.rows), kSMs * b.resident));
+            a.blocks = int32_t(blocks);
+            if (b.smem > 47 * 1024 &&
                 cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      kNormShared) != cudaSuccess) {
                 cudaGetLastError();
                 return VF_ERR_CUDA;
             }
-            rc = launch(kernel, a.blocks, int(threads), smem, stream, a);
+            rc = launch(kernel, blocks, int(s.warps * s.rows * 32), size_t(b.smem), stream, a);
         }
         if (rc != VF_OK) return rc;
     }

@@ -329,6 +329,132 @@ def test_norm_backward_layouts(layout, M):
     backward_check(x, g, w, more=m, views=tuple(view_like(t, layout) for t in (x, g, m)))
 
 
+def check_codes(codes, scales, y, fmt, group):
+    """Against the float64 values y, with the bounds of test_norm_q."""
+    T, M = y.shape
+    rel, groups = (M / 2 + 8) * U, -(-M // group)
+    top = 127.0 if fmt == "int8" else 448.0
+    wide = torch.zeros((T, groups * group), dtype=torch.float64)
+    wide[:, :M] = y
+    amax = wide.view(T, groups, group).abs().amax(dim=2)
+    assert ((scales.cpu().double() - amax / top).abs() <= amax / top * (rel + U)).all()
+    q = y * (top / amax).repeat_interleave(group, dim=1)[:, :M]
+    got = X.values(codes.cpu().view(torch.int8 if fmt == "int8" else torch.uint8),
+                   torch.ones_like(scales.cpu()), FMT[fmt], group)
+    off = q.abs() * (2 * rel + 2 * U)              # y, amax, the quotient and the product
+    half = 0.5 if fmt == "int8" else torch.maximum(q.abs() * 2.0 ** -4, torch.tensor(2.0 ** -10))
+    assert ((got - q).abs() <= half + off * 1.07).all()
+
+
+class Placed:
+    """Rows at any address: the values in a buffer that holds `fill` around them, `base`
+    elements behind an aligned address, rows `pitch` apart."""
+
+    def __init__(self, x, base, pitch, fill):
+        T, M = x.shape
+        self.at = base + (torch.arange(T) * pitch)[:, None] + torch.arange(M)
+        self.flat = torch.full((base + T * pitch + 40,), fill, dtype=x.dtype, device=DEV)
+        self.view = self.flat.as_strided((T, M), (pitch, 1), base).copy_(x)
+        self.fill = fill
+
+    def untouched(self):
+        flat = self.flat.cpu()
+        flat[self.at.reshape(-1)] = self.fill
+        return torch.equal(flat, torch.full_like(flat, self.fill))
+
+
+# (T, M, base, pitch - M): odd lengths, rows that start anywhere, one to many warps to a
+# row, rows of one element and a few, several rounds of a block, the longest in registers
+# and longer ones; the last have one more unit than a multiple of 64
+PLACES = [(5, 1, 0, 0), (9, 3, 0, 0), (7, 3, 5, 4), (33, 7, 0, 0), (40, 9, 1, 2),
+          (20, 33, 0, 0), (21, 97, 3, 1), (17, 255, 0, 0), (11, 257, 7, 0), (9, 777, 0, 0),
+          (8, 1421, 0, 2), (2600, 101, 0, 0), (10001, 37, 0, 0), (5003, 21, 3, 2),
+          (3, 2047, 0, 0), (2, 2047, 2, 3), (1, 4095, 3, 0), (2, 8191, 0, 0), (2, 9001, 1, 0),
+          (1, 32761, 0, 0), (2, 32763, 0, 0), (19, 510, 0, 1), (14, 1022, 4, 5),
+          (9, 513, 0, 0), (9, 1031, 2, 1)]
+
+
+@pytest.mark.parametrize("weight", ["same", "fp32"])
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("T,M,base,gap", PLACES)
+def test_norm_at_any_address(T, M, base, gap, dtype, weight):
+    """What lies around the rows is neither read into a result nor written."""
+    x, r, g, m = (randn((T, M), dtype, i) for i in range(4))
+    w = randn((M,), F32 if weight == "fp32" else dtype, 5)
+    nan, pitch = float("nan"), M + gap
+    place = [Placed(t, base, pitch, nan) for t in (x, r, g, m)]
+    zero = torch.zeros_like(x)
+    outs = [Placed(zero, base, pitch, 7.0) for _ in range(3)]
+    out, total, dx = (o.view for o in outs)
+    xv, rv, gv, mv = (p.view for p in place)
+    # a residual at an address of its own too
+    for other in (rv, Placed(r, base + 1, pitch + 2, nan).view):
+        check_norm(x, w, residual=r, xv=xv, rv=other, out=out, total=total)
+    check_norm(x, w, xv=xv, out=out)
+    want, want_w, mag, mag_w = L.norm_backward(g, x, w, 1e-6, m)
+    err = mag * (2 * M + 20) * U
+    for first in (True, False):
+        got, dw = vf.rms_norm_backward(gv, xv, w.to(DEV), grad_total=mv, grad_x=dx)
+        within(got, want, err + rounding(want.abs() + err, dtype))
+        within(dw, want_w, mag_w * (T + M / 2 + 16) * U + 2.0 ** -149)
+        if first:
+            kept = got.clone(), dw
+    assert torch.equal(got, kept[0]) and torch.equal(dw, kept[1])
+    want, want_w, mag, mag_w = L.norm_backward(g, x, w, 1e-6)
+    err = mag * (2 * M + 20) * U
+    got, dw = vf.rms_norm_backward(gv, xv, w.to(DEV), grad_x=dx)
+    within(got, want, err + rounding(want.abs() + err, dtype))
+    within(dw, want_w, mag_w * (T + M / 2 + 16) * U + 2.0 ** -149)
+    assert all(o.untouched() for o in outs)
+    # a weight that starts anywhere
+    w1 = torch.full((M + 1,), nan, dtype=w.dtype, device=DEV)[1:].copy_(w)
+    a, b = vf.rms_norm(xv, w1), vf.rms_norm(x.to(DEV), w.to(DEV))
+    bound = norm_bound(x, w, 1e-6, dtype)[1]
+    assert ((a - b).cpu().double().abs() <= 2 * bound).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_norm_at_any_address_special_rows(dtype):
+    """A row of NaN or infinities stays by itself where rows share their pieces."""
+    for M in (97, 1421):
+        x, w = randn((9, M), dtype, 1), randn((M,), dtype, 2)
+        x[2], x[5], x[7] = float("nan"), float("inf"), 0.0
+        clean = [0, 1, 3, 4, 6, 7, 8]
+        out = vf.rms_norm(x.to(DEV), w.to(DEV), 1e-5).cpu()
+        want, bound = norm_bound(x, w, 1e-5, dtype)
+        within(out[clean], want[clean], bound[clean])
+        assert torch.isnan(out[2]).all() and torch.isnan(out[5]).all()
+        g = randn((9, M), dtype, 3)
+        dx = vf.rms_norm_backward(g.to(DEV), x.to(DEV), w.to(DEV), 1e-5)[0].cpu()
+        want, _, mag, _ = L.norm_backward(g, x, w, 1e-5)
+        err = mag * (2 * M + 20) * U
+        within(dx[clean], want[clean], (err + rounding(want.abs() + err, dtype))[clean])
+        assert torch.isnan(dx[2]).all()
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("T,M,base,gap", PLACES)
+def test_norm_q_at_any_address(T, M, base, gap, fmt):
+    """Codes, scales and totals, wherever the rows and the codes lie."""
+    x, r, w = randn((T, M), BF16, 1) * 3, randn((T, M), BF16, 2), randn((M,), BF16, 3)
+    nan, pitch = float("nan"), M + gap
+    px, pr = Placed(x, base, pitch, nan), Placed(r, base + 1, pitch + 1, nan)
+    total = Placed(torch.zeros_like(x), base + 2, pitch + 1, 7.0)
+    h = L.total(x, r)
+    for group, off in ((32, 0), (256, 0), (64, 1), (128, 6)):
+        flat = torch.full((off + T * M + 20,), 3, dtype=torch.int8, device=DEV)
+        codes = flat[off:off + T * M].view(T, M)
+        if fmt == "e4m3":
+            codes = codes.view(torch.float8_e4m3fn)
+        _, scales = vf.rms_norm_q(px.view, w.to(DEV), 1e-6, fmt, group, codes=codes)
+        check_codes(codes, scales, L.norm(x, w, 1e-6), fmt, group)
+        vf.rms_norm_q(px.view, w.to(DEV), 1e-6, fmt, group, residual=pr.view, codes=codes,
+                      scales=scales, total=total.view)
+        check_codes(codes, scales, L.norm(h, w, 1e-6), fmt, group)
+        assert torch.equal(total.view.cpu(), h) and total.untouched()
+        assert (flat[:off] == 3).all() and (flat[off + T * M:] == 3).all()
+
+
 def test_norm_differences():
     x, g, w = (randn(s, F32, i) for i, s in enumerate([(4, 48), (4, 48), (48,)]))
     dx, dw = vf.rms_norm_backward(g.to(DEV), x.to(DEV), w.to(DEV), 1e-3)
