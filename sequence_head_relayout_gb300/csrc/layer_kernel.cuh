@@ -91,10 +91,11 @@ struct View {
 // read one by one.  There are two ways to take them:
 // * A lane's unit is a piece, with head = the elements in front of the row in its first
 //   one: unit u has columns u VW - head and on.  All views of a call have to lie alike; the
-//   weight is shifted to them.  This costs next to nothing.
-// * A lane's unit is columns u VW and on (the codes' groups are columns): it shifts together
-//   the two pieces that its unit lies in, the second of which is the next lane's first, and
-//   stores the piece that its unit and the one of the lane before it fill.
+//   weight is shifted to them.  (The order of a row's sums is by its address then.)
+// * A lane's unit is columns u VW and on (the codes' groups are columns, and the halves of
+//   the activation's rows do not lie alike): it shifts together the two pieces that its unit
+//   lies in, the second of which is the next lane's first, and stores the piece that its
+//   unit and the one of the lane before it fill.
 
 // Bytes from .. to - 1 (both even) at p, zeros for the others of the 16.
 __device__ __noinline__ uint4 load_some(uint64_t p, int from, int to) {
@@ -308,7 +309,7 @@ struct GluArgs {
     View gate, up, grad;          // read
     View out, out_up;             // glu: out; backward: the gradients of gate and up
     int32_t rows, E;
-    int32_t units;                // F / VW
+    int32_t F, units;             // units: of VW elements in a row
     int32_t col_blocks;
 };
 
@@ -322,15 +323,23 @@ __device__ __forceinline__ float sigmoid(float g) {
 }
 
 // A thread takes one unit of columns of U rows at a time; blockDim is (columns, rows).
-template <class E, int VW, bool BACKWARD>
+// ANY: rows at any address, in columns.
+template <class E, int VW, bool BACKWARD, bool ANY>
 __global__ void __launch_bounds__(256)
 expert_glu_rows(const __grid_constant__ GluArgs a) {
     using S = typename E::S;
-    constexpr int U = 2;
+    constexpr int U = ANY ? 1 : 2;
     wait_for_previous_grid();
     const int used = min(max(a.offsets[a.E], 0), a.rows);
     const int unit = int(blockIdx.x % uint32_t(a.col_blocks) * blockDim.x + threadIdx.x);
-    if (unit >= a.units) return;
+    const int lane = int(threadIdx.x & 31);
+    if (unit - (ANY ? lane : 0) >= a.units) return;
+    const auto store = [&](const View &view, int64_t r, const Unit<S, VW> &u) {
+        if constexpr (ANY)
+            store_shifted(view.at<S>(r, 0), unit, int64_t(a.F) * sizeof(S), u.b, lane);
+        else
+            u.store(view.unit<S, VW>(r, unit));
+    };
     const int64_t step = int64_t(gridDim.x / uint32_t(a.col_blocks)) * blockDim.y * U;
     for (int64_t r0 = (int64_t(blockIdx.x / uint32_t(a.col_blocks)) * blockDim.y + threadIdx.y) * U;
          r0 < used; r0 += step) {
@@ -341,9 +350,26 @@ expert_glu_rows(const __grid_constant__ GluArgs a) {
             there[i] = r0 + i < used && a.slot_of[r0 + i] >= 0;
             gate[i].b = up[i].b = grad[i].b = {};
         }
+        if constexpr (ANY) {
+            if (there[0]) {
+                const View *const views[3] = {&a.gate, &a.up, &a.grad};
+                Unit<S, VW> *const units[3] = {gate, up, grad};
+                constexpr int N = BACKWARD ? 3 : 2;
+                PieceRow rows[N];
+                Pieces pieces[N];
+#pragma unroll
+                for (int k = 0; k < N; ++k) {
+                    rows[k] = PieceRow(*views[k], r0, a.rows, a.F, S());
+                    pieces[k].load(rows[k], unit);
+                }
+#pragma unroll
+                for (int k = 0; k < N; ++k)
+                    units[k][0].b = join_pieces(rows[k], unit, pieces[k].lo, pieces[k].hi);
+            }
+        }
 #pragma unroll
         for (int i = 0; i < U; ++i)
-            if (there[i]) {
+            if (!ANY && there[i]) {
                 gate[i].load(a.gate.unit<const S, VW>(r0 + i, unit));
                 up[i].load(a.up.unit<const S, VW>(r0 + i, unit));
                 if constexpr (BACKWARD) grad[i].load(a.grad.unit<const S, VW>(r0 + i, unit));
@@ -368,8 +394,8 @@ expert_glu_rows(const __grid_constant__ GluArgs a) {
                 if (!there[i]) y[j] = u[j] = 0.0f;         // a gap row
             }
             if (r0 + i >= used) continue;
-            round_unit<E, VW>(y).store(a.out.unit<S, VW>(r0 + i, unit));
-            if constexpr (BACKWARD) round_unit<E, VW>(u).store(a.out_up.unit<S, VW>(r0 + i, unit));
+            store(a.out, r0 + i, round_unit<E, VW>(y));
+            if constexpr (BACKWARD) store(a.out_up, r0 + i, round_unit<E, VW>(u));
         }
     }
 }

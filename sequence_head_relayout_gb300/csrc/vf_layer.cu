@@ -53,10 +53,10 @@ struct Width {
         vw = 16 / size;
         return true;
     }
-    // The same in columns, for codes (M = 1,421, 1,422 and 1,420: 566 and 257, 478 and 227,
-    // 151 and 216).
-    bool any_columns() {
-        if (!any || vw > 2 || m > 32 * 32 * 2 * 8) return false;
+    // The same in units of columns (codes, M = 1,421, 1,422 and 1,420: 566 and 257, 478 and
+    // 227, 151 and 216).
+    bool any_columns(int64_t narrow, int64_t most) {
+        if (!any || vw > narrow || m > most) return false;
         vw = 16 / size;
         return true;
     }
@@ -65,13 +65,15 @@ struct Width {
 };
 // ---------------------------------------------------------------- gated activation
 
-template <class E, int VW>
+template <class E, int VW, bool ANY = false>
 void (*glu_kernel(bool backward))(vf::GluArgs) {
-    return backward ? vf::expert_glu_rows<E, VW, true> : vf::expert_glu_rows<E, VW, false>;
+    return backward ? vf::expert_glu_rows<E, VW, true, ANY>
+                    : vf::expert_glu_rows<E, VW, false, ANY>;
 }
 
 template <class E>
-void (*glu_kernel(bool backward, int64_t vw))(vf::GluArgs) {
+void (*glu_kernel(bool backward, int64_t vw, bool any))(vf::GluArgs) {
+    if (any) return glu_kernel<E, 16 / int(sizeof(typename E::S)), true>(backward);
     if constexpr (sizeof(typename E::S) == 2)
         if (vw == 8) return glu_kernel<E, 8>(backward);
     switch (vw) {
@@ -142,16 +144,22 @@ int glu(const vf_glu_desc *d, bool backward, cudaStream_t stream) {
         a.out = view(d->out, d->out_strides);
         w.take(d->out, d->out_strides);
     }
-    a.units = int32_t(d->F / w.vw);
+    // 2-byte accesses and units of columns (T = 40,000, bf16; us, activation and backward):
+    //   F = 4,095   424 258   540 401        F = 257   41 37   54 54
+    //   F = 1,421   155  98   199 159        F = 97    15 22   23 32
+    const bool any = size == 2 && d->F >= 192 && w.any_columns(1, int64_t(1) << 24);
+    a.F = int32_t(d->F);
+    a.units = int32_t(w.units(false));
     int64_t bx = 32;
     while (bx < 256 && bx < a.units) bx *= 2;
+    if (any) bx = ceil_div(ceil_div(a.units, ceil_div(a.units, 256)), 32) * 32;
     const int64_t by = 256 / bx;
     a.col_blocks = int32_t(ceil_div(a.units, bx));
-    const int64_t row_blocks =
-        std::min(ceil_div(d->rows, 2 * by), std::max<int64_t>(1, kSMs * 32 / a.col_blocks));
-    auto *kernel = d->type == VF_TYPE_BF16  ? glu_kernel<vf::Bf16>(backward, w.vw)
-                   : d->type == VF_TYPE_F16 ? glu_kernel<vf::F16>(backward, w.vw)
-                                            : glu_kernel<vf::F32>(backward, w.vw);
+    const int64_t row_blocks = std::min(ceil_div(d->rows, (any ? 1 : 2) * by),
+                                        std::max<int64_t>(1, kSMs * 32 / a.col_blocks));
+    auto *kernel = d->type == VF_TYPE_BF16  ? glu_kernel<vf::Bf16>(backward, w.vw, any)
+                   : d->type == VF_TYPE_F16 ? glu_kernel<vf::F16>(backward, w.vw, any)
+                                            : glu_kernel<vf::F32>(backward, w.vw, any);
     return launch(kernel, dim3(unsigned(row_blocks * a.col_blocks)),
                   dim3(unsigned(bx), unsigned(by)), 0, stream, a);
 }
@@ -348,7 +356,7 @@ int norm(const vf_norm_desc *d, cudaStream_t stream) {
         w.take(d->out, d->out_strides);
     }
     take_weight(&w, d);
-    const bool any = fmt ? w.any_columns() : w.any_pieces(1, 32 * 32 * 4);
+    const bool any = fmt ? w.any_columns(2, 32 * 32 * 2 * 8) : w.any_pieces(1, 32 * 32 * 4);
     a.units = int32_t(w.units(any && !fmt));
     const RowShape s = row_shape(a.units, 32, any && fmt ? 2 : 4);
     a.warps = int32_t(s.warps);

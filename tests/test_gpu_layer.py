@@ -413,6 +413,38 @@ def test_norm_at_any_address(T, M, base, gap, dtype, weight):
     assert ((a - b).cpu().double().abs() <= 2 * bound).all()
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("F,base,gap,align", [(191, 0, 0, 1), (193, 0, 0, 8), (255, 1, 0, 1),
+                                              (257, 3, 2, 5), (513, 0, 1, 1), (1421, 5, 0, 4),
+                                              (2047, 0, 0, 1), (2049, 2, 3, 1), (8191, 7, 1, 1)])
+def test_glu_at_any_address(F, base, gap, align, dtype):
+    """What lies around the rows is neither read into a result nor written."""
+    plan = make(23, 2, 5, align)
+    g, u, d = (rows_of(plan, F, dtype, i) for i in range(3))
+    nan = float("nan")
+    gp, up, dp = (Placed(t, base + i, F + gap + i, nan) for i, t in enumerate((g, u, d)))
+    outs = [Placed(torch.full_like(g, 3.0), base + 2 * i, F + gap + 1, 7.0) for i in range(3)]
+    out, dg, du = (o.view for o in outs)
+    bounds = glu_backward_bounds(d, g, u, dtype)
+    vf.expert_glu(gp.view, up.view, plan, out=out)
+    within(out, *masked(plan, *glu_bound(g, u, dtype), 3.0))
+    vf.expert_glu_backward(dp.view, gp.view, up.view, plan, grad_gate=dg, grad_up=du)
+    for got, want in zip((dg, du), bounds):
+        within(got, *masked(plan, *want, 3.0))
+    assert all(o.untouched() for o in outs)
+    # the halves of one buffer, and a gate whose rows repeat
+    both = Placed(torch.full((g.shape[0], 2 * F), 3.0, dtype=dtype), base, 2 * F + gap, 7.0)
+    vf.expert_glu_backward(dp.view, gp.view, up.view, plan, grad_gate=both.view[:, :F],
+                           grad_up=both.view[:, F:])
+    for got, want in zip((both.view[:, :F], both.view[:, F:]), bounds):
+        within(got, *masked(plan, *want, 3.0))
+    assert both.untouched()
+    first = int((plan.slot_of >= 0).int().argmax())
+    one = g[first:first + 1].expand_as(g)
+    got = vf.expert_glu(gp.view[first:first + 1].expand_as(g), up.view, plan, out=out)
+    within(got, *masked(plan, *glu_bound(one, u, dtype), 3.0))
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_norm_at_any_address_special_rows(dtype):
     """A row of NaN or infinities stays by itself where rows share their pieces."""
