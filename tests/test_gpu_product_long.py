@@ -1,0 +1,118 @@
+"""GPU tests of long sums in the experts' products: the forms of the weights' gradient
+that take a sum in parts and those whose CTAs share one, segments of any length.
+
+Whole numbers are compared bit for bit.  All operands are odd, so that no product is 0 and
+a row that is left out or read twice changes every element of the result; all partial sums
+stay below 2^24, so that float32 holds them exactly, whatever the order.
+"""
+import pytest
+import torch
+
+import sequence_head_relayout_gb300 as vf
+from oracle import experts as X
+
+pytestmark = pytest.mark.gpu
+
+DEV = torch.device("cuda:0")
+BF16, F16, F32 = torch.bfloat16, torch.float16, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    vf.lib()
+    yield
+    torch.cuda.synchronize()
+
+
+def plan_of(counts, align=1, seed=0):
+    """A plan of one slot to a token with these counts, every 40th token's dropped."""
+    e = torch.repeat_interleave(torch.arange(len(counts)), torch.tensor(counts))
+    e = torch.cat([e, torch.full((len(e) // 40,), -1)])
+    e = e[torch.randperm(len(e), generator=torch.Generator().manual_seed(seed))]
+    plan = vf.expert_plan(e[:, None].to(DEV), len(counts), align=align)
+    assert plan.counts.tolist() == list(counts)
+    return plan
+
+
+def odd(shape, dtype, seed, top=3):
+    """Odd whole numbers from -top to top."""
+    g = torch.Generator().manual_seed(seed)
+    return (2 * torch.randint(0, top + 1, shape, generator=g) - top).to(dtype)
+
+
+def odd_rows(plan, M, dtype, seed, top=3):
+    x = odd((plan.slot_of.numel(), M), dtype, seed, top)
+    x[plan.slot_of.cpu() < 0] = float("nan")
+    return x
+
+
+# The form that is chosen (by the tiles and the mean of the counts), counts, N, M, align
+FORMS = [
+    # pairs of CTAs; in float32 parts of 768 rows whose last has 1, 63, 64 and all rows
+    ("pairs", [769, 2367, 832, 1536], 260, 1300, 1),
+    ("pairs", [3000, 1, 0, 65], 392, 1288, 16),
+    # single CTAs, tiles of 256 columns: nearly all rows at one expert of few on average
+    ("single", [2400, 0, 1, 63, 64, 65, 100, 50], 260, 1300, 1),
+    ("single", [0, 5, 2560, 90, 8, 0, 31, 32], 257, 1305, 8),
+    # single CTAs, tiles of 128 columns
+    ("few", [1601, 831], 130, 200, 1),
+    ("few", [769, 2304, 0], 128, 192, 5),
+    # two CTAs share a tile's rows, unevenly, or have none
+    ("two", [4001, 2400], 130, 64, 1),
+    ("two", [6208, 64], 72, 200, 4),
+    # four CTAs do
+    ("four", [14001, 12003], 130, 64, 1),
+    ("four", [24000, 7], 72, 100, 128),
+    ("four", [6200], 129, 257, 1),
+    ("four", [0, 12500], 64, 128, 1),
+]
+
+
+def check_exact(counts, N, M, align, dtype, out_dtype):
+    plan = plan_of(counts, align)
+    g, x = odd_rows(plan, N, dtype, 1), odd_rows(plan, M, dtype, 2)
+    want, mag = X.weight_grad(g, x, plan.counts.cpu(), plan.offsets.cpu())
+    assert mag.max() < 2 ** 24
+    assert want.abs().max() < torch.finfo(out_dtype).max
+    got = vf.expert_weight_grad(g.to(DEV), x.to(DEV), plan, dtype=out_dtype)
+    assert torch.equal(got.cpu(), want.to(out_dtype))
+
+
+@pytest.mark.parametrize("dtype,out_dtype", [(BF16, F32), (F16, F32), (BF16, BF16), (F16, F16)])
+@pytest.mark.parametrize("form,counts,N,M,align", FORMS)
+def test_weight_grad_of_whole_numbers(form, counts, N, M, align, dtype, out_dtype):
+    check_exact(counts, N, M, align, dtype, out_dtype)
+
+
+def test_operands_that_need_a_copy():
+    """Odd features at any address: the same sums by way of the workspace."""
+    plan = plan_of([2311, 1])
+    g, x = odd_rows(plan, 131, BF16, 1), odd_rows(plan, 67, BF16, 2)
+    want, _ = X.weight_grad(g, x, plan.counts.cpu(), plan.offsets.cpu())
+    flat = torch.empty(g.numel() + 1, dtype=BF16, device=DEV)[1:].view(g.shape).copy_(g)
+    assert torch.equal(vf.expert_weight_grad(flat, x.to(DEV), plan, dtype=F32).cpu(),
+                       want.float())
+
+
+# Rows of an expert, N, M, the weights' view transposed: forms of one CTA with tiles of 64
+# and 128 rows, and of pairs with tiles of 128 and 256
+PRODUCTS = [(20, 200, 4100, False), (20, 200, 4104, True), (90, 100, 2056, False),
+            (90, 128, 2050, True), (100, 300, 4096, False), (100, 264, 4097, True),
+            (300, 300, 2064, False), (300, 264, 2047, True)]
+
+
+def check_product_exact(rows, N, M, transposed, align=8):
+    plan = plan_of([rows, 2 * rows, 1, 0], align)
+    x = odd_rows(plan, M, F16, 1)
+    w = odd((4, M, N) if transposed else (4, N, M), F16, 2)
+    w_cpu, w = (w.transpose(1, 2), w.to(DEV).transpose(1, 2)) if transposed else (w, w.to(DEV))
+    before = torch.full((x.shape[0], N), 3.0, dtype=F16)
+    want, mag = X.product(x, w_cpu, plan.counts.cpu(), plan.offsets.cpu(), before)
+    assert mag[:int(plan.offsets[-1])].max() < 2 ** 24
+    got = vf.expert_product(x.to(DEV), w, plan, out=before.to(DEV))
+    assert torch.equal(got.cpu(), want.half())
+
+
+@pytest.mark.parametrize("rows,N,M,transposed", PRODUCTS)
+def test_product_of_whole_numbers(rows, N, M, transposed):
+    check_product_exact(rows, N, M, transposed)
