@@ -734,10 +734,13 @@ __host__ __device__ constexpr int64_t shared_bytes(bool weights, bool split, int
 // A_MN     the first operand is stored with i contiguous
 // PARTS    sums are taken in parts of a.part_rows rows, which are added in registers
 // SPLIT    the a.split CTAs of a cluster share the sums of a tile (weights)
-template <int CTAS, bool WEIGHTS, bool A_MN, bool PARTS = false, bool SPLIT = false>
+// OUT32    the result is float32 (weights, in parts)
+template <int CTAS, bool WEIGHTS, bool A_MN, bool PARTS = false, bool SPLIT = false,
+          bool OUT32 = false>
 __global__ void __launch_bounds__(kThreads, 1)
 expert_product(const __grid_constant__ ProductArgs a) {
     static_assert(!SPLIT || (CTAS == 1 && WEIGHTS), "single CTAs share the weights' sums");
+    static_assert(!OUT32 || (PARTS && WEIGHTS), "the weights' sums in float32 are in parts");
     constexpr bool B_MN = WEIGHTS;
     constexpr int kStagingBytes = WEIGHTS ? kStagingWeights : kStagingRows;
     extern __shared__ uint8_t raw[];
@@ -879,7 +882,7 @@ expert_product(const __grid_constant__ ProductArgs a) {
             if (ok && one) mma_commit<CTAS>(smem_addr(&ctl.acc_full[acc]));
             ++it;
         }
-    } else if (PARTS && warp >= 4) {
+    } else if (OUT32 && warp >= 4) {
         const int quarter = warp % 4, turn = (warp - 4) / 4;
         uint8_t *const mine = staging + (warp - 4) * kStagingBytes;
         uint32_t it = 0;
@@ -939,58 +942,101 @@ expert_product(const __grid_constant__ ProductArgs a) {
     } else if (warp >= 4) {
         const int quarter = warp % 4, turn = (warp - 4) / 4;
         uint8_t *const mine = staging + (warp - 4) * kStagingBytes;
-        uint32_t it = 0;
+        uint32_t it = 0, d = 0;
+        bool ok = true;
         Join join;
-        for (; more; more = tiles.next(o)) {
+        // the next accumulator, and its return
+        const auto take = [&] {
             const uint32_t acc = it & 1, acc_phase = it >> 1 & 1;
-            bool ok = true;
-            if (o.kblocks > 0) {
-                // (a sum of 2^20 blocks takes a second)
-                ok = barrier_wait(smem_addr(&ctl.acc_full[acc]), acc_phase, failed,
-                                  uint64_t(o.kblocks) * 8192);
-                ok = __all_sync(kAll, int(ok));
-                fence_after();
-                ++it;
+            // (a sum of 2^20 blocks takes a second)
+            ok = barrier_wait(smem_addr(&ctl.acc_full[acc]), acc_phase, failed,
+                              uint64_t(o.kblocks) * 8192);
+            ok = __all_sync(kAll, int(ok));
+            fence_after();
+            d = tmem + acc * uint32_t(a.acc_stride) + (uint32_t(quarter * 32) << 16);
+            ++it;
+        };
+        const auto give = [&] {
+            const uint32_t acc = smem_addr(&ctl.acc_empty[(it - 1) & 1]);
+            fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if constexpr (CTAS == 1) barrier_arrive(acc);
+                else barrier_arrive_at(acc, 0);
             }
+        };
+        for (; more; more = tiles.next(o)) {
+            ok = true;
             const int f = o.f0 + int(rank) * kTileM + quarter * 32;
-            const uint32_t d = tmem + acc * uint32_t(a.acc_stride) + (uint32_t(quarter * 32) << 16);
             const int n = WEIGHTS ? min(o.n, a.cols - o.c0) : o.valid;
             // 32 columns at a time; of the weights 64, which leave together
             constexpr int kHalves = WEIGHTS ? 2 : 1, kCols = 32 * kHalves;
-            for (int c0 = kCols * turn; c0 < n; c0 += 2 * kCols) {
-                bool store = f < a.feat;             // all lanes alike
+            bool store = false;                      // all lanes alike
+            const auto leave = [&](int c0, int h, uint32_t(&v)[32]) {
+                if (h == 0) store = f < a.feat;
+                if constexpr (SPLIT)
+                    if (!join(a, ctl, reinterpret_cast<float *>(part), turn, quarter, lane,
+                              tiles.slice, c0 / 128 % a.split, failed,
+                              uint64_t(o.kblocks) * 8192, ok, v))
+                        store = false;
+                if constexpr (WEIGHTS) {
+                    if (store) stage_weights16(a, v, h, lane, mine);
+                    if (store && h == 1) store_weights16(a, o.e, f, o.c0 + c0, lane, mine);
+                } else {
+                    if (store) store_rows(a, v, int64_t(o.row0) + c0, n - c0, f, lane, mine);
+                }
+            };
+            if (PARTS && tiles.inside) {
+                // a sum of several parts: half of the columns in registers
+                float sum[4][32] = {};
+                bool all = true;
+                while (true) {
+                    take();
+                    all = all && ok;
 #pragma unroll
-                for (int h = 0; h < kHalves; ++h) {
-                    const int c = c0 + 32 * h;
-                    uint32_t v[32];
-                    if (o.kblocks > 0 && ok && c < n) {
+                    for (int i = 0; i < 8; ++i) {
+                        const int c = kCols * (2 * (i / 2 / kHalves) + turn) +
+                                      32 * (i / 2 % kHalves) + 16 * (i % 2);
+                        uint32_t v[16];
+                        if (!ok || c >= n) continue;
                         tmem_load(d + uint32_t(c), v);
-                    } else {
-                        // an empty sum, or one that was given up: NaN
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) v[j] = ok ? 0u : 0x7FC00000u;
+                        for (int j = 0; j < 16; ++j)
+                            sum[i / 2][16 * (i % 2) + j] += __uint_as_float(v[j]);
                     }
-                    if constexpr (SPLIT)
-                        if (!join(a, ctl, reinterpret_cast<float *>(part), turn, quarter, lane,
-                                  tiles.slice, c0 / 128 % a.split, failed,
-                                  uint64_t(o.kblocks) * 8192, ok, v))
-                            store = false;
-                    if constexpr (WEIGHTS) {
-                        if (store) stage_weights16(a, v, h, lane, mine);
-                    } else {
-                        if (store) store_rows(a, v, int64_t(o.row0) + c, n - c, f, lane, mine);
+                    if (ok) give();
+                    if (!tiles.inside) break;
+                    tiles.next(o);
+                }
+                ok = all;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int c0 = kCols * (2 * (i / kHalves) + turn);
+                    if (c0 >= n) continue;
+                    uint32_t v[32];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        v[j] = ok ? __float_as_uint(sum[i][j]) : 0x7FC00000u;
+                    leave(c0, i % kHalves, v);
+                }
+            } else {
+                if (o.kblocks > 0) take();
+                for (int c0 = kCols * turn; c0 < n; c0 += 2 * kCols) {
+#pragma unroll
+                    for (int h = 0; h < kHalves; ++h) {
+                        const int c = c0 + 32 * h;
+                        uint32_t v[32];
+                        if (o.kblocks > 0 && ok && c < n) {
+                            tmem_load(d + uint32_t(c), v);
+                        } else {
+                            // an empty sum, or one that was given up: NaN
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) v[j] = ok ? 0u : 0x7FC00000u;
+                        }
+                        leave(c0, h, v);
                     }
                 }
-                if constexpr (WEIGHTS)
-                    if (store) store_weights16(a, o.e, f, o.c0 + c0, lane, mine);
-            }
-            if (o.kblocks > 0 && ok) {
-                fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    if constexpr (CTAS == 1) barrier_arrive(smem_addr(&ctl.acc_empty[acc]));
-                    else barrier_arrive_at(smem_addr(&ctl.acc_empty[acc]), 0);
-                }
+                if (o.kblocks > 0 && ok) give();
             }
             if (!WEIGHTS && o.gap > 0 && f < a.feat && turn == 0)
                 zero_rows(a, int64_t(o.row0) + o.valid, o.gap, f, lane);

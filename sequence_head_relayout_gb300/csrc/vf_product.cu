@@ -256,6 +256,18 @@ int64_t workspace_of(const Operand &a, const Operand &b) {
     return n < 0 || m < 0 || !add_ok(n, m, &sum) ? VF_ERR_OVERFLOW : sum;
 }
 
+// The longest sum of one accumulation.  The tensor cores cut off what lies below an
+// accumulator's last bit, always towards zero, so that a sum's error grows with its length:
+// terms of one sign lose some 2 units of 2^-23 with every 16, 4.5e-6 of the result at 768
+// terms, 3e-5 at 4,096, 2.4e-4 at 32,768 (terms of both signs a tenth of that and less).
+// Longer sums are taken in parts that are added with rounding.  Of a 16-bit result a part
+// loses an eighth of the smallest half unit at most (fp16 2^-12, bf16 2^-9); a float32
+// result is as near as parts of 768 make it: T = 4,096, K = 8, E = 32, N = 4,096, M = 2,048
+// takes 384 us in one part, 397 in parts of 768 rows, 415 in parts of 512.
+int64_t part_of(const vf_product_desc *d, bool out32) {
+    return out32 ? 768 : d->type == VF_TYPE_F16 ? 4096 : 32768;
+}
+
 // The form by the rows that an expert has on average.  Measured with E = 64,
 // N = 4,096, M = 2,048 (us; forms by CTAs and rows of a tile):
 //   rows    1 x 32   1 x 64   1 x 128   2 x 128   2 x 256
@@ -364,6 +376,13 @@ Form weights_form(const vf_product_desc *d) {
     return f;
 }
 
+template <int CTAS, bool SPLIT>
+Kernel weights_kernel(bool parts, bool out32) {
+    return out32   ? vfp::expert_product<CTAS, true, true, true, SPLIT, true>
+           : parts ? vfp::expert_product<CTAS, true, true, true, SPLIT>
+                   : vfp::expert_product<CTAS, true, true, false, SPLIT>;
+}
+
 int weight_grad(const vf_product_desc *d, cudaStream_t stream) {
     int rc = check_desc(d);
     if (rc != VF_OK) return rc;
@@ -389,13 +408,10 @@ int weight_grad(const vf_product_desc *d, cudaStream_t stream) {
     a.cols = int32_t(d->M);
     a.out = d->grad_weights;
     const bool out32 = d->out_type == VF_TYPE_F32;
-    // The tensor cores cut off what lies below an accumulator's last bit, always towards
-    // the same side, so that a sum's error grows with its length: 1.2e-6 of the result
-    // at 1,024 rows.  Sums in float32 are therefore taken in parts, which are added with
-    // rounding: some 7e-7 whatever the length.  T = 4,096, K = 8, E = 32, N = 4,096,
-    // M = 2,048 takes 384 us in one part, 397 in parts of 768 rows, 415 in parts of 512.
-    // (The 16-bit types round a thousand times as coarsely.)
-    a.part_rows = out32 ? 768 : INT32_MAX;
+    // Where an expert can have more rows than a part, the sums are taken in parts.
+    const int64_t part = part_of(d, out32);
+    const bool parts = out32 || d->rows > part;
+    a.part_rows = int32_t(part);
     a.vec = d->M % (16 / size) == 0 && aligned16(d->grad_weights);
     const Form f = weights_form(d);
     set_form(&a, f);
@@ -412,12 +428,9 @@ int weight_grad(const vf_product_desc *d, cudaStream_t stream) {
             return rc;
     }
     const Kernel kernel =
-        f.ctas == 2    ? (out32 ? vfp::expert_product<2, true, true, true>
-                                  : vfp::expert_product<2, true, true>)
-        : f.split == 1 ? (out32 ? vfp::expert_product<1, true, true, true>
-                                  : vfp::expert_product<1, true, true>)
-                       : (out32 ? vfp::expert_product<1, true, true, true, true>
-                                  : vfp::expert_product<1, true, true, false, true>);
+        f.ctas == 2    ? weights_kernel<2, false>(parts, out32)
+        : f.split == 1 ? weights_kernel<1, false>(parts, out32)
+                       : weights_kernel<1, true>(parts, out32);
     return launch_product(kernel, a, f, int64_t(a.feat_tiles) * a.col_tiles * a.E, stream);
 }
 

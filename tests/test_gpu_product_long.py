@@ -84,6 +84,54 @@ def test_weight_grad_of_whole_numbers(form, counts, N, M, align, dtype, out_dtyp
     check_exact(counts, N, M, align, dtype, out_dtype)
 
 
+# Segments of one and of several parts of a 16-bit result (4,096 rows of fp16, 32,768 of
+# bf16) that end 0, 1, 63 and 64 rows into one, in every form
+LONG = [
+    ("pairs", [4097, 33000, 20, 8255], 260, 1300, 1),
+    ("single", [16449, 100, 2, 4160, 90, 4096] + [7] * 58, 64, 300, 8),
+    ("few", [4160, 4097, 1], 257, 300, 1),
+    ("two", [8321], 600, 1300, 4),
+    ("four", [0, 32832, 20, 0, 300, 8193], 100, 100, 1),
+    ("four", [140001], 72, 65, 1),
+]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("form,counts,N,M,align", LONG)
+def test_long_segments_of_whole_numbers(form, counts, N, M, align, dtype):
+    check_exact(counts, N, M, align, dtype, dtype)
+
+
+PART = {(F16, F16): 4096, (BF16, BF16): 32768, (F16, F32): 768}
+
+
+def drift(n, part):
+    """Bound of the relative error of a sum of n like terms of one sign in float32: those of
+    a part are added by additions that round or cut off, term i at most one unit, 2^-23, of
+    the i terms there are; the parts with rounding, half a unit each."""
+    return (min(n, part) + 1) / 2 * 2.0 ** -23 + -(-n // part) * 2.0 ** -24
+
+
+def half_units(want, dtype):
+    """The relative error that one rounding may make."""
+    exponent = torch.frexp(want).exponent.double() - 1
+    return 2.0 ** exponent * torch.finfo(dtype).eps / 2 / want
+
+
+@pytest.mark.parametrize("n,dtype,out_dtype", [(1 << 20, F16, F16), (60001, F16, F32)])
+def test_weight_grad_does_not_drift(n, dtype, out_dtype):
+    """What the additions cut off is always of one sign: with terms of one sign it adds up,
+    but for the parts."""
+    g = torch.Generator(device=DEV).manual_seed(1)
+    a = (torch.rand((n, 72), generator=g, device=DEV) + 1).to(dtype)
+    b = ((torch.rand((n, 64), generator=g, device=DEV) + 1) * 2.0 ** -8).to(dtype)
+    plan = vf.expert_plan(torch.zeros((n, 1), dtype=torch.int64, device=DEV), 1)
+    got = vf.expert_weight_grad(a, b, plan, dtype=out_dtype)[0].double()
+    want = a.double().t() @ b.double()                     # float64: 2^-53 of n is nothing
+    bound = drift(n, PART[dtype, out_dtype]) + half_units(want, out_dtype)
+    assert ((got - want).abs() / want <= bound).all()
+
+
 def test_operands_that_need_a_copy():
     """Odd features at any address: the same sums by way of the workspace."""
     plan = plan_of([2311, 1])
