@@ -491,9 +491,12 @@ int vf_expert_merge_backward(const vf_expert_desc *desc, vf_stream_t stream);
  * weights' view transposed (n and m exchanged).
  *
  * Elements are VF_TYPE_BF16 or VF_TYPE_F16.  Products are exact and summed in
- * float32 in an order that is fixed for given sizes (by tensor cores, whose
- * additions may drop bits below an accumulator's last), and each output is rounded
- * once, to nearest even.  Equal calls give equal bits.
+ * float32 in an order that is fixed for given sizes, and each output is rounded
+ * once, to nearest even.  Equal calls give equal bits.  The additions are the tensor
+ * cores', which drop bits below an accumulator's last and so lose towards zero; sums are
+ * taken in parts that are added with rounding, short enough that a part of terms of one
+ * sign loses an eighth of the type's smallest half unit at most (4,096 terms of
+ * VF_TYPE_F16, 32,768 of VF_TYPE_BF16), or 5e-6 of a float32 result (768).
  * Rows that hold no slot are never read into a result.  Of out, gap rows are
  * written as zeros and rows at and behind offsets[E] left as they were; an expert
  * without rows gets zeros in grad_weights, and its weights are not read.

@@ -65,7 +65,7 @@ struct ProductArgs {
     int32_t E, rows;
     int32_t feat, cols, red;      // features; weights: columns; rows: length of the sums
     int32_t feat_tiles, col_tiles;
-    int32_t part_rows;            // weights: most rows of one accumulation
+    int32_t part;                 // most rows (rows form: features) of one accumulation
     int32_t step_experts, step_tiles;    // weights: the grid's tiles, in experts and the rest
     int32_t tile_n;               // most rows (columns) of a tile
     int32_t split;                // CTAs that share the sums of a tile
@@ -351,17 +351,18 @@ struct Tile {
     int e, f0;         // expert, first feature
     int row0, valid;   // first row and rows of the tile; weights: of this part of the sum
     int c0;            // weights: first column
+    int k0;            // rows form in parts: first feature of this part of the sum
     int n;             // rows or columns of the product, a multiple of 16 CTAS
     int kblocks;
     int gap;           // rows to be written as zeros behind the tile
-    bool more;         // weights: a later part of the sum
+    bool more;         // a later part of the sum
 };
 
 // The CTA's (pair's) tiles, by all lanes of a warp together.  Rows form: the
 // experts' tiles in order, an expert's row tiles fastest (they share a tile of
 // weights), each expert's rows cut into equal tiles.  A lane holds four experts, a
 // warp 128 at a time.
-template <int CTAS, bool WEIGHTS, bool SPLIT>
+template <int CTAS, bool WEIGHTS, bool PARTS, bool SPLIT>
 struct Tiles {
     static constexpr int kStep = 16 * CTAS;
     const ProductArgs &a;
@@ -377,7 +378,8 @@ struct Tiles {
     int e, in, each;
     int next_offset, next_count;  // of the next tile's expert, loaded a tile ahead
     int slice = 0;                // SPLIT: this CTA's of a.split shares of the sums
-    int row0, rest;               // what is left of the expert's rows (sums in parts)
+    int row0, rest;               // what is left of the expert's rows (sums in parts), or
+                                  // of the features
     bool inside = false;
 
     __device__ __forceinline__ explicit Tiles(const ProductArgs &args)
@@ -415,6 +417,7 @@ struct Tiles {
         o.e = uniform(o.e);
         o.f0 = uniform(o.f0);
         o.c0 = uniform(o.c0);
+        o.k0 = uniform(o.k0);
         o.row0 = uniform(o.row0);
         o.valid = uniform(o.valid);
         o.n = uniform(o.n);
@@ -453,7 +456,7 @@ struct Tiles {
             ahead();
         }
         o.row0 = row0;
-        o.valid = min(rest, a.part_rows);
+        o.valid = min(rest, a.part);
         o.kblocks = parts(o.valid, kBlockK);
         row0 += o.valid;
         rest -= o.valid;
@@ -461,7 +464,21 @@ struct Tiles {
         return true;
     }
 
+    // The next part of a tile's sums; parts are whole blocks.
+    __device__ __forceinline__ void next_part(Tile &o, bool first) {
+        o.more = !first;
+        o.k0 = first ? 0 : o.k0 + a.part;
+        rest = first ? a.red : rest - a.part;
+        o.kblocks = parts(min(rest, a.part), kBlockK);
+        inside = rest > a.part;
+    }
+
     __device__ __forceinline__ bool next_rows(Tile &o) {
+        if constexpr (PARTS)
+            if (inside) {
+                next_part(o, false);
+                return true;
+            }
         while (t >= before + total) {
             base += 128;
             if (base >= a.E) return false;
@@ -510,7 +527,8 @@ struct Tiles {
         o.valid = min(part, c - r * part);
         o.n = (o.valid + kStep - 1) / kStep * kStep;
         o.c0 = 0;
-        o.kblocks = parts(a.red, kBlockK);
+        if constexpr (PARTS) next_part(o, true);
+        else o.kblocks = parts(a.red, kBlockK);
         o.gap = 0;
         if (a.gaps && r == row_tiles - 1)
             o.gap = max(0, min(a.offsets[o.e + 1], a.rows) - (b + c));
@@ -732,7 +750,7 @@ __host__ __device__ constexpr int64_t shared_bytes(bool weights, bool split, int
 // CTAS     CTAs that share a tile (2: a pair, 256 features, each CTA holds half of B)
 // WEIGHTS  the weights' gradient, else the rows' product
 // A_MN     the first operand is stored with i contiguous
-// PARTS    sums are taken in parts of a.part_rows rows, which are added in registers
+// PARTS    sums are taken in parts of a.part terms, which are added in registers
 // SPLIT    the a.split CTAs of a cluster share the sums of a tile (weights)
 // OUT32    the result is float32 (weights, in parts)
 template <int CTAS, bool WEIGHTS, bool A_MN, bool PARTS = false, bool SPLIT = false,
@@ -773,7 +791,7 @@ expert_product(const __grid_constant__ ProductArgs a) {
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    Tiles<CTAS, WEIGHTS, SPLIT> tiles(a);
+    Tiles<CTAS, WEIGHTS, PARTS, SPLIT> tiles(a);
     Tile o = {};
     bool more = tiles.next(o);
     fence_before();
@@ -812,7 +830,7 @@ expert_product(const __grid_constant__ ProductArgs a) {
                 if (!ok) break;
                 const uint32_t bar = bars + s * 8;
                 const uint32_t da = ring + s * a.stage_bytes, db = da + kStageA;
-                const int k = kb * kBlockK;
+                const int k = kb * kBlockK + (PARTS && !WEIGHTS ? o.k0 : 0);
                 // Weights form: the last block's rows lie at its end, behind zeros: the
                 // maps' second coordinate runs over the same rows as the third, so that
                 // what lies before it is outside the tensor.
@@ -948,9 +966,7 @@ expert_product(const __grid_constant__ ProductArgs a) {
         // the next accumulator, and its return
         const auto take = [&] {
             const uint32_t acc = it & 1, acc_phase = it >> 1 & 1;
-            // (a sum of 2^20 blocks takes a second)
-            ok = barrier_wait(smem_addr(&ctl.acc_full[acc]), acc_phase, failed,
-                              uint64_t(o.kblocks) * 8192);
+            ok = barrier_wait(smem_addr(&ctl.acc_full[acc]), acc_phase, failed);
             ok = __all_sync(kAll, int(ok));
             fence_after();
             d = tmem + acc * uint32_t(a.acc_stride) + (uint32_t(quarter * 32) << 16);

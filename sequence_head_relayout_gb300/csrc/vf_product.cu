@@ -284,6 +284,14 @@ Form rows_form(const vf_product_desc *d) {
     return mean <= 112 ? Form{2, 128, 16} : Form{2, 256, 32};
 }
 
+template <int CTAS>
+Kernel rows_kernel(bool mn, bool parts) {
+    return parts ? (mn ? vfp::expert_product<CTAS, false, true, true>
+                       : vfp::expert_product<CTAS, false, false, true>)
+                 : (mn ? vfp::expert_product<CTAS, false, true>
+                       : vfp::expert_product<CTAS, false, false>);
+}
+
 int product(const vf_product_desc *d, cudaStream_t stream) {
     int rc = check_desc(d);
     if (rc != VF_OK) return rc;
@@ -333,10 +341,10 @@ int product(const vf_product_desc *d, cudaStream_t stream) {
                 rc = make_map(&a.b_maps[i], a.bf16, 2, x.p, dims, str, (i + 1) * f.box);
         if (rc != VF_OK) return rc;
     }
-    const Kernel kernel =
-        f.ctas == 2
-            ? (mn ? vfp::expert_product<2, false, true> : vfp::expert_product<2, false, false>)
-            : (mn ? vfp::expert_product<1, false, true> : vfp::expert_product<1, false, false>);
+    const int64_t part = part_of(d, false);
+    a.part = int32_t(part);
+    const Kernel kernel = f.ctas == 2 ? rows_kernel<2>(mn, d->M > part)
+                                      : rows_kernel<1>(mn, d->M > part);
     const int64_t most = std::min(d->E, d->rows);          // experts that have rows
     return launch_product(kernel, a, f, a.feat_tiles * (most + d->rows / f.tile_n), stream);
 }
@@ -411,7 +419,7 @@ int weight_grad(const vf_product_desc *d, cudaStream_t stream) {
     // Where an expert can have more rows than a part, the sums are taken in parts.
     const int64_t part = part_of(d, out32);
     const bool parts = out32 || d->rows > part;
-    a.part_rows = int32_t(part);
+    a.part = int32_t(part);
     a.vec = d->M % (16 / size) == 0 && aligned16(d->grad_weights);
     const Form f = weights_form(d);
     set_form(&a, f);

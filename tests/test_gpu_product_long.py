@@ -149,18 +149,50 @@ PRODUCTS = [(20, 200, 4100, False), (20, 200, 4104, True), (90, 100, 2056, False
             (300, 300, 2064, False), (300, 264, 2047, True)]
 
 
-def check_product_exact(rows, N, M, transposed, align=8):
+def check_product_exact(rows, N, M, transposed, dtype=F16, align=8):
     plan = plan_of([rows, 2 * rows, 1, 0], align)
-    x = odd_rows(plan, M, F16, 1)
-    w = odd((4, M, N) if transposed else (4, N, M), F16, 2)
+    x = odd_rows(plan, M, dtype, 1)
+    w = odd((4, M, N) if transposed else (4, N, M), dtype, 2)
     w_cpu, w = (w.transpose(1, 2), w.to(DEV).transpose(1, 2)) if transposed else (w, w.to(DEV))
-    before = torch.full((x.shape[0], N), 3.0, dtype=F16)
+    before = torch.full((x.shape[0], N), 3.0, dtype=dtype)
     want, mag = X.product(x, w_cpu, plan.counts.cpu(), plan.offsets.cpu(), before)
     assert mag[:int(plan.offsets[-1])].max() < 2 ** 24
+    assert want.abs().max() < torch.finfo(dtype).max
     got = vf.expert_product(x.to(DEV), w, plan, out=before.to(DEV))
-    assert torch.equal(got.cpu(), want.half())
+    assert torch.equal(got.cpu(), want.to(dtype))
 
 
 @pytest.mark.parametrize("rows,N,M,transposed", PRODUCTS)
 def test_product_of_whole_numbers(rows, N, M, transposed):
     check_product_exact(rows, N, M, transposed)
+
+
+# Features of several parts (4,096 of fp16, 32,768 of bf16) that end 1 to 64 into one
+@pytest.mark.parametrize("rows,N,M,transposed,dtype", [
+    (20, 200, 8200, False, F16), (20, 136, 12289, True, F16), (90, 100, 8256, False, F16),
+    (90, 128, 8192, True, F16), (100, 300, 8255, False, F16), (100, 264, 4160, True, F16),
+    (300, 300, 12352, False, F16), (300, 264, 8193, True, F16),
+    (20, 72, 32769, False, BF16), (20, 72, 65600, True, BF16), (100, 200, 32832, False, BF16),
+    (300, 136, 33000, True, BF16)])
+def test_product_of_many_whole_numbers(rows, N, M, transposed, dtype):
+    check_product_exact(rows, N, M, transposed, dtype)
+
+
+@pytest.mark.parametrize("transposed", [False, True])
+@pytest.mark.parametrize("rows", [6, 300])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_product_does_not_drift(rows, dtype, transposed):
+    M, N = 1 << 20, 72
+    g = torch.Generator(device=DEV).manual_seed(1)
+    x = (torch.rand((rows, M), generator=g, device=DEV) + 1).to(dtype)
+    w = torch.rand((1, M, N) if transposed else (1, N, M), generator=g, device=DEV)
+    w = ((w + 1) * 2.0 ** -8).to(dtype)
+    w = w.transpose(1, 2) if transposed else w
+    plan = vf.expert_plan(torch.zeros((rows, 1), dtype=torch.int64, device=DEV), 1)
+    got = vf.expert_product(x, w, plan).double()
+    want = torch.zeros_like(got)
+    for k in range(0, M, M // 8):
+        mine = slice(k, k + M // 8)
+        want += x[:, mine].double() @ w[0, :, mine].double().t()
+    bound = drift(M, PART[dtype, dtype]) + half_units(want, dtype)
+    assert ((got - want).abs() / want <= bound).all()
