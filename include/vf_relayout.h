@@ -514,8 +514,10 @@ int vf_expert_merge_backward(const vf_expert_desc *desc, vf_stream_t stream);
  * with rows have, of the rows those below offsets[E]): vf_expert_*_workspace() bytes,
  * 16-byte aligned device memory, one for each of the calls that may run at the same time.
  * A call that needs it and is given NULL returns VF_ERR_CAPACITY.
- * A kernel whose internal wait lasts for seconds, which only a failing device can
- * bring about, writes NaN to what it has not stored yet.
+ * A kernel whose warps wait for one another for two seconds of its running time (what a
+ * switched-out context misses does not count) gives up and writes NaN to what it has not
+ * stored yet.  Nothing but a failing device, or a debugger that holds some of its threads,
+ * brings that about; the call has returned by then, and no status tells of it.
  */
 typedef struct vf_product_desc {
     int32_t type;               /* VF_TYPE_BF16 or VF_TYPE_F16 */

@@ -19,6 +19,7 @@ DEPS = SOURCES + [os.path.join(CSRC, n) for n in ("relayout_kernel.cuh", "launch
                                                   "tiled_kernel.cuh", "quant_kernel.cuh",
                                                   "quant.h", "checks.h", "call.h",
                                                   "product_kernel.cuh", "layer_kernel.cuh", "shift.cuh",
+                                                  "wait.h",
                                                   "expert_kernel.cuh", "expert_q_kernel.cuh")] \
     + [os.path.join(ROOT, "include", "vf_relayout.h")]
 LIB = os.path.join(PKG, "libvf_relayout.so")

@@ -29,8 +29,8 @@
 //   weights  T = 4,096, K = 8, E = 32, 4,096 x 2,048       321 us   1.71 PFLOP/s
 //                                    in float32            391 us   1.41 PFLOP/s
 //
-// No wait is without an end: a role that waits for kWaitNs gives up, sets the
-// CTA's flag, and what is still to be stored is stored as NaN.
+// No wait is without an end: a role that waits for kWaitNs of the kernel's own time
+// (wait.h) gives up, sets the CTA's flag, and what is still to be stored is stored as NaN.
 #pragma once
 
 #include <cuda.h>
@@ -40,6 +40,7 @@
 #include <cstdint>
 
 #include "shift.cuh"
+#include "wait.h"
 
 namespace vfp {
 
@@ -53,7 +54,6 @@ constexpr int kEpilogueWarps = 8;              // two for each quarter of the ti
 constexpr int kStagingRows = 2048, kStagingWeights = 4608;
 constexpr int kPartBytes = 2 * 32 * kTileM * 4; // SPLIT: 32 columns of each turn's, in float32
 constexpr int kThreads = 32 * (4 + kEpilogueWarps);
-constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr uint64_t kDrainNs = 100000000ull;
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 
@@ -114,27 +114,22 @@ __device__ __forceinline__ bool barrier_test(uint32_t bar, uint32_t parity) {
     return done != 0;
 }
 
-// Waits for the phase of the given parity to end, for kWaitNs at most (and more_ns
-// for what may be due in between); false when it gave up, or another role did.
-__device__ __forceinline__ bool barrier_wait(uint32_t bar, uint32_t parity, volatile int *failed,
-                                             uint64_t more_ns = 0) {
+// Waits for the phase of the given parity to end; false when it gave up, or another
+// role did.
+__device__ __forceinline__ bool barrier_wait(uint32_t bar, uint32_t parity,
+                                             volatile int *failed) {
     for (int i = 0; i < 64; ++i)
         if (barrier_try(bar, parity)) return true;
-    const uint64_t start = now_ns();
-    while (!barrier_try(bar, parity)) {
-        if (*failed) return false;
-        if (now_ns() - start > kWaitNs + more_ns) {
-            *failed = 1;
-            return false;
-        }
-    }
-    return true;
+    const bool done = wait_until([&] { return barrier_try(bar, parity); },
+                                 [&] { return *failed != 0; }, [] { return now_ns(); });
+    if (!done) *failed = 1;
+    return done;
 }
 
 // The same by a whole warp, `ready`: the result of an earlier test.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *failed,
-                                          bool ready = false, uint64_t more_ns = 0) {
-    if (!ready) ready = barrier_wait(bar, parity, failed, more_ns);
+                                          bool ready = false) {
+    if (!ready) ready = barrier_wait(bar, parity, failed);
     return __all_sync(kAll, int(ready));
 }
 
@@ -703,12 +698,12 @@ struct Join {
 
     __device__ __forceinline__ bool operator()(const ProductArgs &a, Control &ctl, float *part,
                                                int turn, int quarter, int lane, int slice,
-                                               int owner, volatile int *failed,
-                                               uint64_t more_ns, bool &ok, uint32_t (&v)[32]) {
+                                               int owner, volatile int *failed, bool &ok,
+                                               uint32_t (&v)[32]) {
         const uint32_t full = smem_addr(&ctl.part_full[turn]);
         const uint32_t empty = smem_addr(&ctl.part_empty[turn]);
         if (chunk > 0 && ok) {
-            ok = warp_wait(empty, (chunk - 1) & 1, failed, false, more_ns);
+            ok = warp_wait(empty, (chunk - 1) & 1, failed);
             asm volatile("fence.acq_rel.cluster;" ::: "memory");
         }
         ++chunk;
@@ -718,7 +713,7 @@ struct Join {
         __syncwarp();
         if (lane == 0) barrier_arrive_at(full, uint32_t(owner));
         if (slice != owner) return false;
-        if (ok) ok = warp_wait(full, owned & 1, failed, false, more_ns);
+        if (ok) ok = warp_wait(full, owned & 1, failed);
         asm volatile("fence.acq_rel.cluster;" ::: "memory");
         ++owned;
 #pragma unroll
@@ -951,7 +946,7 @@ expert_product(const __grid_constant__ ProductArgs a) {
                     v[j] = ok ? __float_as_uint(sum[i][j]) : 0x7FC00000u;
                 if constexpr (SPLIT)
                     if (!join(a, ctl, reinterpret_cast<float *>(part), turn, quarter, lane,
-                              tiles.slice, i % a.split, failed, uint64_t(o.kblocks) * 8192, ok, v))
+                              tiles.slice, i % a.split, failed, ok, v))
                         continue;
                 if (f >= a.feat) continue;
                 store_weights32(a, v, o.e, f, o.c0 + c, lane, mine);
@@ -992,8 +987,7 @@ expert_product(const __grid_constant__ ProductArgs a) {
                 if (h == 0) store = f < a.feat;
                 if constexpr (SPLIT)
                     if (!join(a, ctl, reinterpret_cast<float *>(part), turn, quarter, lane,
-                              tiles.slice, c0 / 128 % a.split, failed,
-                              uint64_t(o.kblocks) * 8192, ok, v))
+                              tiles.slice, c0 / 128 % a.split, failed, ok, v))
                         store = false;
                 if constexpr (WEIGHTS) {
                     if (store) stage_weights16(a, v, h, lane, mine);
