@@ -859,6 +859,10 @@ expert_product(const __grid_constant__ ProductArgs a) {
                 advance();
             }
         }
+        // The products of the last blocks still arrive at the stages' barriers, of a pair
+        // at those of both CTAs: neither leaves before they have.
+        for (int i = 0; ok && i < a.stages; ++i, advance())
+            ok = warp_wait(empty + s * 8, phase ^ 1, failed);
     } else if (warp == 1 && rank == 0) {
         // products; one thread issues them
         const uint32_t instr = (1u << 4) | (a.bf16 ? (1u << 7) | (1u << 10) : 0u) |
