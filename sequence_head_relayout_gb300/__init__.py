@@ -1167,6 +1167,11 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
     and ``total`` may be any non-overlapping [T,M] views.  No graph is recorded (the
     gradients are :func:`rms_norm_backward`): tensors that require a gradient are
     refused while grad mode is on.
+
+    Rows that all start at multiples of 16 bytes give the same bits in any batch.  Where
+    they do not (M odd, odd row strides), a row's last bits may go by its address, and views
+    that lie otherwise than x (a residual that is a slice of wider rows) are read element
+    by element, which takes about twice as long; so does a weight at no such multiple.
     """
     typ, wtyp, T, M = _norm(x, weight)
     total, sums = _norm_inputs(x, weight, residual, total, stream)

@@ -22,7 +22,9 @@ vf::View view(const void *p, const int64_t str[2]) {
 }
 
 // Widest unit (elements) that keeps every access of the views aligned; and whether their
-// rows can be taken at any address, in pieces of 16 bytes, and lie in them alike.
+// rows can be taken at any address, in pieces of 16 bytes, and lie in them alike.  The stride
+// of a single row counts too (where it is one, not a smaller number of no use): a norm's
+// order of summing goes by all this, and is to be the same for view[:1] and view[:2].
 struct Width {
     int64_t size, n, m, vw;
     bool any = true, alike = true;
@@ -34,11 +36,12 @@ struct Width {
     void take(const void *p, const int64_t str[2]) {
         if (p == nullptr) return;
         const int64_t at = int64_t(reinterpret_cast<uintptr_t>(p) % 16);
-        const int64_t step = n > 1 ? str[0] % (16 / size) : 0;
+        const int64_t row = n > 1 || str[0] >= m ? str[0] : 0;
+        const int64_t step = row % (16 / size);
         if (first < 0) first = at, stride = step;
         else if (at != first || step != stride) alike = false;
         if (str[1] != 1 && m > 1) vw = 1, any = false;
-        while (vw > 1 && (at % (vw * size) || (n > 1 && str[0] % vw))) vw /= 2;
+        while (vw > 1 && (at % (vw * size) || row % vw)) vw /= 2;
     }
     // Rows in pieces, where accesses would have at most `narrow` elements and a block holds
     // the units.  With narrow accesses and in pieces (T = 40,000, with a residual or
@@ -260,7 +263,7 @@ void take_weight(Width *w, const vf_norm_desc *d) {
         w->vw /= 2;
 }
 
-// Units of a lane and warps of a row: by the row alone, so that its result does not
+// Units of a lane and warps of a row: by the row's units alone, so that its result does not
 // depend on how many others there are.
 struct RowShape {
     int64_t nv, warps, rows;       // rows of a block
