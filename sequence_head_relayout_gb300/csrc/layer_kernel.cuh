@@ -328,6 +328,7 @@ template <class E, int VW, bool BACKWARD, bool ANY>
 __global__ void __launch_bounds__(256)
 expert_glu_rows(const __grid_constant__ GluArgs a) {
     using S = typename E::S;
+    static_assert(!ANY || (sizeof(S) == 2 && VW == 8), "units of 16 bytes");
     constexpr int U = ANY ? 1 : 2;
     wait_for_previous_grid();
     const int used = min(max(a.offsets[a.E], 0), a.rows);
@@ -861,6 +862,7 @@ norm_backward_rows(const __grid_constant__ NormArgs a) {
     using S = typename E::S;
     using U = Unit<S, VW>;
     constexpr bool kCopies = copies_rows(int(sizeof(S)), VW, NV, ANY);
+    static_assert(kCopies || !ANY, "rows at any address are copied");
     __shared__ float2 parts[2][32];
     // [kNormStages][h, g, more][NV][threads] units; ANY: the weight's, [VW / 4][NV][threads]
     // in float32 or [NV][threads]
@@ -892,8 +894,7 @@ norm_backward_rows(const __grid_constant__ NormArgs a) {
     };
     const auto load = [&](const View &view, int j) {
         U u;
-        if constexpr (ANY) u.b = PieceRow(view, t, a.T, a.M, S()).load(unit_of(j));
-        else u.load(view.unit<const S, VW>(t, unit_of(j)));
+        u.load(view.unit<const S, VW>(t, unit_of(j)));
         return u;
     };
     uint4 *const weights = dynamic + (kCopies ? kNormStages * 3 * NV * step : 0) + threadIdx.x;

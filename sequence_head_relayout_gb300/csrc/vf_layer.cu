@@ -76,9 +76,10 @@ void (*glu_kernel(bool backward))(vf::GluArgs) {
 
 template <class E>
 void (*glu_kernel(bool backward, int64_t vw, bool any))(vf::GluArgs) {
-    if (any) return glu_kernel<E, 16 / int(sizeof(typename E::S)), true>(backward);
-    if constexpr (sizeof(typename E::S) == 2)
+    if constexpr (sizeof(typename E::S) == 2) {            // (any: 2-byte accesses otherwise)
+        if (any) return glu_kernel<E, 8, true>(backward);
         if (vw == 8) return glu_kernel<E, 8>(backward);
+    }
     switch (vw) {
         case 4: return glu_kernel<E, 4>(backward);
         case 2: return glu_kernel<E, 2>(backward);
