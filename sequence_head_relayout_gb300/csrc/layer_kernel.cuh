@@ -313,13 +313,24 @@ struct GluArgs {
     int32_t col_blocks;
 };
 
-// s(g).  For 16-bit elements the fast exponential and division do: off by some
-// 2^-20 at |g| = 10, where a rounding to the type is 2^-9 or 2^-12 (with the full ones
-// the activation of 110,828 rows, F = 2,048, took 238 us at 201 of HBM's).
+// s(g) = 1 / (1 + e), times e where g is negative, with e = exp(-|g|): exp(-g) overflows from
+// g = -88.7 on, where s has not left float32 and the other factors may bring it far above
+// its smallest values.  For 16-bit elements the fast exponential and reciprocal (of 1 to 2:
+// off by one unit) do: off by some 2^-20 at |g| = 10, where a rounding to the type is 2^-9
+// or 2^-12 (with the full ones the activation of 110,828 rows, F = 2,048, took 238 us at
+// 201 of HBM's).
 template <class S>
 __device__ __forceinline__ float sigmoid(float g) {
-    if constexpr (sizeof(S) == 4) return __frcp_rn(1.0f + expf(-g));
-    return __fdividef(1.0f, 1.0f + __expf(-g));
+    float e, s;
+    if constexpr (sizeof(S) == 4) {
+        e = expf(-fabsf(g));
+        s = __frcp_rn(1.0f + e);
+    } else {
+        e = __expf(-fabsf(g));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + e));
+    }
+    if (g < 0.0f) s *= e;
+    return s;
 }
 
 // A thread takes one unit of columns of U rows at a time; blockDim is (columns, rows).
