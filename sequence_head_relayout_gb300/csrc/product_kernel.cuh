@@ -526,7 +526,8 @@ struct Tiles {
         else o.kblocks = parts(a.red, kBlockK);
         o.gap = 0;
         if (a.gaps && r == row_tiles - 1)
-            o.gap = max(0, min(a.offsets[o.e + 1], a.rows) - (b + c));
+            // (cut to the buffer before the difference, which could wrap else)
+            o.gap = max(0, min(max(a.offsets[o.e + 1], 0), a.rows) - (b + c));
         t += step;
         return true;
     }

@@ -196,3 +196,29 @@ def test_product_does_not_drift(rows, dtype, transposed):
         want += x[:, mine].double() @ w[0, :, mine].double().t()
     bound = drift(M, PART[dtype, dtype]) + half_units(want, dtype)
     assert ((got - want).abs() / want <= bound).all()
+
+
+@pytest.mark.parametrize("M", [64, 8256])
+def test_hostile_plans_of_many_rows(M):
+    """Segments of several parts, cut to the buffer, and ends of experts far in front of
+    them: guard bands stay."""
+    E, N, rows = 4, 72, 9000
+    i32 = dict(dtype=torch.int32, device=DEV)
+    big = 2 ** 31 - 1
+    x = odd((rows, M), F16, 1).to(DEV)
+    w = odd((E, N, M), F16, 2).to(DEV)
+    g = odd((rows, N), F16, 3).to(DEV)
+    for counts, offsets in [([big] * E, [0, 10, 4100, 8999, 9000]),
+                            ([9000, -1, 5000, 4097], [-5, big, 4500, 4903, big]),
+                            ([8192, 8192, 1, big], [0, 808, 9000, 8999, -big])]:
+        plan = vf.ExpertPlan(torch.zeros((rows, 1), **i32), torch.zeros((rows,), **i32),
+                             torch.tensor(counts, **i32), torch.tensor(offsets, **i32), 4)
+        band = torch.full((rows + 200, N), 7.0, dtype=F16, device=DEV)
+        vf.expert_product(x, w, plan, out=band[100:100 + rows])
+        assert (band[:100] == 7).all() and (band[100 + rows:] == 7).all()
+        for cols in (64, 200):
+            band = torch.full((E + 2, N, cols), 7.0, dtype=F16, device=DEV)
+            few = x.repeat(1, 4)[:, :cols].contiguous()
+            vf.expert_weight_grad(g, few, plan, out=band[1:1 + E])
+            assert (band[0] == 7).all() and (band[-1] == 7).all()
+            assert not (band[1:1 + E] == 7).all()
