@@ -1,9 +1,9 @@
 """Build ``libvf_relayout.so`` in-tree with nvcc for sm_103a (GB300).
 
 Five translation units (the exact relayouts, the lossy-transport kernels, the
-expert relayouts, the experts' products and a layer's row-wise operators) compiled in parallel, one ``-gencode``, then linked; the
-CUDA runtime is linked statically so the library needs nothing but the driver
-at load time.
+expert relayouts, the experts' products and a layer's row-wise operators)
+compiled in parallel, one ``-gencode``, then linked; the CUDA runtime is linked
+statically so the library needs nothing but the driver at load time.
 """
 import os
 import subprocess

@@ -149,8 +149,8 @@ int glu(const vf_glu_desc *d, bool backward, cudaStream_t stream) {
         w.take(d->out, d->out_strides);
     }
     // 2-byte accesses and units of columns (T = 40,000, bf16; us, activation and backward):
-    //   F = 4,095   424 258   540 401        F = 257   41 37   54 54
-    //   F = 1,421   155  98   199 159        F = 97    15 22   23 32
+    //   F = 4,095   424 265   540 408        F = 257   41 35   54 53
+    //   F = 1,421   155 101   199 160        F = 97    15 22   23 32
     const bool any = size == 2 && d->F >= 192 && w.any_columns(1, int64_t(1) << 24);
     a.F = int32_t(d->F);
     a.units = int32_t(w.units(false));
