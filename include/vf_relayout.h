@@ -589,9 +589,9 @@ int vf_expert_glu_backward(const vf_glu_desc *desc, vf_stream_t stream);
  * goes by M and by how the call's views and the weight lie in 16-byte pieces (addresses,
  * row strides): not by T, nor by other rows.  Rows that all start at multiples of 16
  * bytes, with M such a multiple, so give the same bits in any batch; where rows start
- * anywhere (M odd, odd strides), a row's place may decide on its last bits.  x, residual, total and
- * out are [T][M] views with any non-negative element strides; weight is M contiguous
- * elements of the type or float32.
+ * anywhere (M odd, odd strides), a row's place may decide on its last bits.
+ * x, residual, total and out are [T][M] views with any non-negative element strides;
+ * weight is M contiguous elements of the type or float32.
  * With a format (VF_TYPE_BF16 only), the float32 values of out are written as codes
  * [T][M] and scales [T][ceil(M / group)] instead, each group of `group` columns
  * (32, 64, 128 or 256) in the lossy transport's format: what vf_expert_restore

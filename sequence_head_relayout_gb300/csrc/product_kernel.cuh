@@ -966,7 +966,8 @@ expert_product(const __grid_constant__ ProductArgs a) {
         // the next accumulator, and its return
         const auto take = [&] {
             const uint32_t acc = it & 1, acc_phase = it >> 1 & 1;
-            ok = barrier_wait(smem_addr(&ctl.acc_full[acc]), acc_phase, failed);
+            // (a sum may have some 2^19 parts: none is waited for once a role gave up)
+            ok = !*failed && barrier_wait(smem_addr(&ctl.acc_full[acc]), acc_phase, failed);
             ok = __all_sync(kAll, int(ok));
             fence_after();
             d = tmem + acc * uint32_t(a.acc_stride) + (uint32_t(quarter * 32) << 16);
